@@ -407,6 +407,161 @@ moe_status_t moe_diag_wait_timeout(void* ws, moe_stream_t stream);
  * finite), CUDA. */
 moe_status_t moe_update_bias(int E, const int32_t* counts, float rate, float* b, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer
+ *
+ * What a block does next to its experts: the residual addition with a
+ * root-mean-square norm in front of the router, the sort of tokens by expert
+ * and the way back for experts other than this library's (the routing of
+ * moe_route_static, or of any router), and the global gradient norm with
+ * clipping. Conventions as above, and:
+ *   - they need no plan; they run on the calling thread's current device, on
+ *     which the pointers and the stream must live;
+ *   - "act" values are fp32 (MOE_FP32) or bf16 (MOE_BF16); any width H >= 1 is
+ *     accepted; row strides (ld*) count elements and are at least H;
+ *   - zero rows, tokens or tensors are accepted: nothing is read, outputs
+ *     that do not depend on rows (weight gradients, counts, the norm) are
+ *     written, and the pointers of empty tensors may be NULL;
+ *   - sums, means and norms are fp32 or wider, in a fixed order: the same
+ *     inputs give the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* 8-bit output of moe_add_rms_norm.
+ *   MOE_NORM_FP8_BLOCK: E4M3 codes (rows x H bytes) with one fp32 scale per
+ *     1x128 block (rows x H/128): amax / 448, 1 for an all-zero block; codes
+ *     of value / scale, nearest even, saturated.
+ *   MOE_NORM_MXFP8: E4M3 codes with one UE8M0 scale per 1x32 block, 2^e with
+ *     e the smallest integer such that amax <= 448 2^e, in the scale atoms of
+ *     moe_mx_quantize: ceil(rows/128) * H/128 atoms of 512 bytes; the scale
+ *     bytes of rows past the last one in the last tile are written as 0.
+ * Both quantise the fp32 norm, before any rounding to act. They need H to be
+ * a multiple of 128 and row strides that are multiples of 16 bytes. */
+enum { MOE_NORM_PLAIN = 0, MOE_NORM_FP8_BLOCK = 1, MOE_NORM_MXFP8 = 2 };
+
+typedef struct {
+    const void*  x;        /* rows x H act, row stride ldx                   */
+    const void*  residual; /* rows x H act, row stride ldr, or NULL          */
+    const float* weight;   /* H fp32                                         */
+    void*        h;        /* optional out (with a residual): x + residual;
+                              may be x or residual itself                    */
+    void*        y;        /* out, rows x H act: the norm (optional with an
+                              8-bit output); may be x or residual itself     */
+    float*       rstd;     /* optional out, rows: 1 / rms, for the backward  */
+    uint8_t*     codes;    /* 8-bit output (NULL for MOE_NORM_PLAIN)         */
+    void*        scales;
+    long long    ldx, ldr, ldh, ldy;
+} moe_norm_fwd_args_t;
+
+/* s = x + residual (fp32), rstd = (mean(s^2) + eps)^(-1/2), y = s rstd weight.
+ * h is s rounded to act; the norm is that of the unrounded sum.
+ * Errors: INVALID_ARG (null or missing pointers, rows < 0, H < 1, a stride
+ * below H, unknown dtype or quant, eps negative or not finite, an 8-bit
+ * output with H not a multiple of 128), MISALIGNED (a pointer, or a stride
+ * with an 8-bit output), CUDA. */
+moe_status_t moe_add_rms_norm(int rows, int H, int dtype, int quant, float eps,
+                              const moe_norm_fwd_args_t* args, moe_stream_t stream);
+
+typedef struct {
+    const void*  dy;       /* rows x H act: gradient of y                     */
+    const void*  h;        /* rows x H act: the normalised sum (h, or x)       */
+    const float* rstd;     /* rows: the forward's                              */
+    const float* weight;   /* H fp32                                           */
+    const void*  dh;       /* rows x H act: gradient that reaches h from the
+                              residual stream, or NULL                         */
+    void*        dx;       /* out, rows x H act: gradient of x, and of the
+                              residual; may be dy or dh itself                 */
+    float*       dweight;  /* optional out, H fp32 (overwritten)               */
+    long long    lddy, ldh, lddh, lddx;
+} moe_norm_bwd_args_t;
+
+/* With n = h rstd and c = mean(weight dy n) over the row:
+ *   dx = rstd (weight dy - n c) + dh,   dweight = sum over rows of dy n.
+ * ws (moe_norm_workspace_size bytes, scratch for dweight's partial sums) may
+ * be NULL when dweight is NULL.
+ * Errors: as the forward's, and WORKSPACE_TOO_SMALL. */
+moe_status_t moe_norm_workspace_size(int rows, int H, size_t* ws_bytes);
+moe_status_t moe_add_rms_norm_backward(int rows, int H, int dtype, const moe_norm_bwd_args_t* args,
+                                       void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Tokens sorted by expert. Slot t k + j is the j-th choice of token t; its
+ * expert is topk[t][j], and any value outside [0, E) drops the slot. Expert
+ * e's segment starts at row offsets[e] (a multiple of `align`), holds its
+ * slots in ascending order, and is padded to the next multiple of `align`.
+ * moe_sort_rows_cap gives the rows that any routing of T tokens fits in,
+ * T k + min(E, T k) (align - 1) rounded up to align; buffers of rows have
+ * at least that many.
+ * moe_sort_index writes
+ *   counts (E):      kept slots of each expert,
+ *   offsets (E + 1): first row of each segment; offsets[E] rows are in use,
+ *   row_of (T x k):  the row of each slot, -1 if dropped,
+ *   slot_of (rows):  the slot of each row, -1 for padding and unused rows.
+ * Limits: 1 <= k <= 32, 1 <= E <= 1024, 1 <= align <= 4096, rows < 2^31.
+ * Errors: INVALID_ARG, MISALIGNED, CUDA. */
+moe_status_t moe_sort_rows_cap(int T, int k, int E, int align, long long* rows);
+moe_status_t moe_sort_index(int T, int k, int E, int align, const int32_t* topk, int32_t* counts,
+                            int32_t* offsets, int32_t* row_of, int32_t* slot_of, long long rows,
+                            moe_stream_t stream);
+
+/* The index that the three calls below move rows by (moe_sort_index's, or
+ * moe_route_static's row_of and offsets). Rows outside [0, rows) in row_of
+ * are dropped slots. */
+typedef struct {
+    int T, k, H, dtype;      /* dtype MOE_FP32 or MOE_BF16                     */
+    long long rows;          /* rows of the sorted buffer                      */
+    const int32_t* row_of;   /* T x k                                          */
+    const int32_t* slot_of;  /* rows, or NULL: padding rows are not written    */
+    const int32_t* in_use;   /* one device int, the rows in use (offsets + E);
+                                needed with slot_of, 4-byte aligned            */
+} moe_sorted_t;
+
+/* Xp[row_of[t][j]] = x[t]; the padding rows (slot_of < 0) below *in_use are
+ * zeros, rows from there on are not written. The gradient of x is
+ * moe_unsort_rows of the rows' gradients without gates.
+ * Errors: INVALID_ARG, MISALIGNED, CUDA. */
+moe_status_t moe_sort_rows(const moe_sorted_t* index, const void* x, long long ldx, void* Xp,
+                           long long ldp, moe_stream_t stream);
+
+/* y[t] = residual[t] + sum_j gates[t][j] Yp[row_of[t][j]], fp32 in slot order,
+ * rounded once. gates (T x k fp32) and residual (T x H act) may be NULL
+ * (weights 1, residual 0); y may be residual itself.
+ * Errors: INVALID_ARG, MISALIGNED, CUDA. */
+moe_status_t moe_unsort_rows(const moe_sorted_t* index, const void* Yp, long long ldp,
+                             const float* gates, const void* residual, long long ldr, void* y,
+                             long long ldy, moe_stream_t stream);
+
+/* Gradient of moe_unsort_rows with respect to Yp and gates (that of the
+ * residual is dY): dYp[row_of[t][j]] = gates[t][j] dY[t], the padding rows as
+ * in moe_sort_rows; dgates[t][j] = <dY[t], Yp[row_of[t][j]]>, 0 for a dropped
+ * slot. dgates may be NULL (Yp may then be NULL too); dYp may be Yp itself.
+ * Errors: INVALID_ARG, MISALIGNED, CUDA. */
+moe_status_t moe_unsort_rows_backward(const moe_sorted_t* index, const void* dY, long long lddy,
+                                      const void* Yp, long long ldp, const float* gates, void* dYp,
+                                      long long ldd, float* dgates, moe_stream_t stream);
+
+/* One gradient tensor of moe_clip_grad_norm: n values at g, clipped into out
+ * (NULL: not written; may be g itself). Pointers need the alignment of their
+ * type only, so views into one flat buffer are fine. Tensors do not overlap. */
+typedef struct {
+    const void* g;
+    void*       out;
+    long long   n;
+    int         dtype;      /* MOE_FP32 or MOE_BF16 */
+    int         reserved;   /* 0 */
+} moe_grad_t;
+
+/* Global gradient norm over `count` tensors and clipping by it:
+ *   norm = sqrt(sum of g^2 over every value of every tensor),
+ *   out = g min(1, max_norm / norm)   (fp32 product, rounded once).
+ * max_norm > 0; infinity clips nothing. A norm that is infinite or NaN leaves
+ * the values as they are (out = g): the caller sees it in *norm and skips the
+ * step. Squares that leave fp32's range are summed in 64 bits. `list` is a
+ * host array, read during the call; *norm is a device float.
+ * Errors: INVALID_ARG (also a norm of more than 2^46 bytes), MISALIGNED,
+ * WORKSPACE_TOO_SMALL, CUDA. */
+moe_status_t moe_clip_workspace_size(int count, size_t* ws_bytes);
+moe_status_t moe_clip_grad_norm(int count, const moe_grad_t* list, float max_norm, float* norm,
+                                void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* MOE_ABI_VERSION of the loaded library. */
 int moe_abi_version(void);
 

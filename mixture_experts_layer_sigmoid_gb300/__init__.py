@@ -36,6 +36,9 @@ EXPORTS = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_size", "moe_for
            "moe_backward", "moe_read_status", "moe_status_string", "moe_stage_times",
            "moe_route_static", "moe_fp8_quantize", "moe_diag_wait_timeout", "moe_update_bias",
            "moe_weight_cache_size", "moe_quantize_weights", "moe_mx_quantize", "moe_nv_quantize",
+           "moe_add_rms_norm", "moe_norm_workspace_size", "moe_add_rms_norm_backward",
+           "moe_sort_rows_cap", "moe_sort_index", "moe_sort_rows", "moe_unsort_rows",
+           "moe_unsort_rows_backward", "moe_clip_workspace_size", "moe_clip_grad_norm",
            "moe_abi_version")
 MOE_Q_ROWS, MOE_Q_TILES, MOE_Q_COLS_T, MOE_Q_TILES_T = 0, 1, 2, 3
 
@@ -63,6 +66,26 @@ class moe_bwd_args_t(ctypes.Structure):
 
 class moe_stage_time_t(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 24), ("launches", ctypes.c_int), ("total_ms", ctypes.c_float)]
+
+
+class moe_norm_fwd_args_t(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("x", "residual", "weight", "h", "y", "rstd", "codes", "scales")] +
+                [(n, ctypes.c_longlong) for n in ("ldx", "ldr", "ldh", "ldy")])
+
+
+class moe_norm_bwd_args_t(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("dy", "h", "rstd", "weight", "dh", "dx", "dweight")] +
+                [(n, ctypes.c_longlong) for n in ("lddy", "ldh", "lddh", "lddx")])
+
+
+class moe_sorted_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("k", ctypes.c_int), ("H", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("rows", ctypes.c_longlong), ("row_of", _vp), ("slot_of", _vp), ("in_use", _vp)]
+
+
+class moe_grad_t(ctypes.Structure):
+    _fields_ = [("g", _vp), ("out", _vp), ("n", ctypes.c_longlong), ("dtype", ctypes.c_int),
+                ("reserved", ctypes.c_int)]
 
 
 class MoEError(RuntimeError):
@@ -103,6 +126,17 @@ def load_library() -> ctypes.CDLL:
         lib.moe_quantize_weights.argtypes = [_vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         lib.moe_mx_quantize.argtypes = [ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp]
         lib.moe_nv_quantize.argtypes = [ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+        i, ll = ctypes.c_int, ctypes.c_longlong
+        lib.moe_add_rms_norm.argtypes = [i, i, i, i, ctypes.c_float, P(moe_norm_fwd_args_t), _vp]
+        lib.moe_norm_workspace_size.argtypes = [i, i, P(ctypes.c_size_t)]
+        lib.moe_add_rms_norm_backward.argtypes = [i, i, i, P(moe_norm_bwd_args_t), _vp, ctypes.c_size_t, _vp]
+        lib.moe_sort_rows_cap.argtypes = [i, i, i, i, P(ll)]
+        lib.moe_sort_index.argtypes = [i, i, i, i, _vp, _vp, _vp, _vp, _vp, ll, _vp]
+        lib.moe_sort_rows.argtypes = [P(moe_sorted_t), _vp, ll, _vp, ll, _vp]
+        lib.moe_unsort_rows.argtypes = [P(moe_sorted_t), _vp, ll, _vp, _vp, ll, _vp, ll, _vp]
+        lib.moe_unsort_rows_backward.argtypes = [P(moe_sorted_t), _vp, ll, _vp, ll, _vp, _vp, ll, _vp, _vp]
+        lib.moe_clip_workspace_size.argtypes = [i, P(ctypes.c_size_t)]
+        lib.moe_clip_grad_norm.argtypes = [i, _vp, ctypes.c_float, _vp, _vp, ctypes.c_size_t, _vp]
         lib.moe_abi_version.argtypes = []
         for n in EXPORTS:
             if n not in ("moe_status_string", "moe_abi_version"):
@@ -212,6 +246,30 @@ def moe_update_bias(E: int, counts: int, rate: float, b: int, stream: int) -> No
     st = load_library().moe_update_bias(E, counts, rate, b, stream)
     if st != MOE_OK:
         raise MoEError(st, "moe_update_bias")
+
+
+def moe_norm_workspace_size(rows: int, H: int) -> int:
+    n = ctypes.c_size_t()
+    st = load_library().moe_norm_workspace_size(rows, H, ctypes.byref(n))
+    if st != MOE_OK:
+        raise MoEError(st, "moe_norm_workspace_size")
+    return n.value
+
+
+def moe_sort_rows_cap(T: int, k: int, E: int, align: int) -> int:
+    n = ctypes.c_longlong()
+    st = load_library().moe_sort_rows_cap(T, k, E, align, ctypes.byref(n))
+    if st != MOE_OK:
+        raise MoEError(st, "moe_sort_rows_cap")
+    return n.value
+
+
+def moe_clip_workspace_size(count: int) -> int:
+    n = ctypes.c_size_t()
+    st = load_library().moe_clip_workspace_size(count, ctypes.byref(n))
+    if st != MOE_OK:
+        raise MoEError(st, "moe_clip_workspace_size")
+    return n.value
 
 
 # ------------------------------------------------- torch-allocated wrapper
@@ -333,3 +391,9 @@ class MoELayer:
     def status(self, T) -> int:
         _, ws = self.buffers(T)
         return moe_read_status(self.plan, ws.data_ptr(), self.stream())
+
+
+# the operators around the layer, on torch tensors
+from .operators import (MOE_NORM_FP8_BLOCK, MOE_NORM_MXFP8, MOE_NORM_PLAIN, add_rms_norm,  # noqa: E402
+                        add_rms_norm_backward, clip_grad_norm, sort_index, sort_rows, unsort_rows,
+                        unsort_rows_backward)

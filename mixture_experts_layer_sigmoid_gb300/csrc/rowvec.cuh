@@ -1,0 +1,136 @@
+// rowvec.cuh -- loads and stores of row pieces for the operators around the
+// layer (norm.cu, sort.cu): V consecutive act values as one access of
+// V * sizeof(T) bytes, unpacked to fp32.
+//
+// The access width of a launch follows from its pointers and row strides:
+// 16 bytes when every row starts on a 16-byte boundary and H is a whole number
+// of such pieces, else 4 bytes on the same terms, else single values.
+#pragma once
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace moe {
+
+template <int BYTES> struct RawOf;
+template <> struct RawOf<16> { using type = uint4; };
+template <> struct RawOf<4> { using type = uint32_t; };
+template <> struct RawOf<2> { using type = uint16_t; };
+template <typename T, int V> using Raw = typename RawOf<V * (int)sizeof(T)>::type;
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V>& q, float (&v)[V])
+{
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (V == 4) {
+            v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
+            v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+        } else {
+            v[0] = __uint_as_float(q);
+        }
+    } else if constexpr (V == 1) {
+        v[0] = __uint_as_float((uint32_t)q << 16);
+    } else {
+        uint32_t w[V / 2];
+        if constexpr (V == 8) { w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w; }
+        else w[0] = q;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+// fp32 -> act, nearest even
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> pack(const float (&v)[V])
+{
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (V == 4)
+            return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                              __float_as_uint(v[3]));
+        else
+            return __float_as_uint(v[0]);
+    } else if constexpr (V == 1) {
+        return __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+    } else {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if constexpr (V == 8) return make_uint4(w[0], w[1], w[2], w[3]);
+        else return w[0];
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* p)
+{
+    return *reinterpret_cast<const Raw<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T, V>& q)
+{
+    *reinterpret_cast<Raw<T, V>*>(p) = q;
+}
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float (&v)[V])
+{
+    unpack<T, V>(load_raw<T, V>(p), v);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float (&v)[V])
+{
+    store_raw<T, V>(p, pack<T, V>(v));
+}
+
+// V consecutive fp32 values that start on a V-value boundary of an aligned
+// array (V = 8: two 16-byte loads; V = 2: 8 bytes)
+template <int V>
+__device__ __forceinline__ void load_f32(const float* p, float (&v)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 q = reinterpret_cast<const float4*>(p)[i];
+            v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+        }
+    } else if constexpr (V == 2) {
+        const float2 q = *reinterpret_cast<const float2*>(p);
+        v[0] = q.x; v[1] = q.y;
+    } else {
+        v[0] = p[0];
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_f32(float* p, const float (&v)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    } else {
+        p[0] = v[0];
+    }
+}
+
+// Bytes of one access for rows of H values with the given strides (in
+// elements, every base pointer 16-byte aligned): 16, 4, or one value.
+inline int access_bytes(int H, int size, const long long* strides, int n)
+{
+    for (int b = 16; b > size; b = 4) {
+        bool ok = (long long)H * size % b == 0;
+        for (int i = 0; i < n; ++i) ok = ok && strides[i] * size % b == 0;
+        if (ok) return b;
+        if (b == 4) break;
+    }
+    return size;
+}
+
+inline bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace moe

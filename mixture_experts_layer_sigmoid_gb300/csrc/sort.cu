@@ -1,0 +1,467 @@
+// sort.cu -- tokens sorted by expert and back: the index (a stable counting
+// sort of the T k slots), the rows' way out, their weighted way back, and the
+// gradient of that.
+//
+// The movers do one or two operations per value moved: bound by HBM when the
+// rows are many, by latency when they are few. They go token by token, so x,
+// dY and the residual are read once and only the sorted rows k times.
+#include "internal.h"
+#include "rowvec.cuh"
+
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+constexpr int kSortMaxK = 32;
+constexpr int kSortMaxE = 1024;
+constexpr int kSortMaxAlign = 4096;
+
+// ------------------------------------------------------------------ index
+constexpr int kIndexThreads = 1024;
+constexpr int kIndexWarps = kIndexThreads / 32;
+
+// Expert of slot i, or E for a dropped slot or one past the end.
+__device__ __forceinline__ int slot_expert(const int32_t* topk, int i, int n, int E)
+{
+    if (i >= n) return E;
+    const int e = topk[i];
+    return (unsigned)e < (unsigned)E ? e : E;
+}
+
+// One block. Warp w takes the w-th run of slots: it counts its slots of each
+// expert, the counts are summed over warps and experts, and it then goes over
+// its slots again in order, 32 at a time; lanes with the same expert find one
+// another with a match, so the rank of a slot needs no atomic and the order is
+// the slots' own. Shared memory: kIndexWarps x E counters.
+__global__ void __launch_bounds__(kIndexThreads)
+sort_index_kernel(const int32_t* __restrict__ topk, int n, int E, int align, int32_t* __restrict__ counts,
+                  int32_t* __restrict__ offsets, int32_t* __restrict__ row_of,
+                  int32_t* __restrict__ slot_of, int rows)
+{
+    extern __shared__ int hist[];            // [kIndexWarps][E]
+    __shared__ int wsum[kIndexWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (n + kIndexThreads - 1) / kIndexThreads * 32;     // slots of a warp
+    const long long lo = (long long)warp * per;
+    int* mine = hist + warp * E;
+    for (int i = tid; i < kIndexWarps * E; i += kIndexThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = 0; i < per; i += 32) {
+        const long long s = lo + i + lane;
+        const int e = s < n ? slot_expert(topk, (int)s, n, E) : E;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        if (e < E && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    // thread e: counts of expert e -> each warp's base inside the segment
+    int total = 0;
+    if (tid < E)
+        for (int w = 0; w < kIndexWarps; ++w) {
+            const int c = hist[w * E + tid];
+            hist[w * E + tid] = total;
+            total += c;
+        }
+    // exclusive scan of the padded counts over the experts
+    const int padded = (total + align - 1) / align * align;
+    int sum = padded;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += t;
+    }
+    if (lane == 31) wsum[warp] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    const int off = before + sum - padded;
+    int used = 0;
+    for (int w = 0; w < kIndexWarps; ++w) used += wsum[w];
+    if (tid < E) {
+        counts[tid] = total;
+        offsets[tid] = off;
+        for (int w = 0; w < kIndexWarps; ++w) hist[w * E + tid] += off;
+        for (int r = off + total; r < off + padded; ++r) slot_of[r] = -1;
+    }
+    if (tid == 0) offsets[E] = used;
+    for (int r = used + tid; r < rows; r += kIndexThreads) slot_of[r] = -1;
+    __syncthreads();
+    for (int i = 0; i < per; i += 32) {
+        const long long s = lo + i + lane;
+        const int e = s < n ? slot_expert(topk, (int)s, n, E) : E;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        int row = -1;
+        if (e < E) row = mine[e] + __popc(peers & ((1u << lane) - 1));
+        __syncwarp();
+        if (e < E && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+        __syncwarp();
+        if (s < n) {
+            row_of[s] = row;
+            if (row >= 0) slot_of[row] = (int)s;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ rows
+constexpr int kMoveThreads = 128;
+// Rows that one block of the padding part looks at.
+constexpr int kPadRows = 16;
+
+struct IndexArgs {
+    int T, k, H;
+    long long rows;
+    const int32_t* row_of; const int32_t* slot_of; const int32_t* in_use;
+};
+
+// Zeros in the padding rows among [r0, r0 + kPadRows).
+template <typename T, int V>
+__device__ __forceinline__ void zero_padding(const IndexArgs& ix, T* buf, long long ld, long long r0)
+{
+    const long long used = *ix.in_use < ix.rows ? *ix.in_use : ix.rows;
+    float z[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] = 0.f;
+    for (long long r = r0; r < r0 + kPadRows && r < used; ++r) {
+        if (ix.slot_of[r] >= 0) continue;
+        for (int c = threadIdx.x * V; c < ix.H; c += kMoveThreads * V) store_vec<T, V>(buf + r * ld + c, z);
+    }
+}
+
+// Rows of token t's slots j0 .. j0 + KM - 1 (-1: dropped, or past k).
+template <int KM>
+__device__ __forceinline__ void slot_rows(const IndexArgs& ix, int t, int j0, long long (&row)[KM])
+{
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+        const int r = j0 + j < ix.k ? ix.row_of[(size_t)t * ix.k + j0 + j] : -1;
+        row[j] = r < ix.rows ? r : -1;
+    }
+}
+
+// Blocks [0, T): token t's row to its k rows. Blocks from T on: padding rows.
+template <typename T, int V, int KM>
+__global__ void __launch_bounds__(kMoveThreads)
+sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __restrict__ Xp, long long ldp)
+{
+    if (blockIdx.x >= (unsigned)ix.T) {
+        zero_padding<T, V>(ix, Xp, ldp, (long long)(blockIdx.x - ix.T) * kPadRows);
+        return;
+    }
+    const int t = blockIdx.x;
+    for (int j0 = 0; j0 < ix.k; j0 += KM) {
+        long long row[KM];
+        slot_rows<KM>(ix, t, j0, row);
+        for (int c = threadIdx.x * V; c < ix.H; c += kMoveThreads * V) {
+            const Raw<T, V> q = load_raw<T, V>(x + (size_t)t * ldx + c);
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (row[j] >= 0) store_raw<T, V>(Xp + row[j] * ldp + c, q);
+        }
+    }
+}
+
+// y[t] = residual[t] + sum over the slots in order of g Yp[row].
+template <typename T, int V, int KM>
+__global__ void __launch_bounds__(kMoveThreads)
+unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const float* __restrict__ gates,
+                   const T* residual, long long ldr, T* y, long long ldy)
+{
+    const int t = blockIdx.x;
+    long long row[KM];
+    float g[KM];
+    const bool whole = ix.k <= KM;           // every slot fits: read the index once
+    if (whole) {
+        slot_rows<KM>(ix, t, 0, row);
+#pragma unroll
+        for (int j = 0; j < KM; ++j) g[j] = gates && j < ix.k ? gates[(size_t)t * ix.k + j] : 1.f;
+    }
+    for (int c = threadIdx.x * V; c < ix.H; c += kMoveThreads * V) {
+        float acc[V];
+        if (residual) {
+            load_vec<T, V>(residual + (size_t)t * ldr + c, acc);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        }
+        for (int j0 = 0; j0 < ix.k; j0 += KM) {
+            if (!whole) {
+                slot_rows<KM>(ix, t, j0, row);
+#pragma unroll
+                for (int j = 0; j < KM; ++j) g[j] = gates && j0 + j < ix.k ? gates[(size_t)t * ix.k + j0 + j] : 1.f;
+            }
+            Raw<T, V> q[KM];
+#pragma unroll
+            for (int j = 0; j < KM; ++j)
+                if (row[j] >= 0) q[j] = load_raw<T, V>(Yp + row[j] * ldp + c);
+#pragma unroll
+            for (int j = 0; j < KM; ++j) {
+                if (row[j] < 0) continue;
+                float v[V];
+                unpack<T, V>(q[j], v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(g[j], v[i], acc[i]);
+            }
+        }
+        store_vec<T, V>(y + (size_t)t * ldy + c, acc);
+    }
+}
+
+// Blocks [0, T): dYp[row_j] = g_j dY[t] and dg_j = <dY[t], Yp[row_j]>.
+// Blocks from T on: padding rows.
+template <typename T, int V, int KM, bool DG>
+__global__ void __launch_bounds__(kMoveThreads)
+unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const T* Yp, long long ldp,
+                  const float* __restrict__ gates, T* dYp, long long ldd, float* __restrict__ dgates)
+{
+    if (blockIdx.x >= (unsigned)ix.T) {
+        zero_padding<T, V>(ix, dYp, ldd, (long long)(blockIdx.x - ix.T) * kPadRows);
+        return;
+    }
+    __shared__ float red[kMoveThreads / 32][KM];
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int j0 = 0; j0 < ix.k; j0 += KM) {
+        long long row[KM];
+        float g[KM], dot[KM];
+        slot_rows<KM>(ix, t, j0, row);
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            g[j] = gates && j0 + j < ix.k ? gates[(size_t)t * ix.k + j0 + j] : 1.f;
+            dot[j] = 0.f;
+        }
+        for (int c = threadIdx.x * V; c < ix.H; c += kMoveThreads * V) {
+            float d[V];
+            load_vec<T, V>(dY + (size_t)t * lddy + c, d);
+            Raw<T, V> q[KM];
+            if constexpr (DG) {
+#pragma unroll
+                for (int j = 0; j < KM; ++j)
+                    if (row[j] >= 0) q[j] = load_raw<T, V>(Yp + row[j] * ldp + c);
+            }
+#pragma unroll
+            for (int j = 0; j < KM; ++j) {
+                if (row[j] < 0) continue;
+                float o[V];
+                if constexpr (DG) {
+                    float v[V];
+                    unpack<T, V>(q[j], v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) dot[j] = fmaf(d[i], v[i], dot[j]);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = g[j] * d[i];
+                store_vec<T, V>(dYp + row[j] * ldd + c, o);
+            }
+        }
+        if constexpr (DG) {
+            __syncthreads();                 // red of the previous slots is read
+#pragma unroll
+            for (int j = 0; j < KM; ++j) {
+                float s = dot[j];
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+                if (lane == 0) red[warp][j] = s;
+            }
+            __syncthreads();
+            if (threadIdx.x < KM && j0 + (int)threadIdx.x < ix.k) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < kMoveThreads / 32; ++w) s += red[w][threadIdx.x];
+                dgates[(size_t)t * ix.k + j0 + threadIdx.x] = s;
+            }
+        }
+    }
+}
+
+// Calls F with the slot bound of k: 1, 2, 4 or 8 rows at a time.
+template <typename F>
+void with_slots(int k, F&& f)
+{
+    if (k <= 1) f(std::integral_constant<int, 1>{});
+    else if (k <= 2) f(std::integral_constant<int, 2>{});
+    else if (k <= 4) f(std::integral_constant<int, 4>{});
+    else f(std::integral_constant<int, 8>{});
+}
+// Calls F with the values per access.
+template <typename T, typename F>
+void with_width(int bytes, F&& f)
+{
+    if (bytes == 16) f(std::integral_constant<int, 16 / (int)sizeof(T)>{});
+    else if (bytes == 4) f(std::integral_constant<int, 4 / (int)sizeof(T)>{});
+    else f(std::integral_constant<int, 1>{});
+}
+
+IndexArgs index_args(const moe_sorted_t& s)
+{
+    return IndexArgs{s.T, s.k, s.H, s.rows, s.row_of, s.slot_of, s.in_use};
+}
+unsigned move_grid(const moe_sorted_t& s)
+{
+    return (unsigned)(s.T + (s.slot_of ? (s.rows + kPadRows - 1) / kPadRows : 0));
+}
+
+template <typename T>
+void sort_rows(const moe_sorted_t& ix, const void* x, long long ldx, void* Xp, long long ldp, cudaStream_t s)
+{
+    const long long st[] = {ldx, ldp};
+    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, 2), [&](auto v) {
+        with_slots(ix.k, [&](auto km) {
+            sort_rows_kernel<T, decltype(v)::value, decltype(km)::value><<<move_grid(ix), kMoveThreads, 0, s>>>(
+                index_args(ix), static_cast<const T*>(x), ldx, static_cast<T*>(Xp), ldp);
+        });
+    });
+}
+
+template <typename T>
+void unsort_rows(const moe_sorted_t& ix, const void* Yp, long long ldp, const float* gates, const void* residual,
+                 long long ldr, void* y, long long ldy, cudaStream_t s)
+{
+    const long long st[] = {ldp, ldy, ldr};
+    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, residual ? 3 : 2), [&](auto v) {
+        with_slots(ix.k, [&](auto km) {
+            unsort_rows_kernel<T, decltype(v)::value, decltype(km)::value><<<ix.T, kMoveThreads, 0, s>>>(
+                index_args(ix), static_cast<const T*>(Yp), ldp, gates, static_cast<const T*>(residual), ldr,
+                static_cast<T*>(y), ldy);
+        });
+    });
+}
+
+template <typename T>
+void unsort_bwd(const moe_sorted_t& ix, const void* dY, long long lddy, const void* Yp, long long ldp,
+                const float* gates, void* dYp, long long ldd, float* dgates, cudaStream_t s)
+{
+    const long long st[] = {lddy, ldd, ldp};
+    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, dgates ? 3 : 2), [&](auto v) {
+        with_slots(ix.k, [&](auto km) {
+            constexpr int V = decltype(v)::value, KM = decltype(km)::value;
+            const T* d = static_cast<const T*>(dY);
+            const T* y = static_cast<const T*>(Yp);
+            T* o = static_cast<T*>(dYp);
+            if (dgates)
+                unsort_bwd_kernel<T, V, KM, true><<<move_grid(ix), kMoveThreads, 0, s>>>(
+                    index_args(ix), d, lddy, y, ldp, gates, o, ldd, dgates);
+            else
+                unsort_bwd_kernel<T, V, KM, false><<<move_grid(ix), kMoveThreads, 0, s>>>(
+                    index_args(ix), d, lddy, y, ldp, gates, o, ldd, dgates);
+        });
+    });
+}
+
+long long rows_cap(int T, int k, int E, int align)
+{
+    const long long n = (long long)T * k;
+    return (n + (n < E ? n : E) * (align - 1) + align - 1) / align * align;
+}
+
+bool sort_args_ok(int T, int k, int E, int align)
+{
+    return T >= 0 && k >= 1 && k <= kSortMaxK && E >= 1 && E <= kSortMaxE && align >= 1 &&
+           align <= kSortMaxAlign && rows_cap(T, k, E, align) < (1ll << 31) - 1;
+}
+
+// The checks that the movers share; MOE_OK if the index can be used.
+moe_status_t check_index(const moe_sorted_t* ix, bool writes_rows)
+{
+    if (!ix || ix->T < 0 || ix->k < 1 || ix->k > kSortMaxK || ix->H < 1 || ix->rows < 0 ||
+        ix->rows >= (1ll << 31) - 1 || (long long)ix->T * ix->k >= (1ll << 31) - 1 ||
+        (ix->dtype != MOE_FP32 && ix->dtype != MOE_BF16))
+        return MOE_ERR_INVALID_ARG;
+    if (ix->T > 0 && !ix->row_of) return MOE_ERR_INVALID_ARG;
+    if (writes_rows && ix->slot_of && !ix->in_use) return MOE_ERR_INVALID_ARG;
+    if (!is_aligned16(ix->row_of) || !is_aligned16(ix->slot_of) ||
+        (reinterpret_cast<uintptr_t>(ix->in_use) & 3u))
+        return MOE_ERR_MISALIGNED;
+    return MOE_OK;
+}
+
+moe_status_t launched()
+{
+    count_launches();
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+moe_status_t moe_sort_rows_cap(int T, int k, int E, int align, long long* rows)
+{
+    if (!rows || !sort_args_ok(T, k, E, align)) return MOE_ERR_INVALID_ARG;
+    *rows = rows_cap(T, k, E, align);
+    return MOE_OK;
+}
+
+moe_status_t moe_sort_index(int T, int k, int E, int align, const int32_t* topk, int32_t* counts,
+                            int32_t* offsets, int32_t* row_of, int32_t* slot_of, long long rows,
+                            moe_stream_t stream)
+{
+    if (!sort_args_ok(T, k, E, align) || rows < rows_cap(T, k, E, align) || rows >= (1ll << 31) - 1 ||
+        !counts || !offsets || (T > 0 && (!topk || !row_of)) || (rows > 0 && !slot_of))
+        return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {topk, counts, offsets, row_of, slot_of};
+    for (const void* p : ptrs)
+        if (!is_aligned16(p)) return MOE_ERR_MISALIGNED;
+    const size_t smem = (size_t)kIndexWarps * E * sizeof(int);
+    if (cudaFuncSetAttribute(sort_index_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kIndexWarps * kSortMaxE * (int)sizeof(int)) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    sort_index_kernel<<<1, kIndexThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
+        topk, T * k, E, align, counts, offsets, row_of, slot_of, (int)rows);
+    return launched();
+}
+
+moe_status_t moe_sort_rows(const moe_sorted_t* index, const void* x, long long ldx, void* Xp,
+                           long long ldp, moe_stream_t stream)
+{
+    const moe_status_t st = check_index(index, true);
+    if (st != MOE_OK) return st;
+    const moe_sorted_t& ix = *index;
+    if (ix.T > 0 && !x) return MOE_ERR_INVALID_ARG;
+    if ((ix.rows > 0 && !Xp) || ldx < ix.H || ldp < ix.H) return MOE_ERR_INVALID_ARG;
+    if (!is_aligned16(x) || !is_aligned16(Xp)) return MOE_ERR_MISALIGNED;
+    if (move_grid(ix) == 0 || ix.rows == 0) return MOE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (ix.dtype == MOE_FP32) sort_rows<float>(ix, x, ldx, Xp, ldp, s);
+    else sort_rows<__nv_bfloat16>(ix, x, ldx, Xp, ldp, s);
+    return launched();
+}
+
+moe_status_t moe_unsort_rows(const moe_sorted_t* index, const void* Yp, long long ldp,
+                             const float* gates, const void* residual, long long ldr, void* y,
+                             long long ldy, moe_stream_t stream)
+{
+    const moe_status_t st = check_index(index, false);
+    if (st != MOE_OK) return st;
+    const moe_sorted_t& ix = *index;
+    if ((ix.rows > 0 && !Yp) || (ix.T > 0 && !y) || ldp < ix.H || ldy < ix.H || (residual && ldr < ix.H))
+        return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {Yp, gates, residual, y};
+    for (const void* p : ptrs)
+        if (!is_aligned16(p)) return MOE_ERR_MISALIGNED;
+    if (ix.T == 0) return MOE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (ix.dtype == MOE_FP32) unsort_rows<float>(ix, Yp, ldp, gates, residual, ldr, y, ldy, s);
+    else unsort_rows<__nv_bfloat16>(ix, Yp, ldp, gates, residual, ldr, y, ldy, s);
+    return launched();
+}
+
+moe_status_t moe_unsort_rows_backward(const moe_sorted_t* index, const void* dY, long long lddy,
+                                      const void* Yp, long long ldp, const float* gates, void* dYp,
+                                      long long ldd, float* dgates, moe_stream_t stream)
+{
+    const moe_status_t st = check_index(index, true);
+    if (st != MOE_OK) return st;
+    const moe_sorted_t& ix = *index;
+    if ((ix.T > 0 && !dY) || (ix.rows > 0 && (!dYp || (dgates && !Yp))) || lddy < ix.H || ldd < ix.H ||
+        (dgates && ldp < ix.H))
+        return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {dY, Yp, gates, dYp, dgates};
+    for (const void* p : ptrs)
+        if (!is_aligned16(p)) return MOE_ERR_MISALIGNED;
+    if (move_grid(ix) == 0) return MOE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (ix.dtype == MOE_FP32) unsort_bwd<float>(ix, dY, lddy, Yp, ldp, gates, dYp, ldd, dgates, s);
+    else unsort_bwd<__nv_bfloat16>(ix, dY, lddy, Yp, ldp, gates, dYp, ldd, dgates, s);
+    return launched();
+}

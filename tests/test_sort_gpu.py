@@ -1,0 +1,275 @@
+"""Tokens sorted by expert and back, against plain 64-bit formulas.
+
+The index is compared exactly. Sums of k terms carry at most k + 2 fp32
+roundings of their absolute terms, a dot product of H terms chains of at most
+H/32 + 40; half a step of the stored type comes on top."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_sigmoid_gb300 as moe
+from opcheck import U32, UNIT, Banded, assert_within, strided
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+def np_index(topk, E, align):
+    T, k = topk.shape
+    flat = topk.reshape(-1).astype(np.int64)
+    rows = moe.moe_sort_rows_cap(T, k, E, align)
+    counts = np.array([(flat == e).sum() for e in range(E)], dtype=np.int64)
+    offsets = np.concatenate([[0], np.cumsum(-(-counts // align) * align)])
+    row_of, slot_of = np.full(T * k, -1), np.full(rows, -1)
+    for e in np.unique(flat[(flat >= 0) & (flat < E)]):
+        s = np.nonzero(flat == e)[0]
+        row_of[s] = offsets[e] + np.arange(len(s))
+        slot_of[offsets[e]:offsets[e] + len(s)] = s
+    return dict(counts=counts, offsets=offsets, row_of=row_of.reshape(T, k), slot_of=slot_of)
+
+
+def routing(T, k, E, seed=0, drop=0.0, skew=1.0):
+    g = np.random.default_rng(seed)
+    p = 1.0 / (1 + np.arange(E)) ** skew
+    topk = g.choice(E, size=(T, k), p=p / p.sum())           # repeated experts in a token are fine
+    topk[g.random((T, k)) < drop] = -1
+    return topk.astype(np.int32)
+
+
+CASES = [(1, 1, 1, 1), (1, 8, 256, 1), (3, 2, 5, 16), (33, 8, 256, 1), (64, 8, 64, 128), (100, 1, 7, 4), (333, 3, 11, 128),
+         (1000, 8, 128, 128), (2049, 5, 513, 3), (4096, 8, 1024, 1), (700, 32, 40, 8), (16384, 8, 128, 128),
+         (70000, 2, 3, 64), (131072, 8, 256, 128)]
+
+
+@pytest.mark.parametrize("drop", [0.0, 0.3, 1.0])
+@pytest.mark.parametrize("T,k,E,align", CASES)
+def test_index(T, k, E, align, drop):
+    topk = routing(T, k, E, seed=T + k, drop=drop)
+    if drop == 0.3:                                           # other values out of range drop a slot too
+        topk[topk < 0] = np.resize(np.array([-1, E, 2 ** 31 - 1, -2 ** 31], dtype=np.int64), (topk < 0).sum()).astype(np.int32)
+    ref = np_index(topk, E, align)
+    got = moe.sort_index(torch.from_numpy(topk).cuda(), E, align)
+    for n, v in ref.items():
+        assert np.array_equal(got[n].cpu().numpy(), v), n
+
+
+def test_index_matches_the_routing_of_the_layer():
+    """From the layer's own top-k, the tables of moe_forward's routing outputs."""
+    import moe_inputs as mi
+    w = mi.scaled(mi.WORKLOADS["qwen3_235b"], T=333, H=256, E=64, k=8, F=256)
+    g = {n: None if v is None else v.cuda() for n, v in mi.make_inputs(w, with_grad_out=False).items()}
+    layer = moe.MoELayer(w.H, w.E, w.F, w.k, w.T, score=w.score)
+    _, r = layer.forward(g["x"], g["Wr"], g["b"], g["Wg"], g["Wu"], g["Wd"], routing=True)
+    ix = moe.sort_index(r["topk_idx"], w.E, 128)
+    for n in ("counts", "offsets", "row_of"):
+        assert torch.equal(ix[n], r[n]), n
+
+
+def test_index_capacity_is_the_callers():
+    """Buffers of more rows than needed: the rest of slot_of is -1."""
+    topk = torch.from_numpy(routing(50, 2, 9, 3)).cuda()
+    ref = moe.sort_index(topk, 9, 16)
+    rows = ref["slot_of"].numel() + 777
+    b = torch.full((rows + 64,), 7, dtype=torch.int32, device="cuda")
+    c, o, r = (torch.full((n,), 7, dtype=torch.int32, device="cuda") for n in (12, 12, 104))
+    st = moe.load_library().moe_sort_index(50, 2, 9, 16, topk.data_ptr(), c.data_ptr(), o.data_ptr(), r.data_ptr(),
+                                           b.data_ptr(), rows, torch.cuda.current_stream().cuda_stream)
+    assert st == moe.MOE_OK
+    torch.cuda.synchronize()
+    n = ref["slot_of"].numel()
+    assert torch.equal(b[:n], ref["slot_of"]) and bool((b[n:rows] == -1).all()) and bool((b[rows:] == 7).all())
+    assert torch.equal(c[:9], ref["counts"]) and bool((c[9:] == 7).all())
+    assert torch.equal(o[:10], ref["offsets"]) and bool((o[10:] == 7).all())
+    assert torch.equal(r[:100], ref["row_of"].flatten()) and bool((r[100:] == 7).all())
+
+
+MOVES = [(1, 1, 1, 1, 1), (1, 8, 256, 1, 7168), (5, 2, 3, 16, 33), (33, 8, 64, 1, 4096), (50, 3, 11, 8, 1002),
+         (77, 6, 20, 128, 1001), (40, 9, 12, 4, 520), (21, 17, 30, 1, 100), (12, 32, 33, 16, 264), (300, 4, 8, 128, 2048),
+         (200, 8, 128, 16, 96), (9, 5, 6, 1, 9000)]
+
+
+def setup(T, k, E, align, H, dtype, drop):
+    topk = routing(T, k, E, seed=H + T, drop=drop)
+    ix = moe.sort_index(torch.from_numpy(topk).cuda(), E, align)
+    g = torch.Generator(device="cuda").manual_seed(H * T + k)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    rows = ix["slot_of"].numel()
+    d = dict(x=r(T, H).to(dtype), Yp=r(rows, H).to(dtype), res=r(T, H).to(dtype), dY=r(T, H).to(dtype), gates=r(T, k))
+    # rows that no slot refers to hold NaN: they must not be read into a result
+    d["Yp"][ix["slot_of"] < 0] = float("nan")
+    return ix, d
+
+
+def written(ix):
+    """Rows below offsets[E], and which of them hold a slot."""
+    used = int(ix["offsets"][-1])
+    return used, (ix["slot_of"][:used] >= 0)
+
+
+@pytest.mark.parametrize("drop", [0.0, 0.4, 1.0])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,align,H", MOVES)
+def test_rows_out_and_back(T, k, E, align, H, dtype, drop):
+    ix, d = setup(T, k, E, align, H, dtype, drop)
+    rows, u = ix["slot_of"].numel(), UNIT[dtype]
+    used, live = written(ix)
+    b = Banded(rows, H, dtype)
+    Xp = moe.sort_rows(d["x"], ix, out=b.t)
+    slot = ix["slot_of"][:used].long()
+    want = torch.where(live[:, None], d["x"][slot.clamp_min(0) // k], torch.zeros((), dtype=dtype, device="cuda"))
+    assert torch.equal(Xp[:used], want)
+    assert bool(Xp[used:].isnan().all()) and b.intact()
+
+    row_of = ix["row_of"].long()
+    keep = (row_of >= 0)[..., None]
+    v = torch.where(keep, d["Yp"][row_of.clamp_min(0)].double(), torch.zeros((), dtype=torch.float64, device="cuda"))
+    for gates, res in ((d["gates"], d["res"]), (d["gates"], None), (None, d["res"]), (None, None)):
+        w = v if gates is None else v * gates.double()[..., None]
+        z = torch.zeros((), dtype=torch.float64, device="cuda") if res is None else res.double()
+        ref = w.sum(1) + z
+        by = Banded(T, H, dtype)
+        y = moe.unsort_rows(d["Yp"], ix, gates, res, out=by.t)
+        assert_within(y, ref, ref.abs() * u + (k + 2) * U32 * (w.abs().sum(1) + z.abs()) * (1 + u) + 1e-37, "y")
+        assert by.intact()
+
+    bd = Banded(rows, H, dtype)
+    dYp, dg = moe.unsort_rows_backward(d["dY"], d["Yp"], ix, d["gates"], out=bd.t)
+    g = torch.zeros(used, dtype=torch.float64, device="cuda")
+    g[live] = d["gates"].flatten().double()[slot[live]]
+    ref = torch.where(live[:, None], g[:, None] * d["dY"].double()[slot.clamp_min(0) // k], torch.zeros_like(g)[:, None])
+    assert_within(dYp[:used], ref, ref.abs() * (u + U32 * (1 + u)) + 1e-37, "dYp")
+    assert bool(dYp[used:].isnan().all()) and bd.intact()
+    t = v * d["dY"].double()[:, None]
+    assert_within(dg, t.sum(2), (H / 32 + 40) * U32 * t.abs().sum(2) + 1e-37, "dgates")
+    assert bool((dg[row_of < 0] == 0).all())
+    # in place, and without the gates' gradient
+    inplace = d["Yp"].clone()
+    a, dg2 = moe.unsort_rows_backward(d["dY"], inplace, ix, d["gates"], out=inplace)
+    assert a is inplace and torch.equal(a[:used], dYp[:used]) and torch.equal(dg2, dg)
+    a, none = moe.unsort_rows_backward(d["dY"], d["Yp"], ix, d["gates"], want_dgates=False)
+    assert none is None and torch.equal(a[:used], dYp[:used])
+    # weights of one: a copy
+    a, dg1 = moe.unsort_rows_backward(d["dY"], d["Yp"], ix, None)
+    want = torch.where(live[:, None], d["dY"][slot.clamp_min(0) // k], torch.zeros((), dtype=dtype, device="cuda"))
+    assert torch.equal(a[:used], want) and torch.equal(dg1, dg)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,ld", [(96, 104), (96, 97), (1002, 1004), (1001, 1003), (4096, 4097)])
+def test_row_strides(H, ld, dtype):
+    T, k = 30, 3
+    ix, d = setup(T, k, 7, 4, H, dtype, 0.1)
+    rows = ix["slot_of"].numel()
+    used, _ = written(ix)
+    flat = dict(X=moe.sort_rows(d["x"], ix), y=moe.unsort_rows(d["Yp"], ix, d["gates"], d["res"]))
+    flat["dYp"], flat["dg"] = moe.unsort_rows_backward(d["dY"], d["Yp"], ix, d["gates"])
+    s = {n: strided(d[n], ld + 8 * i) for i, n in enumerate(("x", "Yp", "res", "dY"))}
+    b = [Banded(rows, H, dtype, ld), Banded(T, H, dtype, ld + 16), Banded(rows, H, dtype, ld)]
+    X = moe.sort_rows(s["x"], ix, out=b[0].t)
+    y = moe.unsort_rows(s["Yp"], ix, d["gates"], s["res"], out=b[1].t)
+    dYp, dg = moe.unsort_rows_backward(s["dY"], s["Yp"], ix, d["gates"], out=b[2].t)
+    assert torch.equal(X[:used], flat["X"][:used]) and torch.equal(y, flat["y"]) and torch.equal(dYp[:used], flat["dYp"][:used])
+    t = (s["Yp"][ix["row_of"].clamp_min(0).long()].double() * d["dY"].double()[:, None]).nan_to_num(0)
+    assert_within(dg, torch.where(ix["row_of"] >= 0, t.sum(2), torch.zeros_like(t.sum(2))),
+                  (H / 32 + 40) * U32 * t.abs().sum(2) + 1e-37, "dgates")
+    assert all(x.intact() for x in b)
+
+
+def test_y_may_be_the_residual_and_rows_past_the_buffer_are_dropped():
+    ix, d = setup(40, 4, 6, 1, 257, torch.bfloat16, 0.2)
+    ref = moe.unsort_rows(d["Yp"], ix, d["gates"], d["res"])
+    res = d["res"].clone()
+    assert torch.equal(moe.unsort_rows(d["Yp"], ix, d["gates"], res, out=res), ref)
+    # a shorter buffer: slots whose row it does not have count as dropped
+    short = 50
+    cut = dict(ix, row_of=torch.where(ix["row_of"] < short, ix["row_of"], torch.full_like(ix["row_of"], -1)))
+    assert torch.equal(moe.unsort_rows(d["Yp"][:short], ix, d["gates"], d["res"]),
+                       moe.unsort_rows(d["Yp"], cut, d["gates"], d["res"]))
+    b = Banded(short, 257, torch.bfloat16)
+    moe.sort_rows(d["x"], ix, out=b.t)
+    assert b.intact()
+
+
+def test_no_tokens():
+    ix = moe.sort_index(torch.empty((0, 4), dtype=torch.int32, device="cuda"), 7, 16)
+    assert bool((ix["counts"] == 0).all()) and bool((ix["offsets"] == 0).all()) and ix["slot_of"].numel() == 0
+    x = torch.empty((0, 64), device="cuda")
+    assert moe.sort_rows(x, ix).shape == (0, 64)
+    assert moe.unsort_rows(x, ix).shape == (0, 64)
+    dYp, dg = moe.unsort_rows_backward(x, x, ix)
+    assert dYp.shape == (0, 64) and dg.shape == (0, 4)
+
+
+def test_gradients_against_differences():
+    """d/dx, d/dgates of sum(c * unsort(f(sort(x)), gates)) with a linear f."""
+    T, k, E, H = 6, 3, 4, 10
+    ix, d = setup(T, k, E, 2, H, torch.float32, 0.2)
+    used, live = written(ix)
+    row_of = ix["row_of"].long()
+    keep = (row_of >= 0)[..., None]
+    scale = torch.linspace(0.5, 2.0, ix["slot_of"].numel(), dtype=torch.float64, device="cuda")[:, None]
+
+    def loss(x, gates):
+        per = torch.where(keep, scale[row_of.clamp_min(0)] * x[:, None], torch.zeros((), dtype=torch.float64, device="cuda"))
+        return ((per * gates[..., None]).sum(1) * d["dY"].double()).sum()
+
+    Yp = moe.sort_rows(d["x"], ix) * scale.float()
+    dYp, dg = moe.unsort_rows_backward(d["dY"], Yp, ix, d["gates"])
+    dx = moe.unsort_rows(dYp * scale.float(), ix)
+    x, g = d["x"].double(), d["gates"].double()
+    h = 1e-4          # the loss is linear in each of x and gates: only cancellation, 1e-16 / h
+    for t, c in ((0, 0), (3, 7), (5, 9)):
+        e = torch.zeros_like(x)
+        e[t, c] = h
+        assert abs((loss(x + e, g) - loss(x - e, g)) / (2 * h) - dx[t, c].double()) <= 1e-5 * (1 + dx.double().abs().max())
+    for t, j in ((0, 0), (2, 1), (5, 2)):
+        e = torch.zeros_like(g)
+        e[t, j] = h
+        assert abs((loss(x, g + e) - loss(x, g - e)) / (2 * h) - dg[t, j].double()) <= 1e-5 * (1 + dg.double().abs().max())
+
+
+def test_far_rows():
+    """A sorted buffer of more than 2^32 bytes: rows past the 32-bit offsets."""
+    T, k, E, H = 8192, 8, 16, 36000
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    ix = moe.sort_index(torch.from_numpy(routing(T, k, E, 1, 0.0, 0.0)).cuda(), E, 1)
+    x = torch.randn((T, H), device="cuda").to(torch.bfloat16)
+    Xp = moe.sort_rows(x, ix)
+    assert Xp.numel() * 2 > 1 << 32
+    for r in (0, 30000, 59653, 65535):
+        assert torch.equal(Xp[r], x[int(ix["slot_of"][r]) // k])
+    y = moe.unsort_rows(Xp, ix)
+    assert_within(y[::97], k * x[::97].double(), k * x[::97].double().abs() * (UNIT[torch.bfloat16] + (k + 2) * U32) + 1e-37)
+
+
+def test_side_stream_and_graph():
+    topk = torch.from_numpy(routing(60, 4, 9, 2, 0.1)).cuda()
+    other = torch.from_numpy(routing(60, 4, 9, 77, 0.3)).cuda()
+    x, gates = torch.randn((60, 264), device="cuda"), torch.rand((60, 4), device="cuda")
+
+    def step(tk, X):
+        ix = moe.sort_index(tk, 9, 8)
+        X = moe.sort_rows(x, ix, out=X)
+        y = moe.unsort_rows(X, ix, gates, x)
+        dYp, dg = moe.unsort_rows_backward(y, X, ix, gates)
+        return dict(ix, y=y, dg=dg, dx=moe.unsort_rows(dYp, ix))
+
+    buf = torch.zeros((moe.moe_sort_rows_cap(60, 4, 9, 8), 264), device="cuda")
+    ref = {n: v.clone() for n, v in step(topk, buf).items()}
+    ref2 = {n: v.clone() for n, v in step(other, buf).items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step(topk, buf)
+    side.synchronize()
+    assert all(torch.equal(got[n], ref[n]) for n in ref)
+    tk = topk.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(tk, buf)
+    tk.copy_(other)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[n], ref2[n]) for n in ref2)
