@@ -80,11 +80,13 @@ __device__ __forceinline__ void quantise(const float (&v)[V], bool act, int row,
         *out = e4m3x4(q[0], q[1], q[2], q[3]);
 }
 
-// The scale bytes of rows past the last one in the last 128-row tile (their
-// blocks run beside the rows' blocks).
-__device__ __forceinline__ void zero_scale_row(uint8_t* scales, int row, int H)
+// The scale bytes of a row past the last one in the last 128-row tile (those
+// rows' groups run beside the others).
+template <int GROUP>
+__device__ __forceinline__ void zero_scale_row(uint8_t* scales, long long row, int rows, int tid, int H)
 {
-    for (int kb = threadIdx.x; kb < H / 128; kb += blockDim.x)
+    if (row >= ((long long)rows + 127) / 128 * 128) return;
+    for (int kb = tid; kb < H / 128; kb += GROUP)
         *reinterpret_cast<uint32_t*>(scales + ((size_t)(row >> 7) * (H / 128) + kb) * 512 +
                                      atom_byte(row & 127, 0)) = 0u;
 }
@@ -98,7 +100,7 @@ norm_fwd_loop_kernel(FwdArgs<T> a)
     __shared__ float red[kNormThreads / 32];
     const int row = blockIdx.x;
     if (QUANT == MOE_NORM_MXFP8 && row >= a.rows) {
-        zero_scale_row(static_cast<uint8_t*>(a.scales), row, a.H);
+        zero_scale_row<kNormThreads>(static_cast<uint8_t*>(a.scales), row, a.rows, threadIdx.x, a.H);
         return;
     }
     const T* x = a.x + (size_t)row * a.ldx;
@@ -137,6 +139,71 @@ norm_fwd_loop_kernel(FwdArgs<T> a)
             if (a.y) store_vec<T, V>(a.y + (size_t)row * a.ldy + c, v);
         }
         if constexpr (QUANT != MOE_NORM_PLAIN) quantise<QUANT, V>(v, act, row, c, a.H, a.codes, a.scales);
+    }
+}
+
+// One row per group of GROUP threads (a warp, or the block), held in registers
+// between the sum and the output: each value is read once. N pieces of V values
+// per thread cover the row, so H <= GROUP * N * V.
+template <typename T, int V, int N, int GROUP, int QUANT>
+__global__ void __launch_bounds__(GROUP == 32 ? kNormThreads : GROUP)
+norm_fwd_kernel(FwdArgs<T> a)
+{
+    constexpr int NT = GROUP == 32 ? kNormThreads : GROUP;
+    __shared__ float red[NT / 32];
+    const int tid = GROUP == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const long long row = GROUP == 32 ? (long long)blockIdx.x * (NT / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= a.rows) {                     // whole groups leave together
+        if constexpr (QUANT == MOE_NORM_MXFP8)
+            zero_scale_row<GROUP>(static_cast<uint8_t*>(a.scales), row, a.rows, tid, a.H);
+        return;
+    }
+    const T* x = a.x + row * a.ldx;
+    const T* r = a.r ? a.r + row * a.ldr : nullptr;
+    Raw<T, V> qx[N], qr[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = (tid + i * GROUP) * V;
+        if (c < a.H) {
+            qx[i] = load_raw<T, V>(x + c);
+            if (r) qr[i] = load_raw<T, V>(r + c);
+        }
+    }
+    float v[N][V];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool act = (tid + i * GROUP) * V < a.H;
+        if (act) {
+            unpack<T, V>(qx[i], v[i]);
+            if (r) {
+                float u[V];
+                unpack<T, V>(qr[i], u);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[i][j] += u[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[i][j] = act ? v[i][j] : 0.f;
+            ss = fmaf(v[i][j], v[i][j], ss);
+        }
+    }
+    const float rstd = rsqrtf(block_sum<GROUP>(ss, red) / (float)a.H + a.eps);
+    if (tid == 0 && a.rstd) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = (tid + i * GROUP) * V;
+        const bool act = c < a.H;
+        if (act) {
+            float w[V];
+            if (a.h) store_vec<T, V>(a.h + row * a.ldh + c, v[i]);
+            load_f32<V>(a.w + c, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * rstd * w[j];
+            if (a.y) store_vec<T, V>(a.y + row * a.ldy + c, v[i]);
+        }
+        if constexpr (QUANT != MOE_NORM_PLAIN) quantise<QUANT, V>(v[i], act, (int)row, c, a.H, a.codes, a.scales);
     }
 }
 
@@ -203,6 +270,161 @@ norm_bwd_loop_kernel(BwdArgs<T> a)
     }
 }
 
+// The same with rows streamed through shared memory: each thread copies its own
+// pieces of dy, h and dh of the next rows into a ring of S stages (cp.async) and
+// later reads back nothing but what it copied, so the ring needs no barrier and
+// S rows per group are in flight while one is worked on. w and the partial sums
+// of dw stay in registers over all rows of the thread.
+// GROUP threads take a row (a warp, or the block); H <= GROUP * N * V.
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+template <typename T, int V, int N, int GROUP, int NT>
+struct Ring {
+    static constexpr int kPiece = V * (int)sizeof(T);
+    static constexpr int kTensor = NT * N * kPiece;          // one tensor's rows of one stage
+    static constexpr int kStage = 3 * kTensor;
+    // as many stages as fit beside a second block on the SM, at most 4
+    static constexpr int kStages = kStage * 4 <= 104 * 1024 ? 4 : (kStage * 3 <= 104 * 1024 ? 3 : 2);
+    static constexpr int kBytes = kStages * kStage;
+};
+
+template <typename T, int V, int N, int GROUP, int NT>
+__global__ void __launch_bounds__(NT, NT <= 256 ? 2 : 1)
+norm_bwd_kernel(BwdArgs<T> a)
+{
+    using R = Ring<T, V, N, GROUP, NT>;
+    constexpr int S = R::kStages;
+    constexpr int GROUPS = NT / GROUP;
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ float red[2][NT / 32];
+    __shared__ float rs[S][NT / 32];
+    const int tid = GROUP == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long first = GROUP == 32 ? (long long)blockIdx.x * GROUPS + warp : blockIdx.x;
+    const long long step = (long long)gridDim.x * GROUPS;
+
+    auto slot = [&](int stage, int tensor, int i) {
+        return reinterpret_cast<Raw<T, V>*>(ring + stage * R::kStage + tensor * R::kTensor) + i * NT + threadIdx.x;
+    };
+    auto fetch = [&](int stage, long long row) {
+        if (row < a.rows) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = (tid + i * GROUP) * V;
+                if (c < a.H) {
+                    copy_async<R::kPiece>(slot(stage, 0, i), a.dy + row * a.lddy + c);
+                    copy_async<R::kPiece>(slot(stage, 1, i), a.h + row * a.ldh + c);
+                    if (a.dh) copy_async<R::kPiece>(slot(stage, 2, i), a.dh + row * a.lddh + c);
+                }
+            }
+            if (lane == 0) copy_async<4>(&rs[stage][warp], a.rstd + row);
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch(s, first + s * step);
+
+    float w[N][V], dw[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = (tid + i * GROUP) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) { w[i][j] = 0.f; dw[i][j] = 0.f; }
+        if (c < a.H) load_f32<V>(a.w + c, w[i]);
+    }
+    int stage = 0, parity = 0;
+    for (long long row = first; row < a.rows; row += step) {
+        copy_wait<S - 1>();
+        __syncwarp();
+        const float rstd = rs[stage][warp];
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if ((tid + i * GROUP) * V >= a.H) break;
+            float g[V], v[V];
+            unpack<T, V>(*slot(stage, 0, i), g);
+            unpack<T, V>(*slot(stage, 1, i), v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) d = fmaf(g[j] * w[i][j], v[j], d);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+        if constexpr (GROUP != 32) {
+            // one barrier a row: the sums alternate between two arrays
+            if (lane == 0) red[parity][warp] = d;
+            __syncthreads();
+            d = 0.f;
+#pragma unroll
+            for (int k = 0; k < NT / 32; ++k) d += red[parity][k];
+            parity ^= 1;
+        }
+        const float m = d * rstd / (float)a.H;
+        T* dx = a.dx + row * a.lddx;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (tid + i * GROUP) * V;
+            if (c >= a.H) break;
+            float g[V], v[V], o[V];
+            unpack<T, V>(*slot(stage, 0, i), g);
+            unpack<T, V>(*slot(stage, 1, i), v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float n = v[j] * rstd;
+                o[j] = rstd * fmaf(-n, m, g[j] * w[i][j]);
+                dw[i][j] = fmaf(g[j], n, dw[i][j]);
+            }
+            if (a.dh) {
+                float u[V];
+                unpack<T, V>(*slot(stage, 2, i), u);
+#pragma unroll
+                for (int j = 0; j < V; ++j) o[j] += u[j];
+            }
+            store_vec<T, V>(dx + c, o);
+        }
+        __syncwarp();                         // rs is read
+        fetch(stage, row + S * step);
+        stage = stage + 1 == S ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+    if (!a.part) return;
+    float* part = a.part + (size_t)blockIdx.x * a.H;
+    if constexpr (GROUP == 32) {
+        // the warps' sums, added in warp order
+        float* sum = reinterpret_cast<float*>(ring);         // GROUP * N * V floats
+        for (int k = 0; k < GROUPS; ++k) {
+            __syncthreads();
+            if (warp == k) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        float* p = sum + (tid + i * GROUP) * V + j;
+                        *p = k == 0 ? dw[i][j] : *p + dw[i][j];
+                    }
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.H; c += NT) part[c] = sum[c];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (tid + i * GROUP) * V;
+            if (c < a.H) store_f32<V>(part + c, dw[i]);
+        }
+    }
+}
+
 // dw[c] = sum of the parts in ascending order within each of 8 phases, the
 // phases then added in order.
 __global__ void __launch_bounds__(256)
@@ -226,15 +448,29 @@ norm_dweight_kernel(const float* __restrict__ part, int nparts, int H, float* __
 
 int norm_parts(int rows) { return rows < kNormParts ? rows : kNormParts; }
 
+template <typename T, int V, int QUANT>
+void launch_fwd_width(const FwdArgs<T>& a, cudaStream_t s)
+{
+    constexpr int P = 32 / V;                // pieces of 32 values
+    const int rows = QUANT == MOE_NORM_MXFP8 ? (a.rows + 127) / 128 * 128 : a.rows;
+    const int warps = (rows + kNormThreads / 32 - 1) / (kNormThreads / 32);
+    if (a.H <= 256) norm_fwd_kernel<T, V, P / 4, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
+    else if (a.H <= 1024) norm_fwd_kernel<T, V, P, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
+    else if (a.H <= 2048) norm_fwd_kernel<T, V, P / 4, 256, QUANT><<<rows, 256, 0, s>>>(a);
+    else if (a.H <= 4096) norm_fwd_kernel<T, V, P / 2, 256, QUANT><<<rows, 256, 0, s>>>(a);
+    else if (a.H <= 8192) norm_fwd_kernel<T, V, P, 256, QUANT><<<rows, 256, 0, s>>>(a);
+    else if (a.H <= 16384) norm_fwd_kernel<T, V, P, 512, QUANT><<<rows, 512, 0, s>>>(a);
+    else norm_fwd_loop_kernel<T, V, QUANT><<<rows, kNormThreads, 0, s>>>(a);
+}
+
 template <typename T, int QUANT>
 cudaError_t launch_fwd(const FwdArgs<T>& a, int bytes, cudaStream_t s)
 {
     constexpr int V16 = 16 / (int)sizeof(T);
-    const int grid = QUANT == MOE_NORM_MXFP8 ? (a.rows + 127) / 128 * 128 : a.rows;
-    if (bytes == 16) norm_fwd_loop_kernel<T, V16, QUANT><<<grid, kNormThreads, 0, s>>>(a);
+    if (bytes == 16) launch_fwd_width<T, V16, QUANT>(a, s);
     if constexpr (QUANT == MOE_NORM_PLAIN) {
-        if (bytes == 4) norm_fwd_loop_kernel<T, 4 / (int)sizeof(T), QUANT><<<grid, kNormThreads, 0, s>>>(a);
-        else if (bytes == 2) norm_fwd_loop_kernel<T, 1, QUANT><<<grid, kNormThreads, 0, s>>>(a);
+        if (bytes == 4) launch_fwd_width<T, 4 / (int)sizeof(T), QUANT>(a, s);
+        else if (bytes == 2) launch_fwd_width<T, 1, QUANT>(a, s);
     }
     count_launches();
     return cudaGetLastError();
@@ -262,6 +498,31 @@ moe_status_t fwd(int rows, int H, int quant, float eps, const moe_norm_fwd_args_
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+template <typename T, int V, int N, int GROUP, int NT>
+void launch_ring(const BwdArgs<T>& a, int parts, cudaStream_t s)
+{
+    constexpr int bytes = Ring<T, V, N, GROUP, NT>::kBytes;
+    if (bytes > 40 * 1024)
+        cudaFuncSetAttribute(norm_bwd_kernel<T, V, N, GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    norm_bwd_kernel<T, V, N, GROUP, NT><<<parts, NT, bytes, s>>>(a);
+}
+
+template <typename T, int V>
+void launch_bwd_width(const BwdArgs<T>& a, int parts, cudaStream_t s)
+{
+    if constexpr (V * sizeof(T) >= 4) {
+        constexpr int P = 32 / V;            // pieces of 32 values
+        if (a.H <= 256) return launch_ring<T, V, P / 4, 32, 256>(a, parts, s);
+        if (a.H <= 1024) return launch_ring<T, V, P, 32, 256>(a, parts, s);
+        if (a.H <= 2048) return launch_ring<T, V, P / 4, 256, 256>(a, parts, s);
+        if (a.H <= 4096) return launch_ring<T, V, P / 2, 256, 256>(a, parts, s);
+        if (a.H <= 8192 && sizeof(T) == 2) return launch_ring<T, V, P, 256, 256>(a, parts, s);
+        if (a.H <= 8192 || (a.H <= 16384 && sizeof(T) == 2))
+            return launch_ring<T, V, sizeof(T) == 2 ? P : P / 2, 512, 512>(a, parts, s);
+    }
+    norm_bwd_loop_kernel<T, V><<<parts, kNormThreads, 0, s>>>(a);
+}
+
 template <typename T>
 moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cudaStream_t s)
 {
@@ -275,11 +536,13 @@ moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cud
     if (g.dh) st[n++] = g.lddh;
     st[n++] = g.lddx;
     const int bytes = access_bytes(H, (int)sizeof(T), st, n);
-    const int parts = norm_parts(rows);
+    // a block of the warp-a-row kernel takes eight rows at a time
+    const bool warps = H <= 1024 && bytes >= 4;
+    const int parts = norm_parts(warps ? (rows + 7) / 8 : rows);
     if (rows > 0) {
-        if (bytes == 16) norm_bwd_loop_kernel<T, 16 / (int)sizeof(T)><<<parts, kNormThreads, 0, s>>>(a);
-        else if (bytes == 4) norm_bwd_loop_kernel<T, 4 / (int)sizeof(T)><<<parts, kNormThreads, 0, s>>>(a);
-        else norm_bwd_loop_kernel<T, 1><<<parts, kNormThreads, 0, s>>>(a);
+        if (bytes == 16) launch_bwd_width<T, 16 / (int)sizeof(T)>(a, parts, s);
+        else if (bytes == 4) launch_bwd_width<T, 4 / (int)sizeof(T)>(a, parts, s);
+        else launch_bwd_width<T, 1>(a, parts, s);
         count_launches();
     }
     if (g.dweight) {
