@@ -9,6 +9,7 @@
 // here is bound by HBM (large inputs) or by latency (a few rows).
 #include "internal.h"
 #include "mx.cuh"
+#include "ptx.cuh"
 #include "rowvec.cuh"
 
 namespace moe {
@@ -343,6 +344,7 @@ norm_bwd_kernel(BwdArgs<T> a)
         for (int j = 0; j < V; ++j) { w[i][j] = 0.f; dw[i][j] = 0.f; }
         if (c < a.H) load_f32<V>(a.w + c, w[i]);
     }
+    ptx::griddep_launch_dependents();
     int stage = 0, parity = 0;
     for (long long row = first; row < a.rows; row += step) {
         copy_wait<S - 1>();
@@ -425,23 +427,25 @@ norm_bwd_kernel(BwdArgs<T> a)
     }
 }
 
-// dw[c] = sum of the parts in ascending order within each of 8 phases, the
-// phases then added in order.
-__global__ void __launch_bounds__(256)
+// dw[c] = sum of the parts: ascending order within each of 32 phases, the
+// phases then added in order. Launched ahead of the parts' kernel's end.
+constexpr int kPhases = 32;
+__global__ void __launch_bounds__(32 * kPhases)
 norm_dweight_kernel(const float* __restrict__ part, int nparts, int H, float* __restrict__ dw)
 {
-    __shared__ float red[8][33];
+    __shared__ float red[kPhases][33];
     const int lane = threadIdx.x & 31, ph = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.f;
+    ptx::griddep_wait();
     if (c < H)
-        for (int b = ph; b < nparts; b += 8) s += part[(size_t)b * H + c];
+        for (int b = ph; b < nparts; b += kPhases) s += part[(size_t)b * H + c];
     red[ph][lane] = s;
     __syncthreads();
     if (ph == 0 && c < H) {
         float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += red[i][lane];
+        for (int i = 0; i < kPhases; ++i) t += red[i][lane];
         dw[c] = t;
     }
 }
@@ -546,7 +550,9 @@ moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cud
         count_launches();
     }
     if (g.dweight) {
-        norm_dweight_kernel<<<(H + 31) / 32, 256, 0, s>>>(part, parts, H, g.dweight);
+        if (launch_early(norm_dweight_kernel, dim3((H + 31) / 32), dim3(32 * kPhases), s, (const float*)part, parts, H,
+                         g.dweight) != cudaSuccess)
+            return MOE_ERR_CUDA;
         count_launches();
     }
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

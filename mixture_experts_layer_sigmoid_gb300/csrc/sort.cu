@@ -6,6 +6,7 @@
 // rows are many, by latency when they are few. They go token by token, so x,
 // dY and the residual are read once and only the sorted rows k times.
 #include "internal.h"
+#include "ptx.cuh"
 #include "rowvec.cuh"
 
 #include <type_traits>
@@ -29,40 +30,62 @@ __device__ __forceinline__ int slot_expert(const int32_t* topk, int i, int n, in
     return (unsigned)e < (unsigned)E ? e : E;
 }
 
-// One block. Warp w takes the w-th run of slots: it counts its slots of each
-// expert, the counts are summed over warps and experts, and it then goes over
-// its slots again in order, 32 at a time; lanes with the same expert find one
-// another with a match, so the rank of a slot needs no atomic and the order is
-// the slots' own. Shared memory: kIndexWarps x E counters.
+// The blocks of one cluster. Each warp takes a run of consecutive slots: it
+// counts its slots of each expert, the counts are summed over warps, blocks
+// (through distributed shared memory) and experts, and it then goes over its
+// slots again in order, 32 at a time; lanes with the same expert find one
+// another with a match, so a slot's rank needs no atomic and the order is the
+// slots' own. Shared memory: `warps` x E counters and the block's E totals.
 __global__ void __launch_bounds__(kIndexThreads)
-sort_index_kernel(const int32_t* __restrict__ topk, int n, int E, int align, int32_t* __restrict__ counts,
-                  int32_t* __restrict__ offsets, int32_t* __restrict__ row_of,
+sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, int E, int align,
+                  int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ row_of,
                   int32_t* __restrict__ slot_of, int rows)
 {
-    extern __shared__ int hist[];            // [kIndexWarps][E]
+    extern __shared__ int hist[];            // [warps][E], then [E]
     __shared__ int wsum[kIndexWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (n + kIndexThreads - 1) / kIndexThreads * 32;     // slots of a warp
-    const long long lo = (long long)warp * per;
+    const int rank = (int)ptx::cluster_ctarank(), blocks = gridDim.x;
+    const long long lo = ((long long)rank * warps + warp) * per;      // slots [lo, lo + per) of this warp
+    const long long left = n - lo;
+    const int mine_n = warp < warps && left > 0 ? (left < per ? (int)left : per) : 0;
     int* mine = hist + warp * E;
-    for (int i = tid; i < kIndexWarps * E; i += kIndexThreads) hist[i] = 0;
+    int* tot = hist + warps * E;
+    for (int i = tid; i < warps * E; i += kIndexThreads) hist[i] = 0;
     __syncthreads();
-    for (int i = 0; i < per; i += 32) {
-        const long long s = lo + i + lane;
-        const int e = s < n ? slot_expert(topk, (int)s, n, E) : E;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        if (e < E && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
+    constexpr int U = 4;                     // groups of 32 slots loaded together
+    for (int i = 0; i < mine_n; i += 32 * U) {
+        int ex[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) ex[u] = slot_expert(topk + lo, i + 32 * u + lane, mine_n, E);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned peers = __match_any_sync(0xffffffffu, ex[u]);
+            if (ex[u] < E && lane == __ffs(peers) - 1) mine[ex[u]] += __popc(peers);
+            __syncwarp();
+        }
     }
     __syncthreads();
-    // thread e: counts of expert e -> each warp's base inside the segment
-    int total = 0;
-    if (tid < E)
-        for (int w = 0; w < kIndexWarps; ++w) {
+    // thread e: counts of expert e -> each warp's base among the block's slots
+    if (tid < E) {
+        int total = 0;
+        for (int w = 0; w < warps; ++w) {
             const int c = hist[w * E + tid];
             hist[w * E + tid] = total;
             total += c;
         }
+        tot[tid] = total;
+    }
+    ptx::cluster_sync();
+    int total = 0, below = 0;
+    if (tid < E) {
+        const uint32_t at = ptx::smem_u32(tot + tid);
+        for (int r = 0; r < blocks; ++r) {
+            int c;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(ptx::mapa_shared(at, r)) : "memory");
+            total += c;
+            below += r < rank ? c : 0;
+        }
+    }
     // exclusive scan of the padded counts over the experts
     const int padded = (total + align - 1) / align * align;
     int sum = padded;
@@ -73,34 +96,78 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int E, int align, int
     }
     if (lane == 31) wsum[warp] = sum;
     __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    const int off = before + sum - padded;
-    int used = 0;
-    for (int w = 0; w < kIndexWarps; ++w) used += wsum[w];
-    if (tid < E) {
-        counts[tid] = total;
-        offsets[tid] = off;
-        for (int w = 0; w < kIndexWarps; ++w) hist[w * E + tid] += off;
-        for (int r = off + total; r < off + padded; ++r) slot_of[r] = -1;
+    int before = 0, used = 0;
+#pragma unroll
+    for (int w = 0; w < kIndexWarps; ++w) {
+        before += w < warp ? wsum[w] : 0;
+        used += wsum[w];
     }
-    if (tid == 0) offsets[E] = used;
-    for (int r = used + tid; r < rows; r += kIndexThreads) slot_of[r] = -1;
+    const int off = before + sum - padded;
+    if (tid < E) {
+        for (int w = 0; w < warps; ++w) hist[w * E + tid] += off + below;
+        if (rank == 0) {
+            counts[tid] = total;
+            offsets[tid] = off;
+        }
+        if (tid % blocks == rank)
+            for (int r = off + total; r < off + padded; ++r) slot_of[r] = -1;
+    }
+    if (rank == 0 && tid == 0) offsets[E] = used;
+    for (long long r = used + (long long)rank * kIndexThreads + tid; r < rows; r += blocks * kIndexThreads) slot_of[r] = -1;
     __syncthreads();
-    for (int i = 0; i < per; i += 32) {
-        const long long s = lo + i + lane;
-        const int e = s < n ? slot_expert(topk, (int)s, n, E) : E;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        int row = -1;
-        if (e < E) row = mine[e] + __popc(peers & ((1u << lane) - 1));
-        __syncwarp();
-        if (e < E && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
-        if (s < n) {
-            row_of[s] = row;
-            if (row >= 0) slot_of[row] = (int)s;
+    for (int i = 0; i < mine_n; i += 32 * U) {
+        int ex[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) ex[u] = slot_expert(topk + lo, i + 32 * u + lane, mine_n, E);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned peers = __match_any_sync(0xffffffffu, ex[u]);
+            int row = -1;
+            if (ex[u] < E) row = mine[ex[u]] + __popc(peers & ((1u << lane) - 1));
+            __syncwarp();
+            if (ex[u] < E && lane == __ffs(peers) - 1) mine[ex[u]] += __popc(peers);
+            __syncwarp();
+            const int s = i + 32 * u + lane;
+            if (s < mine_n) {
+                row_of[lo + s] = row;
+                if (row >= 0) slot_of[row] = (int)(lo + s);
+            }
         }
     }
+    ptx::cluster_sync();                     // no block leaves while another may read its totals
+}
+
+// Blocks of the cluster: one up to 4096 slots, where a cluster's barriers cost
+// more than they save, else eight.
+constexpr int kIndexOneBlock = 4096;
+constexpr int kIndexCluster = 8;
+
+cudaError_t launch_index(int n, int E, int align, const int32_t* topk, int32_t* counts, int32_t* offsets,
+                         int32_t* row_of, int32_t* slot_of, int rows, cudaStream_t s)
+{
+    const int blocks = n <= kIndexOneBlock ? 1 : kIndexCluster;
+    const int groups = (n + 31) / 32;
+    int warps = (groups + blocks - 1) / blocks;
+    warps = warps < 1 ? 1 : (warps > kIndexWarps ? kIndexWarps : warps);
+    const int per = (groups + blocks * warps - 1) / (blocks * warps) * 32;
+    const size_t smem = (size_t)(warps + 1) * E * sizeof(int);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(sort_index_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (kIndexWarps + 1) * kSortMaxE * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = blocks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kIndexThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sort_index_kernel, topk, n, per, warps, E, align, counts, offsets, row_of, slot_of, rows);
 }
 
 // ------------------------------------------------------------------ rows
@@ -402,12 +469,9 @@ moe_status_t moe_sort_index(int T, int k, int E, int align, const int32_t* topk,
     const void* ptrs[] = {topk, counts, offsets, row_of, slot_of};
     for (const void* p : ptrs)
         if (!is_aligned16(p)) return MOE_ERR_MISALIGNED;
-    const size_t smem = (size_t)kIndexWarps * E * sizeof(int);
-    if (cudaFuncSetAttribute(sort_index_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kIndexWarps * kSortMaxE * (int)sizeof(int)) != cudaSuccess)
+    if (launch_index(T * k, E, align, topk, counts, offsets, row_of, slot_of, (int)rows,
+                     reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return MOE_ERR_CUDA;
-    sort_index_kernel<<<1, kIndexThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
-        topk, T * k, E, align, counts, offsets, row_of, slot_of, (int)rows);
     return launched();
 }
 
