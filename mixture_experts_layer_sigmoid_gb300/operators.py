@@ -36,34 +36,36 @@ def _load():
 
 
 def _call(where, dev, fn, *args):
-    """fn(*args, the current stream of dev) with dev current; raises on a status."""
+    """fn(*args, the current stream of device dev) with dev current; raises on a status."""
     cuda = _torch.cuda
-    stream = cuda.current_stream(dev).cuda_stream
-    if cuda.current_device() == dev.index:
-        st = fn(*args, stream)
+    if cuda.current_device() == dev:
+        st = fn(*args, cuda.current_stream().cuda_stream)
     else:
         with cuda.device(dev):
-            st = fn(*args, stream)
+            st = fn(*args, cuda.current_stream().cuda_stream)
     if st != MOE_OK:
         raise MoEError(st, where)
 
 
 def _act(t, name, shape=None, like=None):
     """Checks an activation matrix; returns its row stride."""
-    if not t.is_cuda or t.dim() != 2 or t.dtype not in _dtypes:
-        raise ValueError(f"{name}: a 2-D fp32 or bf16 CUDA tensor is needed, got {t.dim()}-D {t.dtype} on {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    sh = t.shape
+    if like is None:
+        if not t.is_cuda or len(sh) != 2 or t.dtype not in _dtypes:
+            raise ValueError(f"{name}: a 2-D fp32 or bf16 CUDA tensor is needed, got {len(sh)}-D {t.dtype} on {t.device}")
+    elif t.dtype != like.dtype or t.get_device() != like.get_device():
         raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    rows, H = t.shape
-    if H > 1 and t.stride(1) != 1:
+    if shape is not None and sh != shape:
+        raise ValueError(f"{name}: shape {tuple(sh)}, expected {tuple(shape)}")
+    ld, one = t.stride()
+    rows, H = sh
+    if one != 1 and H > 1:
         raise ValueError(f"{name}: the last dimension has to be contiguous")
-    return t.stride(0) if rows > 1 else H
+    return ld if rows > 1 else H
 
 
 def _vec(t, name, n, dtype, like):
-    if t.dtype != dtype or t.device != like.device or t.numel() != n or not t.is_contiguous():
+    if t.dtype != dtype or t.numel() != n or t.get_device() != like.get_device() or not t.is_contiguous():
         raise ValueError(f"{name}: {n} contiguous {dtype} values on {like.device} are needed")
     return t.data_ptr()
 
@@ -85,24 +87,24 @@ def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quant: int = MO
     lib = _load()
     t = _torch
     ldx = _act(x, "x")
-    rows, H = x.shape
+    shape = rows, H = x.shape
     a = moe_norm_fwd_args_t(x.data_ptr(), None, _vec(weight, "weight", H, t.float32, x))
     a.ldx = ldx
     out = {}
     if residual is not None:
-        a.ldr = _act(residual, "residual", (rows, H), x)
+        a.ldr = _act(residual, "residual", shape, x)
         a.residual = residual.data_ptr()
         if h is None:
-            h = t.empty((rows, H), dtype=x.dtype, device=x.device)
-        a.ldh = _act(h, "h", (rows, H), x)
+            h = t.empty_like(x) if ldx == H else t.empty(shape, dtype=x.dtype, device=x.device)
+        a.ldh = _act(h, "h", shape, x)
         a.h = h.data_ptr()
         out["h"] = h
     elif h is not None:
         raise ValueError("h: without a residual there is no sum to store")
     if want_y or y is not None or quant == MOE_NORM_PLAIN:
         if y is None:
-            y = t.empty((rows, H), dtype=x.dtype, device=x.device)
-        a.ldy = _act(y, "y", (rows, H), x)
+            y = t.empty_like(x) if ldx == H else t.empty(shape, dtype=x.dtype, device=x.device)
+        a.ldy = _act(y, "y", shape, x)
         a.y = y.data_ptr()
         out["y"] = y
     if want_rstd:
@@ -116,7 +118,7 @@ def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quant: int = MO
             out["scales"] = t.empty((rows + 127) // 128 * (H // 128) * 512, dtype=t.uint8, device=x.device)
         a.codes = out["codes"].data_ptr()
         a.scales = out["scales"].data_ptr()
-    _call("moe_add_rms_norm", x.device, lib.moe_add_rms_norm, rows, H, _dtypes[x.dtype], quant, eps, ctypes.byref(a))
+    _call("moe_add_rms_norm", x.get_device(), lib.moe_add_rms_norm, rows, H, _dtypes[x.dtype], quant, eps, ctypes.byref(a))
     return out
 
 
@@ -129,16 +131,16 @@ def add_rms_norm_backward(dy, h, rstd, weight, dh=None, *, dx=None, want_dweight
     lib = _load()
     t = _torch
     lddy = _act(dy, "dy")
-    rows, H = dy.shape
+    shape = rows, H = dy.shape
     a = moe_norm_bwd_args_t(dy.data_ptr(), h.data_ptr(), _vec(rstd, "rstd", rows, t.float32, dy),
                             _vec(weight, "weight", H, t.float32, dy))
-    a.lddy, a.ldh = lddy, _act(h, "h", (rows, H), dy)
+    a.lddy, a.ldh = lddy, _act(h, "h", shape, dy)
     if dh is not None:
-        a.lddh = _act(dh, "dh", (rows, H), dy)
+        a.lddh = _act(dh, "dh", shape, dy)
         a.dh = dh.data_ptr()
     if dx is None:
-        dx = t.empty((rows, H), dtype=dy.dtype, device=dy.device)
-    a.lddx = _act(dx, "dx", (rows, H), dy)
+        dx = t.empty_like(dy) if lddy == H else t.empty(shape, dtype=dy.dtype, device=dy.device)
+    a.lddx = _act(dx, "dx", shape, dy)
     a.dx = dx.data_ptr()
     dweight = None
     if want_dweight:
@@ -146,7 +148,7 @@ def add_rms_norm_backward(dy, h, rstd, weight, dh=None, *, dx=None, want_dweight
         a.dweight = dweight.data_ptr()
         if ws is None:
             ws = t.empty(moe_norm_workspace_size(rows, H), dtype=t.uint8, device=dy.device)
-    _call("moe_add_rms_norm_backward", dy.device, lib.moe_add_rms_norm_backward, rows, H, _dtypes[dy.dtype],
+    _call("moe_add_rms_norm_backward", dy.get_device(), lib.moe_add_rms_norm_backward, rows, H, _dtypes[dy.dtype],
           ctypes.byref(a), _p(ws), 0 if ws is None else ws.numel() * ws.element_size())
     return dx, dweight
 
@@ -170,7 +172,7 @@ def sort_index(topk, E: int, align: int = 1) -> Dict[str, object]:
     ix = {"counts": buf[:E], "offsets": buf[at[1]:at[1] + E + 1], "row_of": buf[at[2]:at[2] + T * k].view(T, k),
           "slot_of": buf[at[3]:]}
     p = buf.data_ptr()
-    _call("moe_sort_index", topk.device, lib.moe_sort_index, T, k, E, align, topk.data_ptr(), p, p + 4 * at[1],
+    _call("moe_sort_index", topk.get_device(), lib.moe_sort_index, T, k, E, align, topk.data_ptr(), p, p + 4 * at[1],
           p + 4 * at[2], p + 4 * at[3], rows)
     return ix
 
@@ -203,7 +205,7 @@ def sort_rows(x, index, out=None):
     s = _sorted(index, H, x.dtype, x, out.shape[0])
     if s.T != T:
         raise ValueError(f"x: {T} rows, the index has {s.T} tokens")
-    _call("moe_sort_rows", x.device, lib.moe_sort_rows, ctypes.byref(s), x.data_ptr(), ldx, out.data_ptr(), ldp)
+    _call("moe_sort_rows", x.get_device(), lib.moe_sort_rows, ctypes.byref(s), x.data_ptr(), ldx, out.data_ptr(), ldp)
     return out
 
 
@@ -221,7 +223,7 @@ def unsort_rows(rows, index, gates=None, residual=None, out=None):
     if out is None:
         out = t.empty((s.T, H), dtype=rows.dtype, device=rows.device)
     ldy = _act(out, "out", (s.T, H), rows)
-    _call("moe_unsort_rows", rows.device, lib.moe_unsort_rows, ctypes.byref(s), rows.data_ptr(), ldp, g,
+    _call("moe_unsort_rows", rows.get_device(), lib.moe_unsort_rows, ctypes.byref(s), rows.data_ptr(), ldp, g,
           _p(residual), ldr, out.data_ptr(), ldy)
     return out
 
@@ -242,7 +244,7 @@ def unsort_rows_backward(dY, rows, index, gates=None, out=None, want_dgates: boo
         out = t.empty((rows.shape[0], H), dtype=dY.dtype, device=dY.device)
     ldd = _act(out, "out", (rows.shape[0], H), dY)
     dg = t.empty((T, s.k), dtype=t.float32, device=dY.device) if want_dgates else None
-    _call("moe_unsort_rows_backward", dY.device, lib.moe_unsort_rows_backward, ctypes.byref(s), dY.data_ptr(), lddy,
+    _call("moe_unsort_rows_backward", dY.get_device(), lib.moe_unsort_rows_backward, ctypes.byref(s), dY.data_ptr(), lddy,
           rows.data_ptr(), ldp, g, out.data_ptr(), ldd, _p(dg))
     return out, dg
 
@@ -254,22 +256,27 @@ def clip_grad_norm(grads: Sequence, max_norm: float, outs: Optional[Sequence] = 
     lib = _load()
     t = _torch
     grads = list(grads)
-    outs = grads if outs is None else list(outs)
-    if not grads or len(outs) != len(grads):
+    if not grads or (outs is not None and len(outs) != len(grads)):
         raise ValueError("grads: at least one tensor, and as many outs")
-    dev = grads[0].device
-    vals = []
-    for g, o in zip(grads, outs):
-        dt = _dtypes.get(g.dtype)
-        if dt is None or g.device != dev or not g.is_cuda or not g.is_contiguous():
-            raise ValueError(f"grads: contiguous fp32 or bf16 CUDA tensors on one device are needed, got {g.dtype} on {g.device}")
-        if o is not g and (o.dtype != g.dtype or o.device != dev or o.numel() != g.numel() or not o.is_contiguous()):
-            raise ValueError("outs: as the gradients, contiguous")
-        vals += (g.data_ptr(), o.data_ptr() if clip else 0, g.numel(), dt)
-    table = array.array("q", vals)
+    tensor = t.Tensor
+    dev = grads[0].get_device()
+    ns = list(map(tensor.numel, grads))
+    kinds = [_dtypes.get(g.dtype, -1) for g in grads]
+    if dev < 0 or -1 in kinds or any(d != dev for d in map(tensor.get_device, grads)) or not all(map(tensor.is_contiguous, grads)):
+        raise ValueError("grads: contiguous fp32 or bf16 CUDA tensors on one device are needed")
+    ptrs = list(map(tensor.data_ptr, grads))
+    to = ptrs
+    if not clip:
+        to = [0] * len(grads)
+    elif outs is not None:
+        if (list(map(tensor.numel, outs)) != ns or [_dtypes.get(o.dtype, -1) for o in outs] != kinds or
+                any(d != dev for d in map(tensor.get_device, outs)) or not all(map(tensor.is_contiguous, outs))):
+            raise ValueError("outs: types, sizes and device of the gradients, contiguous")
+        to = list(map(tensor.data_ptr, outs))
+    table = array.array("q", [v for entry in zip(ptrs, to, ns, kinds) for v in entry])
     if ws is None:
-        ws = t.empty(moe_clip_workspace_size(len(grads)), dtype=t.uint8, device=dev)
-    norm = t.empty((), dtype=t.float32, device=dev)
+        ws = t.empty(moe_clip_workspace_size(len(grads)), dtype=t.uint8, device=grads[0].device)
+    norm = t.empty((), dtype=t.float32, device=grads[0].device)
     _call("moe_clip_grad_norm", dev, lib.moe_clip_grad_norm, len(grads), table.buffer_info()[0], max_norm,
           norm.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return norm
