@@ -5,18 +5,25 @@
 // Two passes over the values (the norm has to be known before the first
 // product): bound by HBM for large sets, by launches for small ones. The
 // tensors' table travels in the kernel's parameters, so a call copies nothing
-// to the device and can be captured; blocks take 64 KiB chunks of any tensor,
+// to the device and can be captured; blocks take chunks of any tensor,
 // so neither one large tensor nor hundreds of small ones leave SMs idle.
 #include "internal.h"
+#include "ptx.cuh"
 #include "rowvec.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kChunkBytes = 1 << 16;
+// Chunk sizes: the largest that still gives every block one, so a small set is
+// spread over the SMs and a large one keeps its pieces long.
+constexpr int kAhead = 4;               // 16-byte pieces that a thread loads together
+constexpr int kChunkMin = kClipThreads * kAhead * 16, kChunkMax = 1 << 16;
 constexpr int kClipBlocks = 1216;       // eight per SM
-constexpr int kClipBatch = 896;         // tensors per launch: 32 bytes each, within 32,764 of parameters
+// Tensors per launch: 32 bytes each, within the 32,764 of kernel parameters; a
+// short list takes a short table, which the launch copies faster.
+constexpr int kClipBatch = 896;
+constexpr int kClipShort = 64;
 
 struct Entry {
     const void* g;      // aligned down to 16 bytes
@@ -25,12 +32,15 @@ struct Entry {
     int chunk;          // first chunk of this tensor in the batch
     int info;           // bit 0: bf16; bits 1-3: values below the first; bit 4: out is not 16-byte aligned as g is
 };
+template <int CAP>
 struct Table {
     int count, chunks;
-    Entry e[kClipBatch];
+    int chunk_bytes;
+    Entry e[CAP];
 };
 
-__device__ __forceinline__ int find_entry(const Table& t, int chunk)
+template <int CAP>
+__device__ __forceinline__ int find_entry(const Table<CAP>& t, int chunk)
 {
     int lo = 0, hi = t.count - 1;
     while (lo < hi) {
@@ -60,64 +70,153 @@ __device__ __forceinline__ double block_sum_double(double v, double* red)
     return s;
 }
 
-// Values of the piece at index v0 that belong to the tensor: [lo, n).
-template <typename T, int V>
-__device__ __forceinline__ void load_piece(const T* g, long long v0, int lo, long long n, float (&v)[V])
+// One chunk of a tensor: `base` is 16-byte aligned, its values [lo, hi) belong
+// to the tensor.
+template <typename T>
+struct Chunk {
+    const T* base;
+    T* out;
+    int lo, hi;
+    bool whole;      // all of the chunk's pieces are whole
+    bool aligned;    // out is aligned as base is
+};
+
+template <typename T>
+__device__ __forceinline__ Chunk<T> chunk_of(const Entry& e, int chunk, int chunk_bytes)
 {
-    if (v0 >= lo && v0 + V <= n) {
-        load_vec<T, V>(g + v0, v);
-    } else {
+    const int values = chunk_bytes / (int)sizeof(T);
+    const long long v0 = (long long)(chunk - e.chunk) * values;
+    const long long left = e.n - v0;
+    Chunk<T> c;
+    c.base = static_cast<const T*>(e.g) + v0;
+    c.out = static_cast<T*>(e.out) + v0;
+    c.lo = chunk == e.chunk ? (e.info >> 1) & 7 : 0;
+    c.hi = left < values ? (int)left : values;
+    c.whole = c.lo == 0 && c.hi == values;
+    c.aligned = !(e.info & 16);
+    return c;
+}
+
+// Gives each piece of V values of a whole chunk to fn(index, raw), kAhead pieces
+// of the thread loaded before the first is used.
+template <typename T, typename FN>
+__device__ __forceinline__ void whole_chunk(const Chunk<T>& c, FN&& fn)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int STEP = kClipThreads * V;
+#pragma unroll 1
+    for (int at = threadIdx.x * V; at < c.hi; at += kAhead * STEP) {    // whole chunks are whole batches
+        Raw<T, V> q[kAhead];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float u[1] = {0.f};
-            if (v0 + i >= lo && v0 + i < n) load_vec<T, 1>(g + v0 + i, u);
-            v[i] = u[0];
+        for (int i = 0; i < kAhead; ++i) q[i] = load_raw<T, V>(c.base + at + i * STEP);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fn(at + i * STEP, q[i]);
+    }
+}
+
+// The same for a tensor's first and last chunks: fn gets the whole pieces,
+// fn1(index, raw) the single values of the others.
+template <typename T, typename FN, typename FN1>
+__device__ __forceinline__ void ragged_chunk(const Chunk<T>& c, FN&& fn, FN1&& fn1)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int STEP = kClipThreads * V;
+    constexpr int AHEAD = 4;
+#pragma unroll 1
+    for (int p0 = threadIdx.x * V; p0 < c.hi; p0 += AHEAD * STEP) {
+        Raw<T, V> q[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int p = p0 + i * STEP;
+            if (p >= c.lo && p + V <= c.hi) q[i] = load_raw<T, V>(c.base + p);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int p = p0 + i * STEP;
+            if (p >= c.lo && p + V <= c.hi) {
+                fn(p, q[i]);
+            } else {
+#pragma unroll 1
+                for (int j = p; j < p + V; ++j)
+                    if (j >= c.lo && j < c.hi) fn1(j, load_raw<T, 1>(c.base + j));
+            }
         }
     }
 }
 
-// This thread's share of the sum of squares of one chunk. The squares are
-// added in fp32; where that leaves its range (a sum that is not finite, or so
-// small that squares may have been flushed), the share is summed again in 64
-// bits, so the norm is right from the smallest values to the largest.
+// Sum of squares of the thread's share in 64 bits.
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T* g, long long v0, int lo, long long n)
+__device__ __noinline__ double squares_64(Chunk<T> c)
 {
     constexpr int V = 16 / (int)sizeof(T);
-    constexpr int VALUES = kChunkBytes / (int)sizeof(T);
-    const long long end = v0 + VALUES < n ? v0 + VALUES : n;
-    float s = 0.f;
-    bool any = false;
-    for (long long c = v0 + threadIdx.x * V; c < end; c += kClipThreads * V) {
-        float v[V];
-        load_piece<T, V>(g, c, lo, n, v);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            s = fmaf(v[i], v[i], s);
-            any = any || v[i] != 0.f;
-        }
-    }
-    if (!any || (s > 0x1p-60f && s < 0x1p126f)) return (double)s;
     double d = 0.0;
-    for (long long c = v0 + threadIdx.x * V; c < end; c += kClipThreads * V) {
-        float v[V];
-        load_piece<T, V>(g, c, lo, n, v);
-        for (int i = 0; i < V; ++i) d += (double)v[i] * (double)v[i];
-    }
+#pragma unroll 1
+    for (int p = threadIdx.x * V; p < c.hi; p += kClipThreads * V)
+#pragma unroll 1
+        for (int j = p; j < p + V; ++j)
+            if (j >= c.lo && j < c.hi) {
+                float v[1];
+                unpack<T, 1>(load_raw<T, 1>(c.base + j), v);
+                d += (double)v[0] * (double)v[0];
+            }
     return d;
 }
 
-__global__ void __launch_bounds__(kClipThreads)
-norm_kernel(const __grid_constant__ Table t, double* __restrict__ part)
+template <typename T, int V>
+__device__ __forceinline__ void add_squares(const Raw<T, V>& q, float& s, uint32_t& any)
+{
+    float v[V];
+    unpack<T, V>(q, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s = fmaf(v[i], v[i], s);
+    if constexpr (V == 1) any |= q;
+    else any |= q.x | q.y | q.z | q.w;
+}
+
+// The squares are added in fp32; where that leaves its range (a sum that is not
+// finite, or so small that squares may have been flushed), the share is summed
+// again in 64 bits, so the norm is right from the smallest values to the
+// largest. `any`: some bit of the values is set.
+template <typename T>
+__device__ __forceinline__ double checked(const Chunk<T>& c, float s, uint32_t any)
+{
+    return !any || (s > 0x1p-60f && s < 0x1p126f) ? (double)s : squares_64(c);
+}
+
+template <typename T>
+__device__ __noinline__ double ragged_squares(Chunk<T> c)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    float s = 0.f;
+    uint32_t any = 0;
+    ragged_chunk(c, [&](int, const Raw<T, V>& q) { add_squares<T, V>(q, s, any); },
+                 [&](int, const Raw<T, 1>& q) { add_squares<T, 1>(q, s, any); });
+    return checked(c, s, any);
+}
+
+// This thread's share of the sum of squares of one chunk.
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const Chunk<T>& c)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    if (!c.whole) return ragged_squares(c);
+    float s = 0.f;
+    uint32_t any = 0;
+    whole_chunk(c, [&](int, const Raw<T, V>& q) { add_squares<T, V>(q, s, any); });
+    return checked(c, s, any);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kClipThreads, 4)
+norm_kernel(const __grid_constant__ Table<CAP> t, double* __restrict__ part)
 {
     __shared__ double red[kClipThreads / 32];
+    ptx::griddep_launch_dependents();
     double s = 0.0;
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const Entry& e = t.e[find_entry(t, c)];
-        const int lo = (e.info >> 1) & 7;
-        const long long at = (long long)(c - e.chunk) * kChunkBytes;
-        s += e.info & 1 ? chunk_squares(static_cast<const __nv_bfloat16*>(e.g), at / 2, lo, e.n)
-                        : chunk_squares(static_cast<const float*>(e.g), at / 4, lo, e.n);
+        s += e.info & 1 ? chunk_squares(chunk_of<__nv_bfloat16>(e, c, t.chunk_bytes))
+                        : chunk_squares(chunk_of<float>(e, c, t.chunk_bytes));
     }
     s = block_sum_double(s, red);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -127,7 +226,7 @@ norm_kernel(const __grid_constant__ Table t, double* __restrict__ part)
 __device__ __forceinline__ double total_norm(const double* part, int nparts, double* red)
 {
     double s = 0.0;
-    for (int i = threadIdx.x; i < nparts; i += kClipThreads) s += part[i];
+    for (int i = threadIdx.x; i < nparts; i += kClipThreads) s += __ldcg(part + i);
     return sqrt(block_sum_double(s, red));
 }
 
@@ -135,64 +234,65 @@ __global__ void __launch_bounds__(kClipThreads)
 norm_finish_kernel(const double* __restrict__ part, int nparts, float* __restrict__ norm)
 {
     __shared__ double red[kClipThreads / 32];
+    ptx::griddep_wait();
     const double n = total_norm(part, nparts, red);
     if (threadIdx.x == 0) *norm = (float)n;
 }
 
-// One chunk of out = g c, or without CLIP a copy of its bits.
-template <typename T, bool CLIP>
-__device__ __forceinline__ void scale_chunk(const T* g, T* out, long long v0, int lo, long long n, bool aligned, float c)
+// The bits of value i of a piece.
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, 1> piece_value(const Raw<T, V>& q, int i)
 {
-    constexpr int V = 16 / (int)sizeof(T);
-    constexpr int VALUES = kChunkBytes / (int)sizeof(T);
-    const long long end = v0 + VALUES < n ? v0 + VALUES : n;
-    for (long long p = v0 + threadIdx.x * V; p < end; p += kClipThreads * V) {
-        if (aligned && p >= lo && p + V <= n) {
-            Raw<T, V> q = load_raw<T, V>(g + p);
-            if constexpr (CLIP) {
-                float v[V];
-                unpack<T, V>(q, v);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (sizeof(T) == 4) return w[i];
+    else return (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> scaled(const Raw<T, V>& q, float f)
+{
+    float v[V];
+    unpack<T, V>(q, v);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] *= c;
-                q = pack<T, V>(v);
-            }
-            store_raw<T, V>(out + p, q);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (p + i < lo || p + i >= n) continue;
-                Raw<T, 1> q = load_raw<T, 1>(g + p + i);
-                if constexpr (CLIP) {
-                    float v[1];
-                    unpack<T, 1>(q, v);
-                    v[0] *= c;
-                    q = pack<T, 1>(v);
-                }
-                store_raw<T, 1>(out + p + i, q);
-            }
-        }
-    }
+    for (int i = 0; i < V; ++i) v[i] *= f;
+    return pack<T, V>(v);
 }
 
 template <typename T>
-__device__ __forceinline__ void clip_chunk(const Entry& e, int chunk, bool clip, float f)
+__device__ __noinline__ void ragged_scale(Chunk<T> c, bool clip, float f)
 {
-    const T* g = static_cast<const T*>(e.g);
-    T* out = static_cast<T*>(e.out);
-    const long long v0 = (long long)(chunk - e.chunk) * (kChunkBytes / (int)sizeof(T));
-    const int lo = (e.info >> 1) & 7;
-    const bool aligned = !(e.info & 16);
-    if (clip) scale_chunk<T, true>(g, out, v0, lo, e.n, aligned, f);
-    else scale_chunk<T, false>(g, out, v0, lo, e.n, aligned, f);
+    constexpr int V = 16 / (int)sizeof(T);
+    ragged_chunk(c,
+        [&](int p, const Raw<T, V>& q) {
+            const Raw<T, V> r = clip ? scaled<T, V>(q, f) : q;
+            if (c.aligned) {
+                store_raw<T, V>(c.out + p, r);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) store_raw<T, 1>(c.out + p + i, piece_value<T, V>(r, i));
+            }
+        },
+        [&](int p, const Raw<T, 1>& q) { store_raw<T, 1>(c.out + p, clip ? scaled<T, 1>(q, f) : q); });
+}
+
+// One chunk of out = g f, or without clip a copy of its bits.
+template <typename T>
+__device__ __forceinline__ void clip_chunk(const Chunk<T>& c, bool clip, float f)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    if (!c.whole || !c.aligned) ragged_scale(c, clip, f);
+    else whole_chunk(c, [&](int p, const Raw<T, V>& q) { store_raw<T, V>(c.out + p, clip ? scaled<T, V>(q, f) : q); });
 }
 
 // out = g c with c from the norm; the last chunks first, since the norm's
 // pass read them last and L2 still holds them.
-__global__ void __launch_bounds__(kClipThreads)
-clip_kernel(const __grid_constant__ Table t, const double* __restrict__ part, int nparts, float max_norm,
+template <int CAP>
+__global__ void __launch_bounds__(kClipThreads, 4)
+clip_kernel(const __grid_constant__ Table<CAP> t, const double* __restrict__ part, int nparts, float max_norm,
             float* __restrict__ norm)
 {
     __shared__ double red[kClipThreads / 32];
+    ptx::griddep_wait();
     const double n = total_norm(part, nparts, red);
     if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = (float)n;
     const bool clip = n > (double)max_norm && n - n == 0.0;
@@ -200,17 +300,19 @@ clip_kernel(const __grid_constant__ Table t, const double* __restrict__ part, in
     for (int c = t.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
         const Entry& e = t.e[find_entry(t, c)];
         if (!e.out || (!clip && e.out == e.g)) continue;
-        if (e.info & 1) clip_chunk<__nv_bfloat16>(e, c, clip, f);
-        else clip_chunk<float>(e, c, clip, f);
+        if (e.info & 1) clip_chunk(chunk_of<__nv_bfloat16>(e, c, t.chunk_bytes), clip, f);
+        else clip_chunk(chunk_of<float>(e, c, t.chunk_bytes), clip, f);
     }
 }
 
 int batches(int count) { return (count + kClipBatch - 1) / kClipBatch; }
 
 // The table of tensors [first, first + count) of the list.
-void fill_table(const moe_grad_t* list, int first, int count, Table& t)
+template <int CAP>
+void fill_table(const moe_grad_t* list, int first, int count, int chunk_bytes, Table<CAP>& t)
 {
     t.count = count;
+    t.chunk_bytes = chunk_bytes;
     long long chunks = 0;
     for (int i = 0; i < count; ++i) {
         const moe_grad_t& m = list[first + i];
@@ -223,12 +325,58 @@ void fill_table(const moe_grad_t* list, int first, int count, Table& t)
         e.g = m.n > 0 ? reinterpret_cast<const void*>(a - lo * size) : nullptr;
         e.out = m.n > 0 && m.out ? reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(m.out) - lo * size) : nullptr;
         e.info = (m.dtype == MOE_BF16 ? 1 : 0) | lo << 1 | (reinterpret_cast<uintptr_t>(e.out) % 16 ? 16 : 0);
-        chunks += (e.n * size + kChunkBytes - 1) / kChunkBytes;
+        chunks += (e.n * size + chunk_bytes - 1) / chunk_bytes;
     }
     t.chunks = (int)chunks;
 }
 
-unsigned clip_grid(const Table& t) { return t.chunks < kClipBlocks ? (t.chunks > 0 ? t.chunks : 1) : kClipBlocks; }
+// The launches of one call, CAP tensors at a time: every batch's sum of
+// squares, then (writes) every batch's product, or the norm alone.
+template <int CAP>
+cudaError_t run_clip(int count, const moe_grad_t* list, int chunk_bytes, bool writes, float max_norm, float* norm,
+                     double* part, cudaStream_t s)
+{
+    Table<CAP> t;
+    int nparts = 0;
+    auto fill = [&](int first) {
+        fill_table(list, first, count - first < CAP ? count - first : CAP, chunk_bytes, t);
+        return (unsigned)(t.chunks < kClipBlocks ? (t.chunks > 0 ? t.chunks : 1) : kClipBlocks);
+    };
+    unsigned grid = 0;
+    for (int first = 0; first < count || first == 0; first += CAP) {
+        grid = fill(first);
+        double* to = part + nparts;
+        void* args[] = {&t, &to};
+        const cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(norm_kernel<CAP>), dim3(grid),
+                                               dim3(kClipThreads), args, 0, s);
+        if (e != cudaSuccess) return e;
+        count_launches();
+        nparts += (int)grid;
+    }
+    if (!writes) {
+        count_launches();
+        return launch_early(norm_finish_kernel, dim3(1), dim3(kClipThreads), s, (const double*)part, nparts, norm);
+    }
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kClipThreads);
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    for (int first = 0; first < count; first += CAP) {
+        if (count > CAP) grid = fill(first);
+        cfg.gridDim = dim3(grid);
+        float* to = first == 0 ? norm : nullptr;
+        const double* from = part;
+        void* args[] = {&t, &from, &nparts, &max_norm, &to};
+        const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(clip_kernel<CAP>), args);
+        if (e != cudaSuccess) return e;
+        count_launches();
+    }
+    return cudaSuccess;
+}
 
 }  // namespace
 }  // namespace moe
@@ -266,24 +414,10 @@ moe_status_t moe_clip_grad_norm(int count, const moe_grad_t* list, float max_nor
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     double* part = static_cast<double*>(ws);
-    Table t;
-    int nparts = 0;
-    for (int first = 0; first < count || first == 0; first += kClipBatch) {
-        fill_table(list, first, count - first < kClipBatch ? count - first : kClipBatch, t);
-        const unsigned grid = clip_grid(t);
-        norm_kernel<<<grid, kClipThreads, 0, s>>>(t, part + nparts);
-        count_launches();
-        nparts += (int)grid;
-    }
-    if (writes) {
-        for (int first = 0; first < count; first += kClipBatch) {
-            fill_table(list, first, count - first < kClipBatch ? count - first : kClipBatch, t);
-            clip_kernel<<<clip_grid(t), kClipThreads, 0, s>>>(t, part, nparts, max_norm, first == 0 ? norm : nullptr);
-            count_launches();
-        }
-    } else {
-        norm_finish_kernel<<<1, kClipThreads, 0, s>>>(part, nparts, norm);
-        count_launches();
-    }
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    int chunk_bytes = kChunkMax;
+    while (chunk_bytes > kChunkMin && bytes / chunk_bytes < kClipBlocks) chunk_bytes /= 2;
+    const cudaError_t e = count <= kClipShort
+        ? run_clip<kClipShort>(count, list, chunk_bytes, writes, max_norm, norm, part, s)
+        : run_clip<kClipBatch>(count, list, chunk_bytes, writes, max_norm, norm, part, s);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -19,6 +19,8 @@ constexpr int kNormThreads = 256;
 // Row groups of the weight gradient's partial sums (blocks of the backward):
 // two per SM.
 constexpr int kNormParts = 304;
+// Up to one row per SM the forward gives a row more threads.
+constexpr int kFewRows = 152;
 
 // Sum of v over the block's NT threads, the same order on every call; `red`
 // holds NT / 32 floats and may be reused after the next __syncthreads.
@@ -146,7 +148,9 @@ norm_fwd_loop_kernel(FwdArgs<T> a)
 // One row per group of GROUP threads (a warp, or the block), held in registers
 // between the sum and the output: each value is read once. N pieces of V values
 // per thread cover the row, so H <= GROUP * N * V.
-template <typename T, int V, int N, int GROUP, int QUANT>
+// AHEAD fetches the weights with the row, for launches of few rows, whose time
+// is the chain of loads.
+template <typename T, int V, int N, int GROUP, int QUANT, bool AHEAD = false>
 __global__ void __launch_bounds__(GROUP == 32 ? kNormThreads : GROUP)
 norm_fwd_kernel(FwdArgs<T> a)
 {
@@ -168,6 +172,14 @@ norm_fwd_kernel(FwdArgs<T> a)
         if (c < a.H) {
             qx[i] = load_raw<T, V>(x + c);
             if (r) qr[i] = load_raw<T, V>(r + c);
+        }
+    }
+    float wa[AHEAD ? N : 1][V];
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (tid + i * GROUP) * V;
+            if (c < a.H) load_f32<V>(a.w + c, wa[i]);
         }
     }
     float v[N][V];
@@ -199,9 +211,9 @@ norm_fwd_kernel(FwdArgs<T> a)
         if (act) {
             float w[V];
             if (a.h) store_vec<T, V>(a.h + row * a.ldh + c, v[i]);
-            load_f32<V>(a.w + c, w);
+            if constexpr (!AHEAD) load_f32<V>(a.w + c, w);
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * rstd * w[j];
+            for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * rstd * (AHEAD ? wa[AHEAD ? i : 0][j] : w[j]);
             if (a.y) store_vec<T, V>(a.y + row * a.ldy + c, v[i]);
         }
         if constexpr (QUANT != MOE_NORM_PLAIN) quantise<QUANT, V>(v[i], act, (int)row, c, a.H, a.codes, a.scales);
@@ -439,7 +451,7 @@ norm_dweight_kernel(const float* __restrict__ part, int nparts, int H, float* __
     float s = 0.f;
     ptx::griddep_wait();
     if (c < H)
-        for (int b = ph; b < nparts; b += kPhases) s += part[(size_t)b * H + c];
+        for (int b = ph; b < nparts; b += kPhases) s += __ldcg(part + (size_t)b * H + c);
     red[ph][lane] = s;
     __syncthreads();
     if (ph == 0 && c < H) {
@@ -460,6 +472,11 @@ void launch_fwd_width(const FwdArgs<T>& a, cudaStream_t s)
     const int warps = (rows + kNormThreads / 32 - 1) / (kNormThreads / 32);
     if (a.H <= 256) norm_fwd_kernel<T, V, P / 4, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
     else if (a.H <= 1024) norm_fwd_kernel<T, V, P, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
+    else if (a.rows <= kFewRows && a.H <= 8192) {
+        // few rows: a thread per eight values shortens each row's own chain
+        if (a.H <= 4096) norm_fwd_kernel<T, V, P / 4, 512, QUANT, true><<<rows, 512, 0, s>>>(a);
+        else norm_fwd_kernel<T, V, P / 4, 1024, QUANT, true><<<rows, 1024, 0, s>>>(a);
+    }
     else if (a.H <= 2048) norm_fwd_kernel<T, V, P / 4, 256, QUANT><<<rows, 256, 0, s>>>(a);
     else if (a.H <= 4096) norm_fwd_kernel<T, V, P / 2, 256, QUANT><<<rows, 256, 0, s>>>(a);
     else if (a.H <= 8192) norm_fwd_kernel<T, V, P, 256, QUANT><<<rows, 256, 0, s>>>(a);

@@ -22,52 +22,65 @@ constexpr int kSortMaxAlign = 4096;
 constexpr int kIndexThreads = 1024;
 constexpr int kIndexWarps = kIndexThreads / 32;
 
-// Expert of slot i, or E for a dropped slot or one past the end.
+// Expert of slot i < n, or -1 for a dropped slot or one past the end.
 __device__ __forceinline__ int slot_expert(const int32_t* topk, int i, int n, int E)
 {
-    if (i >= n) return E;
+    if (i >= n) return -1;
     const int e = topk[i];
-    return (unsigned)e < (unsigned)E ? e : E;
+    return (unsigned)e < (unsigned)E ? e : -1;
 }
 
-// The blocks of one cluster. Each warp takes a run of consecutive slots: it
+// The blocks of a cluster. Each warp takes a run of consecutive slots: it
 // counts its slots of each expert, the counts are summed over warps, blocks
 // (through distributed shared memory) and experts, and it then goes over its
 // slots again in order, 32 at a time; lanes with the same expert find one
-// another with a match, so a slot's rank needs no atomic and the order is the
-// slots' own. Shared memory: `warps` x E counters and the block's E totals.
+// another by one ballot per bit of the expert's number (a match instruction
+// took 8x as long), so a slot's rank needs no atomic and the order is the
+// slots' own. With several clusters each counts everything, and a run's second
+// part is done by one of them: the scattered stores of slot_of, about one a
+// cycle and SM, are what takes longest. Shared memory: `warps` x E counters,
+// the block's E totals and the E padding ranges.
 __global__ void __launch_bounds__(kIndexThreads)
-sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, int E, int align,
+sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, int E, int bits, int align,
                   int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ row_of,
                   int32_t* __restrict__ slot_of, int rows)
 {
-    extern __shared__ int hist[];            // [warps][E], then [E]
+    extern __shared__ int hist[];            // [warps][E], [E], [E][2]
     __shared__ int wsum[kIndexWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = (int)ptx::cluster_ctarank(), blocks = gridDim.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+    const int rank = (int)ptx::cluster_ctarank(), cluster = (int)ptx::cluster_id_x();
+    const int clusters = (int)ptx::nclusters_x(), blocks = gridDim.x / clusters;
     const long long lo = ((long long)rank * warps + warp) * per;      // slots [lo, lo + per) of this warp
     const long long left = n - lo;
     const int mine_n = warp < warps && left > 0 ? (left < per ? (int)left : per) : 0;
     int* mine = hist + warp * E;
     int* tot = hist + warps * E;
-    for (int i = tid; i < warps * E; i += kIndexThreads) hist[i] = 0;
+    int2* pad = reinterpret_cast<int2*>(tot + E + (E * (warps + 1) & 1));
+    for (int i = tid; i < warps * E; i += nt) hist[i] = 0;
     __syncthreads();
-    constexpr int U = 4;                     // groups of 32 slots loaded together
+    // U groups of 32 slots are loaded together; the second part's first groups
+    // are its last here
+    constexpr int U = 8;
+    int next[U];
+    auto load = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) next[u] = slot_expert(topk + lo, i + 32 * u + lane, mine_n, E);
+    };
+    load(0);
     for (int i = 0; i < mine_n; i += 32 * U) {
         int ex[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) ex[u] = slot_expert(topk + lo, i + 32 * u + lane, mine_n, E);
+        for (int u = 0; u < U; ++u) ex[u] = next[u];
+        load(i + 32 * U < mine_n ? i + 32 * U : 0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const unsigned peers = __match_any_sync(0xffffffffu, ex[u]);
-            if (ex[u] < E && lane == __ffs(peers) - 1) mine[ex[u]] += __popc(peers);
-            __syncwarp();
-        }
+        for (int u = 0; u < U; ++u)
+            if (ex[u] >= 0) atomicAdd(mine + ex[u], 1);      // integers: the order does not matter
     }
     __syncthreads();
     // thread e: counts of expert e -> each warp's base among the block's slots
     if (tid < E) {
         int total = 0;
+#pragma unroll 4
         for (int w = 0; w < warps; ++w) {
             const int c = hist[w * E + tid];
             hist[w * E + tid] = total;
@@ -79,6 +92,7 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
     int total = 0, below = 0;
     if (tid < E) {
         const uint32_t at = ptx::smem_u32(tot + tid);
+#pragma unroll 4
         for (int r = 0; r < blocks; ++r) {
             int c;
             asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(ptx::mapa_shared(at, r)) : "memory");
@@ -97,35 +111,45 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
     if (lane == 31) wsum[warp] = sum;
     __syncthreads();
     int before = 0, used = 0;
-#pragma unroll
-    for (int w = 0; w < kIndexWarps; ++w) {
+    for (int w = 0; w < nt / 32; ++w) {
         before += w < warp ? wsum[w] : 0;
         used += wsum[w];
     }
     const int off = before + sum - padded;
     if (tid < E) {
+#pragma unroll 4
         for (int w = 0; w < warps; ++w) hist[w * E + tid] += off + below;
-        if (rank == 0) {
+        if (blockIdx.x == 0) {
             counts[tid] = total;
             offsets[tid] = off;
         }
-        if (tid % blocks == rank)
-            for (int r = off + total; r < off + padded; ++r) slot_of[r] = -1;
+        pad[tid] = make_int2(off + total, off + padded);
     }
-    if (rank == 0 && tid == 0) offsets[E] = used;
-    for (long long r = used + (long long)rank * kIndexThreads + tid; r < rows; r += blocks * kIndexThreads) slot_of[r] = -1;
+    if (blockIdx.x == 0 && tid == 0) offsets[E] = used;
     __syncthreads();
-    for (int i = 0; i < mine_n; i += 32 * U) {
+    for (int i = 0; i < mine_n && warp % clusters == cluster; i += 32 * U) {
         int ex[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) ex[u] = slot_expert(topk + lo, i + 32 * u + lane, mine_n, E);
+        unsigned peers[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const unsigned peers = __match_any_sync(0xffffffffu, ex[u]);
+            ex[u] = next[u];
+            peers[u] = __ballot_sync(0xffffffffu, ex[u] >= 0);
+        }
+        load(i + 32 * U);
+        for (int b = 0; b < bits; ++b) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool one = ex[u] >> b & 1;
+                const unsigned m = __ballot_sync(0xffffffffu, one);
+                peers[u] &= one ? m : ~m;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             int row = -1;
-            if (ex[u] < E) row = mine[ex[u]] + __popc(peers & ((1u << lane) - 1));
+            if (ex[u] >= 0) row = mine[ex[u]] + __popc(peers[u] & ((1u << lane) - 1));
             __syncwarp();
-            if (ex[u] < E && lane == __ffs(peers) - 1) mine[ex[u]] += __popc(peers);
+            if (ex[u] >= 0 && lane == __ffs(peers[u]) - 1) mine[ex[u]] += __popc(peers[u]);
             __syncwarp();
             const int s = i + 32 * u + lane;
             if (s < mine_n) {
@@ -134,12 +158,17 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
             }
         }
     }
+    // a warp per segment's padding, and the rows after the last segment
+    for (int e = blockIdx.x * (nt / 32) + warp; e < E; e += gridDim.x * (nt / 32))
+        for (int r = pad[e].x + lane; r < pad[e].y; r += 32) slot_of[r] = -1;
+    for (long long r = used + (long long)blockIdx.x * nt + tid; r < rows; r += gridDim.x * nt) slot_of[r] = -1;
     ptx::cluster_sync();                     // no block leaves while another may read its totals
 }
 
-// Blocks of the cluster: one up to 4096 slots, where a cluster's barriers cost
-// more than they save, else eight.
-constexpr int kIndexOneBlock = 4096;
+// Four groups of slots for a warp while there are few; one block up to eight
+// warps, where a cluster's barriers cost more than they save, else clusters of
+// eight: one for each 16384 slots, at most 16.
+constexpr int kIndexOneBlock = 1024;
 constexpr int kIndexCluster = 8;
 
 cudaError_t launch_index(int n, int E, int align, const int32_t* topk, int32_t* counts, int32_t* offsets,
@@ -147,13 +176,16 @@ cudaError_t launch_index(int n, int E, int align, const int32_t* topk, int32_t* 
 {
     const int blocks = n <= kIndexOneBlock ? 1 : kIndexCluster;
     const int groups = (n + 31) / 32;
-    int warps = (groups + blocks - 1) / blocks;
+    int warps = (groups + 4 * blocks - 1) / (4 * blocks);
     warps = warps < 1 ? 1 : (warps > kIndexWarps ? kIndexWarps : warps);
     const int per = (groups + blocks * warps - 1) / (blocks * warps) * 32;
-    const size_t smem = (size_t)(warps + 1) * E * sizeof(int);
+    const int threads = 32 * warps > E ? 32 * warps : (E + 31) / 32 * 32;
+    int bits = 0;
+    while (1 << bits < E) ++bits;
+    const size_t smem = (size_t)(warps + 3) * E * sizeof(int) + 8;
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(sort_index_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (kIndexWarps + 1) * kSortMaxE * (int)sizeof(int));
+                                                   (kIndexWarps + 3) * kSortMaxE * (int)sizeof(int) + 8);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute at{};
@@ -161,17 +193,22 @@ cudaError_t launch_index(int n, int E, int align, const int32_t* topk, int32_t* 
     at.val.clusterDim.x = blocks;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kIndexThreads);
+    const int clusters = blocks == 1 || n < 32768 ? 1 : (n >= 16 * 16384 ? 16 : n / 16384);
+    cfg.gridDim = dim3(blocks * clusters);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sort_index_kernel, topk, n, per, warps, E, align, counts, offsets, row_of, slot_of, rows);
+    return cudaLaunchKernelEx(&cfg, sort_index_kernel, topk, n, per, warps, E, bits, align, counts, offsets, row_of,
+                              slot_of, rows);
 }
 
 // ------------------------------------------------------------------ rows
 constexpr int kMoveThreads = 128;
+// Up to this many tokens a block per token leaves SMs idle: rows are then cut
+// into column parts (or, for the gradient's dot products, blocks are larger).
+constexpr int kFewTokens = 1216;
 // Rows that one block of the padding part looks at.
 constexpr int kPadRows = 16;
 
@@ -191,7 +228,8 @@ __device__ __forceinline__ void zero_padding(const IndexArgs& ix, T* buf, long l
     for (int i = 0; i < V; ++i) z[i] = 0.f;
     for (long long r = r0; r < r0 + kPadRows && r < used; ++r) {
         if (ix.slot_of[r] >= 0) continue;
-        for (int c = threadIdx.x * V; c < ix.H; c += kMoveThreads * V) store_vec<T, V>(buf + r * ld + c, z);
+        for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * V; c < ix.H; c += gridDim.y * blockDim.x * V)
+            store_vec<T, V>(buf + r * ld + c, z);
     }
 }
 
@@ -219,7 +257,7 @@ sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __rest
     for (int j0 = 0; j0 < ix.k; j0 += KM) {
         long long row[KM];
         slot_rows<KM>(ix, t, j0, row);
-        for (int c = threadIdx.x * V; c < ix.H; c += kMoveThreads * V) {
+        for (int c = (blockIdx.y * kMoveThreads + threadIdx.x) * V; c < ix.H; c += gridDim.y * kMoveThreads * V) {
             const Raw<T, V> q = load_raw<T, V>(x + (size_t)t * ldx + c);
 #pragma unroll
             for (int j = 0; j < KM; ++j)
@@ -228,39 +266,44 @@ sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __rest
     }
 }
 
-// y[t] = residual[t] + sum over the slots in order of g Yp[row].
-template <typename T, int V, int KM>
+// Row of slot j of token t, -1 if dropped or past k.
+__device__ __forceinline__ int slot_row(const IndexArgs& ix, int t, int j)
+{
+    const int r = j < ix.k ? ix.row_of[(size_t)t * ix.k + j] : -1;
+    return r < ix.rows ? r : -1;
+}
+
+// y[t] = residual[t] + sum over the slots in order of g Yp[row]. WHOLE: k <= KM,
+// the index is read once per token.
+template <typename T, int V, int KM, bool WHOLE>
 __global__ void __launch_bounds__(kMoveThreads)
 unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const float* __restrict__ gates,
                    const T* residual, long long ldr, T* y, long long ldy)
 {
     const int t = blockIdx.x;
-    long long row[KM];
+    int row[KM];
     float g[KM];
-    const bool whole = ix.k <= KM;           // every slot fits: read the index once
-    if (whole) {
-        slot_rows<KM>(ix, t, 0, row);
+    auto index = [&](int j0) {
 #pragma unroll
-        for (int j = 0; j < KM; ++j) g[j] = gates && j < ix.k ? gates[(size_t)t * ix.k + j] : 1.f;
-    }
-    for (int c = threadIdx.x * V; c < ix.H; c += kMoveThreads * V) {
-        float acc[V];
-        if (residual) {
-            load_vec<T, V>(residual + (size_t)t * ldr + c, acc);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        for (int j = 0; j < KM; ++j) {
+            row[j] = slot_row(ix, t, j0 + j);
+            g[j] = gates && j0 + j < ix.k ? gates[(size_t)t * ix.k + j0 + j] : 1.f;
         }
-        for (int j0 = 0; j0 < ix.k; j0 += KM) {
-            if (!whole) {
-                slot_rows<KM>(ix, t, j0, row);
+    };
+    if (WHOLE) index(0);
+    for (int c = (blockIdx.y * kMoveThreads + threadIdx.x) * V; c < ix.H; c += gridDim.y * kMoveThreads * V) {
+        float acc[V];
 #pragma unroll
-                for (int j = 0; j < KM; ++j) g[j] = gates && j0 + j < ix.k ? gates[(size_t)t * ix.k + j0 + j] : 1.f;
-            }
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        Raw<T, V> res;
+        if (residual) res = load_raw<T, V>(residual + (size_t)t * ldr + c);
+        for (int j0 = 0; j0 < (WHOLE ? 1 : ix.k); j0 += KM) {
+            if (!WHOLE) index(j0);
             Raw<T, V> q[KM];
 #pragma unroll
             for (int j = 0; j < KM; ++j)
                 if (row[j] >= 0) q[j] = load_raw<T, V>(Yp + row[j] * ldp + c);
+            if (j0 == 0 && residual) unpack<T, V>(res, acc);
 #pragma unroll
             for (int j = 0; j < KM; ++j) {
                 if (row[j] < 0) continue;
@@ -276,8 +319,8 @@ unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const 
 
 // Blocks [0, T): dYp[row_j] = g_j dY[t] and dg_j = <dY[t], Yp[row_j]>.
 // Blocks from T on: padding rows.
-template <typename T, int V, int KM, bool DG>
-__global__ void __launch_bounds__(kMoveThreads)
+template <typename T, int V, int KM, int NT, bool DG>
+__global__ void __launch_bounds__(NT)
 unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const T* Yp, long long ldp,
                   const float* __restrict__ gates, T* dYp, long long ldd, float* __restrict__ dgates)
 {
@@ -285,7 +328,7 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
         zero_padding<T, V>(ix, dYp, ldd, (long long)(blockIdx.x - ix.T) * kPadRows);
         return;
     }
-    __shared__ float red[kMoveThreads / 32][KM];
+    __shared__ float red[NT / 32][KM];
     const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int j0 = 0; j0 < ix.k; j0 += KM) {
         long long row[KM];
@@ -296,7 +339,7 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
             g[j] = gates && j0 + j < ix.k ? gates[(size_t)t * ix.k + j0 + j] : 1.f;
             dot[j] = 0.f;
         }
-        for (int c = threadIdx.x * V; c < ix.H; c += kMoveThreads * V) {
+        for (int c = threadIdx.x * V; c < ix.H; c += NT * V) {
             float d[V];
             load_vec<T, V>(dY + (size_t)t * lddy + c, d);
             Raw<T, V> q[KM];
@@ -333,7 +376,7 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
             if (threadIdx.x < KM && j0 + (int)threadIdx.x < ix.k) {
                 float s = 0.f;
 #pragma unroll
-                for (int w = 0; w < kMoveThreads / 32; ++w) s += red[w][threadIdx.x];
+                for (int w = 0; w < NT / 32; ++w) s += red[w][threadIdx.x];
                 dgates[(size_t)t * ix.k + j0 + threadIdx.x] = s;
             }
         }
@@ -341,13 +384,14 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
 }
 
 // Calls F with the slot bound of k: 1, 2, 4 or 8 rows at a time.
+constexpr int kMaxSlots = 8;
 template <typename F>
 void with_slots(int k, F&& f)
 {
     if (k <= 1) f(std::integral_constant<int, 1>{});
     else if (k <= 2) f(std::integral_constant<int, 2>{});
     else if (k <= 4) f(std::integral_constant<int, 4>{});
-    else f(std::integral_constant<int, 8>{});
+    else f(std::integral_constant<int, kMaxSlots>{});
 }
 // Calls F with the values per access.
 template <typename T, typename F>
@@ -366,6 +410,13 @@ unsigned move_grid(const moe_sorted_t& s)
 {
     return (unsigned)(s.T + (s.slot_of ? (s.rows + kPadRows - 1) / kPadRows : 0));
 }
+// Column parts of a launch whose blocks take V values per thread at a time.
+unsigned column_parts(const moe_sorted_t& s, int V)
+{
+    const int most = (s.H + kMoveThreads * V - 1) / (kMoveThreads * V);
+    const int wanted = s.T > 0 ? (kFewTokens + s.T - 1) / s.T : 1;
+    return (unsigned)(s.T >= kFewTokens ? 1 : (wanted < most ? wanted : most));
+}
 
 template <typename T>
 void sort_rows(const moe_sorted_t& ix, const void* x, long long ldx, void* Xp, long long ldp, cudaStream_t s)
@@ -373,7 +424,8 @@ void sort_rows(const moe_sorted_t& ix, const void* x, long long ldx, void* Xp, l
     const long long st[] = {ldx, ldp};
     with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, 2), [&](auto v) {
         with_slots(ix.k, [&](auto km) {
-            sort_rows_kernel<T, decltype(v)::value, decltype(km)::value><<<move_grid(ix), kMoveThreads, 0, s>>>(
+            constexpr int V = decltype(v)::value;
+            sort_rows_kernel<T, V, decltype(km)::value><<<dim3(move_grid(ix), column_parts(ix, V)), kMoveThreads, 0, s>>>(
                 index_args(ix), static_cast<const T*>(x), ldx, static_cast<T*>(Xp), ldp);
         });
     });
@@ -386,9 +438,16 @@ void unsort_rows(const moe_sorted_t& ix, const void* Yp, long long ldp, const fl
     const long long st[] = {ldp, ldy, ldr};
     with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, residual ? 3 : 2), [&](auto v) {
         with_slots(ix.k, [&](auto km) {
-            unsort_rows_kernel<T, decltype(v)::value, decltype(km)::value><<<ix.T, kMoveThreads, 0, s>>>(
-                index_args(ix), static_cast<const T*>(Yp), ldp, gates, static_cast<const T*>(residual), ldr,
-                static_cast<T*>(y), ldy);
+            constexpr int V = decltype(v)::value;
+            constexpr int KM = decltype(km)::value;
+            auto launch = [&](auto whole) {
+                unsort_rows_kernel<T, V, KM, decltype(whole)::value>
+                    <<<dim3(ix.T, column_parts(ix, V)), kMoveThreads, 0, s>>>(
+                        index_args(ix), static_cast<const T*>(Yp), ldp, gates, static_cast<const T*>(residual), ldr,
+                        static_cast<T*>(y), ldy);
+            };
+            if (ix.k <= KM) launch(std::true_type{});
+            else if constexpr (KM == kMaxSlots) launch(std::false_type{});
         });
     });
 }
@@ -404,12 +463,14 @@ void unsort_bwd(const moe_sorted_t& ix, const void* dY, long long lddy, const vo
             const T* d = static_cast<const T*>(dY);
             const T* y = static_cast<const T*>(Yp);
             T* o = static_cast<T*>(dYp);
-            if (dgates)
-                unsort_bwd_kernel<T, V, KM, true><<<move_grid(ix), kMoveThreads, 0, s>>>(
+            auto launch = [&](auto nt, auto dg) {
+                constexpr int NT = decltype(nt)::value;
+                unsort_bwd_kernel<T, V, KM, NT, decltype(dg)::value><<<move_grid(ix), NT, 0, s>>>(
                     index_args(ix), d, lddy, y, ldp, gates, o, ldd, dgates);
-            else
-                unsort_bwd_kernel<T, V, KM, false><<<move_grid(ix), kMoveThreads, 0, s>>>(
-                    index_args(ix), d, lddy, y, ldp, gates, o, ldd, dgates);
+            };
+            if (!dgates) launch(std::integral_constant<int, kMoveThreads>{}, std::false_type{});
+            else if (ix.T < kFewTokens / 2) launch(std::integral_constant<int, 512>{}, std::true_type{});
+            else launch(std::integral_constant<int, kMoveThreads>{}, std::true_type{});
         });
     });
 }
