@@ -57,14 +57,17 @@ __device__ __forceinline__ double shfl_xor_double(double v, int off)
                             __shfl_xor_sync(0xffffffffu, __double2loint(v), off));
 }
 
+// Sum of v over the block, in a fixed order; valid in the first warp. 64-bit
+// additions run at two a cycle and SM, so the block's values go through shared
+// memory to one warp (13 instructions) and not through every warp's shuffles.
 __device__ __forceinline__ double block_sum_double(double v, double* red)
 {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += shfl_xor_double(v, off);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane == 0) red[warp] = v;
+    red[threadIdx.x] = v;
     __syncthreads();
-    double s = lane < kClipThreads / 32 ? red[lane] : 0.0;
+    if (threadIdx.x >= 32) return 0.0;
+    double s = red[threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kClipThreads / 32; ++w) s += red[threadIdx.x + 32 * w];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += shfl_xor_double(s, off);
     return s;
@@ -210,7 +213,7 @@ template <int CAP>
 __global__ void __launch_bounds__(kClipThreads, 4)
 norm_kernel(const __grid_constant__ Table<CAP> t, double* __restrict__ part)
 {
-    __shared__ double red[kClipThreads / 32];
+    __shared__ double red[kClipThreads];
     ptx::griddep_launch_dependents();
     double s = 0.0;
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
@@ -222,21 +225,37 @@ norm_kernel(const __grid_constant__ Table<CAP> t, double* __restrict__ part)
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// sqrt of the parts' sum: every block adds them in the same order.
-__device__ __forceinline__ double total_norm(const double* part, int nparts, double* red)
+// sqrt(s) in fp32 for any s >= 0 in 64 bits: s = m 4^e with m in [1, 4), the
+// root of m taken in fp32 (64-bit roots and quotients cost microseconds here).
+__device__ __forceinline__ float root(double s)
 {
+    const int hi = __double2hiint(s), lo = __double2loint(s);
+    if (!(s > 0.0) || hi >= 0x7FF00000) return (float)s;             // zero, infinite or NaN
+    if (hi < 0x00100000) return 0.f;                                // below 2^-1022: its root is below fp32's range
+    const int e = ((hi >> 20) - 1023) >> 1;                         // floor
+    const double m = __hiloint2double(hi - (e << 21), lo);
+    return ldexpf(__fsqrt_rn((float)m), e);
+}
+
+// The norm from the parts' sum; every block adds them in the same order.
+__device__ __forceinline__ float total_norm(const double* part, int nparts, double* red)
+{
+    __shared__ float norm;
     double s = 0.0;
     for (int i = threadIdx.x; i < nparts; i += kClipThreads) s += __ldcg(part + i);
-    return sqrt(block_sum_double(s, red));
+    s = block_sum_double(s, red);
+    if (threadIdx.x == 0) norm = root(s);
+    __syncthreads();
+    return norm;
 }
 
 __global__ void __launch_bounds__(kClipThreads)
 norm_finish_kernel(const double* __restrict__ part, int nparts, float* __restrict__ norm)
 {
-    __shared__ double red[kClipThreads / 32];
+    __shared__ double red[kClipThreads];
     ptx::griddep_wait();
-    const double n = total_norm(part, nparts, red);
-    if (threadIdx.x == 0) *norm = (float)n;
+    const float n = total_norm(part, nparts, red);
+    if (threadIdx.x == 0) *norm = n;
 }
 
 // The bits of value i of a piece.
@@ -291,12 +310,12 @@ __global__ void __launch_bounds__(kClipThreads, 4)
 clip_kernel(const __grid_constant__ Table<CAP> t, const double* __restrict__ part, int nparts, float max_norm,
             float* __restrict__ norm)
 {
-    __shared__ double red[kClipThreads / 32];
+    __shared__ double red[kClipThreads];
     ptx::griddep_wait();
-    const double n = total_norm(part, nparts, red);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = (float)n;
-    const bool clip = n > (double)max_norm && n - n == 0.0;
-    const float f = clip ? (float)((double)max_norm / n) : 1.f;
+    const float n = total_norm(part, nparts, red);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = n;
+    const bool clip = n > max_norm && n - n == 0.f;
+    const float f = clip ? __fdiv_rn(max_norm, n) : 1.f;
     for (int c = t.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
         const Entry& e = t.e[find_entry(t, c)];
         if (!e.out || (!clip && e.out == e.g)) continue;

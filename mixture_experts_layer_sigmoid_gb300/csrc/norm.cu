@@ -415,21 +415,19 @@ norm_bwd_kernel(BwdArgs<T> a)
     float* part = a.part + (size_t)blockIdx.x * a.H;
     if constexpr (GROUP == 32) {
         // the warps' sums, added in warp order
-        float* sum = reinterpret_cast<float*>(ring);         // GROUP * N * V floats
-        for (int k = 0; k < GROUPS; ++k) {
-            __syncthreads();
-            if (warp == k) {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        float* p = sum + (tid + i * GROUP) * V + j;
-                        *p = k == 0 ? dw[i][j] : *p + dw[i][j];
-                    }
-            }
-        }
+        constexpr int W = GROUP * N * V;
+        static_assert(GROUPS * W * 4 <= R::kBytes, "the sums fit the ring");
+        float* sum = reinterpret_cast<float*>(ring);
         __syncthreads();
-        for (int c = threadIdx.x; c < a.H; c += NT) part[c] = sum[c];
+#pragma unroll
+        for (int i = 0; i < N; ++i) store_f32<V>(sum + warp * W + (tid + i * GROUP) * V, dw[i]);
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.H; c += NT) {
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) t += sum[k * W + c];
+            part[c] = t;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -519,6 +517,10 @@ moe_status_t fwd(int rows, int H, int quant, float eps, const moe_norm_fwd_args_
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Whether the backward gives a row to a warp: narrow rows, and enough of them
+// that every warp has one (else the block's threads share the row's chain).
+bool warp_rows(int rows, int H) { return H <= 256 || (H <= 1024 && rows >= 8 * kNormParts); }
+
 template <typename T, int V, int N, int GROUP, int NT>
 void launch_ring(const BwdArgs<T>& a, int parts, cudaStream_t s)
 {
@@ -534,7 +536,7 @@ void launch_bwd_width(const BwdArgs<T>& a, int parts, cudaStream_t s)
     if constexpr (V * sizeof(T) >= 4) {
         constexpr int P = 32 / V;            // pieces of 32 values
         if (a.H <= 256) return launch_ring<T, V, P / 4, 32, 256>(a, parts, s);
-        if (a.H <= 1024) return launch_ring<T, V, P, 32, 256>(a, parts, s);
+        if (warp_rows(a.rows, a.H)) return launch_ring<T, V, P, 32, 256>(a, parts, s);
         if (a.H <= 2048) return launch_ring<T, V, P / 4, 256, 256>(a, parts, s);
         if (a.H <= 4096) return launch_ring<T, V, P / 2, 256, 256>(a, parts, s);
         if (a.H <= 8192 && sizeof(T) == 2) return launch_ring<T, V, P, 256, 256>(a, parts, s);
@@ -558,8 +560,7 @@ moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cud
     st[n++] = g.lddx;
     const int bytes = access_bytes(H, (int)sizeof(T), st, n);
     // a block of the warp-a-row kernel takes eight rows at a time
-    const bool warps = H <= 1024 && bytes >= 4;
-    const int parts = norm_parts(warps ? (rows + 7) / 8 : rows);
+    const int parts = norm_parts(warp_rows(rows, H) && bytes >= 4 ? (rows + 7) / 8 : rows);
     if (rows > 0) {
         if (bytes == 16) launch_bwd_width<T, 16 / (int)sizeof(T)>(a, parts, s);
         else if (bytes == 4) launch_bwd_width<T, 4 / (int)sizeof(T)>(a, parts, s);

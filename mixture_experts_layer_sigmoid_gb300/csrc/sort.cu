@@ -233,15 +233,11 @@ __device__ __forceinline__ void zero_padding(const IndexArgs& ix, T* buf, long l
     }
 }
 
-// Rows of token t's slots j0 .. j0 + KM - 1 (-1: dropped, or past k).
-template <int KM>
-__device__ __forceinline__ void slot_rows(const IndexArgs& ix, int t, int j0, long long (&row)[KM])
+// Row of slot j of token t, -1 if dropped or past k.
+__device__ __forceinline__ int slot_row(const IndexArgs& ix, int t, int j)
 {
-#pragma unroll
-    for (int j = 0; j < KM; ++j) {
-        const int r = j0 + j < ix.k ? ix.row_of[(size_t)t * ix.k + j0 + j] : -1;
-        row[j] = r < ix.rows ? r : -1;
-    }
+    const int r = j < ix.k ? ix.row_of[(size_t)t * ix.k + j] : -1;
+    return r < ix.rows ? r : -1;
 }
 
 // Blocks [0, T): token t's row to its k rows. Blocks from T on: padding rows.
@@ -255,8 +251,9 @@ sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __rest
     }
     const int t = blockIdx.x;
     for (int j0 = 0; j0 < ix.k; j0 += KM) {
-        long long row[KM];
-        slot_rows<KM>(ix, t, j0, row);
+        int row[KM];
+#pragma unroll
+        for (int j = 0; j < KM; ++j) row[j] = slot_row(ix, t, j0 + j);
         for (int c = (blockIdx.y * kMoveThreads + threadIdx.x) * V; c < ix.H; c += gridDim.y * kMoveThreads * V) {
             const Raw<T, V> q = load_raw<T, V>(x + (size_t)t * ldx + c);
 #pragma unroll
@@ -264,13 +261,6 @@ sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __rest
                 if (row[j] >= 0) store_raw<T, V>(Xp + row[j] * ldp + c, q);
         }
     }
-}
-
-// Row of slot j of token t, -1 if dropped or past k.
-__device__ __forceinline__ int slot_row(const IndexArgs& ix, int t, int j)
-{
-    const int r = j < ix.k ? ix.row_of[(size_t)t * ix.k + j] : -1;
-    return r < ix.rows ? r : -1;
 }
 
 // y[t] = residual[t] + sum over the slots in order of g Yp[row]. WHOLE: k <= KM,
@@ -320,7 +310,7 @@ unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const 
 // Blocks [0, T): dYp[row_j] = g_j dY[t] and dg_j = <dY[t], Yp[row_j]>.
 // Blocks from T on: padding rows.
 template <typename T, int V, int KM, int NT, bool DG>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, NT == kMoveThreads ? 6 : 1)
 unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const T* Yp, long long ldp,
                   const float* __restrict__ gates, T* dYp, long long ldd, float* __restrict__ dgates)
 {
@@ -331,11 +321,11 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
     __shared__ float red[NT / 32][KM];
     const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int j0 = 0; j0 < ix.k; j0 += KM) {
-        long long row[KM];
+        int row[KM];
         float g[KM], dot[KM];
-        slot_rows<KM>(ix, t, j0, row);
 #pragma unroll
         for (int j = 0; j < KM; ++j) {
+            row[j] = slot_row(ix, t, j0 + j);
             g[j] = gates && j0 + j < ix.k ? gates[(size_t)t * ix.k + j0 + j] : 1.f;
             dot[j] = 0.f;
         }
