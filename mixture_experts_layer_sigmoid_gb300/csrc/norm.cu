@@ -39,6 +39,54 @@ __device__ __forceinline__ float block_sum(float v, float* red)
     return s;
 }
 
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+// 16 bytes of which the first n come from src, the rest zeros
+__device__ __forceinline__ void copy_async_part(void* dst, const void* src, int n)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+
+// Rows staged whole in shared memory, for rows that are too wide for registers
+// or do not start on 16-byte boundaries (WINDOW: the 16-byte windows that cover
+// the row are copied, so any alignment moves in full accesses; values are then
+// taken one at a time at the row's place inside them).
+template <typename T, bool WINDOW>
+struct Staged {
+    static constexpr int V = WINDOW ? 1 : 16 / (int)sizeof(T);
+    // bytes of one staged row
+    __host__ __device__ static int row_bytes(int H) { return (H * (int)sizeof(T) + (WINDOW ? 30 : 0)) / 16 * 16; }
+    static __device__ __forceinline__ int phase(const T* p) { return WINDOW ? (int)(reinterpret_cast<uintptr_t>(p) & 15) : 0; }
+    // this thread's part of the copy of a row (tid of NT threads)
+    template <int NT>
+    static __device__ __forceinline__ void fetch(unsigned char* dst, const T* p, int H, int tid)
+    {
+        const int ph = phase(p);
+        const unsigned char* src = reinterpret_cast<const unsigned char*>(p) - ph;
+        const int bytes = ph + H * (int)sizeof(T);
+        for (int at = tid * 16; at < bytes; at += NT * 16) {
+            if constexpr (WINDOW) copy_async_part(dst + at, src + at, bytes - at < 16 ? bytes - at : 16);
+            else copy_async<16>(dst + at, src + at);
+        }
+    }
+    // values [c, c + V) of the row staged at buf
+    static __device__ __forceinline__ void get(const unsigned char* buf, int phase, int c, float (&v)[V])
+    {
+        unpack<T, V>(*reinterpret_cast<const Raw<T, V>*>(buf + phase + c * (int)sizeof(T)), v);
+    }
+};
+
 template <typename T> struct FwdArgs {
     const T* x; const T* r; const float* w;
     T* h; T* y; float* rstd; uint8_t* codes; void* scales;
@@ -72,8 +120,21 @@ __device__ __forceinline__ void quantise(const float (&v)[V], bool act, int row,
     } else {
         const float t = __fdiv_rn(a, 448.f);
         const float s = t == 0.f ? 1.f : t;              // zero, or too small for a scale
+        if (s >= 0x1p-112f && s < 0x1p100f) {
+            // v / s from the rounded reciprocal and one correction of the product by
+            // its remainder (P. Markstein, IBM J. Res. Dev. 34(1), 1990): within an
+            // ulp of the quotient, nearly always equal to it, where an 8-bit code
+            // only needs 2^-5; a division per value took half of the kernel's time
+            const float r = __frcp_rn(s);
 #pragma unroll
-        for (int i = 0; i < V; ++i) q[i] = __fdiv_rn(v[i], s);
+            for (int i = 0; i < V; ++i) {
+                const float y = v[i] * r;
+                q[i] = fmaf(fmaf(-s, y, v[i]), r, y);
+            }
+        } else {                                         // the remainder could underflow
+#pragma unroll
+            for (int i = 0; i < V; ++i) q[i] = __fdiv_rn(v[i], s);
+        }
         if (c % BLOCK == 0) static_cast<float*>(scales)[(size_t)row * (H / 128) + c / 128] = s;
     }
     uint32_t* out = reinterpret_cast<uint32_t*>(codes + (size_t)row * H + c);
@@ -220,6 +281,83 @@ norm_fwd_kernel(FwdArgs<T> a)
     }
 }
 
+// One row per block at a time, the next rows' x and residual on their way into
+// a ring of S staged rows. Without WINDOW a thread reads back only what it
+// copied itself, so the row's sum is the only barrier.
+constexpr int kWideThreads = 512;
+template <typename T, bool WINDOW, int QUANT, int S>
+__global__ void __launch_bounds__(kWideThreads)
+norm_fwd_ring_kernel(FwdArgs<T> a)
+{
+    using R = Staged<T, WINDOW>;
+    constexpr int V = R::V;
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ float red[2][kWideThreads / 32];
+    const int tid = threadIdx.x;
+    const int rb = R::row_bytes(a.H), sb = a.r ? 2 * rb : rb;
+    auto fetch = [&](int stage, long long row) {
+        if (row < a.rows) {
+            R::template fetch<kWideThreads>(ring + stage * sb, a.x + row * a.ldx, a.H, tid);
+            if (a.r) R::template fetch<kWideThreads>(ring + stage * sb + rb, a.r + row * a.ldr, a.H, tid);
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < S; ++s) fetch(s, (long long)blockIdx.x + (long long)s * gridDim.x);
+    int stage = 0, parity = 0;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        copy_wait<S - 1>();
+        if constexpr (WINDOW) __syncthreads();
+        const unsigned char* bx = ring + stage * sb;
+        const unsigned char* br = bx + rb;
+        const int px = R::phase(a.x + row * a.ldx), pr = a.r ? R::phase(a.r + row * a.ldr) : 0;
+        auto value = [&](int c, float (&v)[V]) {
+            R::get(bx, px, c, v);
+            if (a.r) {
+                float u[V];
+                R::get(br, pr, c, u);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] += u[i];
+            }
+        };
+        float ss = 0.f;
+#pragma unroll 4
+        for (int c = tid * V; c < a.H; c += kWideThreads * V) {
+            float v[V];
+            value(c, v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) ss = fmaf(v[i], v[i], ss);
+        }
+        const float rstd = rsqrtf(block_sum<kWideThreads>(ss, red[parity]) / (float)a.H + a.eps);
+        parity ^= 1;
+        if (tid == 0 && a.rstd) a.rstd[row] = rstd;
+#pragma unroll 4
+        for (int c0 = 0; c0 < a.H; c0 += kWideThreads * V) {
+            const int c = c0 + tid * V;
+            const bool act = c < a.H;
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = 0.f;
+            if (act) {
+                float w[V];
+                value(c, v);
+                if (a.h) store_vec<T, V>(a.h + row * a.ldh + c, v);
+                load_f32<V>(a.w + c, w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = v[i] * rstd * w[i];
+                if (a.y) store_vec<T, V>(a.y + row * a.ldy + c, v);
+            }
+            if constexpr (QUANT != MOE_NORM_PLAIN) quantise<QUANT, V>(v, act, (int)row, c, a.H, a.codes, a.scales);
+        }
+        if constexpr (WINDOW) __syncthreads();          // the stage is read
+        fetch(stage, row + (long long)S * gridDim.x);
+        stage = stage + 1 == S ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+    if constexpr (QUANT == MOE_NORM_MXFP8)
+        for (long long row = (long long)a.rows + blockIdx.x; row < ((long long)a.rows + 127) / 128 * 128; row += gridDim.x)
+            zero_scale_row<kWideThreads>(static_cast<uint8_t*>(a.scales), row, a.rows, tid, a.H);
+}
+
 template <typename T> struct BwdArgs {
     const T* dy; const T* h; const float* rstd; const float* w; const T* dh;
     T* dx; float* part;   // part: gridDim.x x H partial sums of dw, or null
@@ -289,19 +427,6 @@ norm_bwd_loop_kernel(BwdArgs<T> a)
 // S rows per group are in flight while one is worked on. w and the partial sums
 // of dw stay in registers over all rows of the thread.
 // GROUP threads take a row (a warp, or the block); H <= GROUP * N * V.
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src)
-{
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
-
 template <typename T, int V, int N, int GROUP, int NT>
 struct Ring {
     static constexpr int kPiece = V * (int)sizeof(T);
@@ -437,6 +562,78 @@ norm_bwd_kernel(BwdArgs<T> a)
     }
 }
 
+// The same for rows of any alignment and width, staged whole (as in the
+// forward's ring); dw is summed in shared memory, each column by one thread.
+template <typename T, int S>
+__global__ void __launch_bounds__(kWideThreads)
+norm_bwd_window_kernel(BwdArgs<T> a)
+{
+    using R = Staged<T, true>;
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ float red[2][kWideThreads / 32];
+    const int tid = threadIdx.x;
+    const int rb = R::row_bytes(a.H), sb = (a.dh ? 3 : 2) * rb;
+    float* dw = reinterpret_cast<float*>(ring + S * sb);
+    auto fetch = [&](int stage, long long row) {
+        if (row < a.rows) {
+            unsigned char* to = ring + stage * sb;
+            R::template fetch<kWideThreads>(to, a.dy + row * a.lddy, a.H, tid);
+            R::template fetch<kWideThreads>(to + rb, a.h + row * a.ldh, a.H, tid);
+            if (a.dh) R::template fetch<kWideThreads>(to + 2 * rb, a.dh + row * a.lddh, a.H, tid);
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < S; ++s) fetch(s, (long long)blockIdx.x + (long long)s * gridDim.x);
+    if (a.part)
+        for (int c = tid; c < a.H; c += kWideThreads) dw[c] = 0.f;
+    ptx::griddep_launch_dependents();
+    int stage = 0, parity = 0;
+    float rstd = blockIdx.x < (unsigned)a.rows ? a.rstd[blockIdx.x] : 0.f;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const float next = row + gridDim.x < a.rows ? a.rstd[row + gridDim.x] : 0.f;
+        copy_wait<S - 1>();
+        __syncthreads();
+        const unsigned char* bg = ring + stage * sb;
+        const unsigned char* bh = bg + rb;
+        const unsigned char* bd = bh + rb;
+        const int pg = R::phase(a.dy + row * a.lddy), ph = R::phase(a.h + row * a.ldh);
+        const int pd = a.dh ? R::phase(a.dh + row * a.lddh) : 0;
+        float d = 0.f;
+#pragma unroll 4
+        for (int c = tid; c < a.H; c += kWideThreads) {
+            float g[1], v[1];
+            R::get(bg, pg, c, g);
+            R::get(bh, ph, c, v);
+            d = fmaf(g[0] * a.w[c], v[0], d);
+        }
+        const float m = block_sum<kWideThreads>(d, red[parity]) * rstd / (float)a.H;
+        parity ^= 1;
+        T* dx = a.dx + row * a.lddx;
+#pragma unroll 4
+        for (int c = tid; c < a.H; c += kWideThreads) {
+            float g[1], v[1], o[1];
+            R::get(bg, pg, c, g);
+            R::get(bh, ph, c, v);
+            const float n = v[0] * rstd;
+            o[0] = rstd * fmaf(-n, m, g[0] * a.w[c]);
+            if (a.part) dw[c] = fmaf(g[0], n, dw[c]);
+            if (a.dh) {
+                float u[1];
+                R::get(bd, pd, c, u);
+                o[0] += u[0];
+            }
+            store_vec<T, 1>(dx + c, o);
+        }
+        __syncthreads();                                  // the stage is read
+        fetch(stage, row + (long long)S * gridDim.x);
+        stage = stage + 1 == S ? 0 : stage + 1;
+        rstd = next;
+    }
+    copy_wait<0>();
+    if (a.part)
+        for (int c = tid; c < a.H; c += kWideThreads) a.part[(size_t)blockIdx.x * a.H + c] = dw[c];
+}
+
 // dw[c] = sum of the parts: ascending order within each of 32 phases, the
 // phases then added in order. Launched ahead of the parts' kernel's end.
 constexpr int kPhases = 32;
@@ -462,24 +659,49 @@ norm_dweight_kernel(const float* __restrict__ part, int nparts, int H, float* __
 
 int norm_parts(int rows) { return rows < kNormParts ? rows : kNormParts; }
 
+// Shared memory that leaves room for a second block on the SM, and for one.
+constexpr int kSmemTwo = 108 * 1024, kSmemOne = 220 * 1024;
+
+template <typename K, typename A>
+void launch_staged(K kernel, const A& a, int smem, cudaStream_t s)
+{
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+    const int blocks = smem <= kSmemTwo ? kNormParts : kNormParts / 2;
+    kernel<<<a.rows < blocks ? a.rows : blocks, kWideThreads, smem, s>>>(a);
+}
+
+// The forward's ring; false if two stages of a row do not fit.
+template <typename T, bool WINDOW, int QUANT>
+bool launch_fwd_ring(const FwdArgs<T>& a, cudaStream_t s)
+{
+    const int stage = Staged<T, WINDOW>::row_bytes(a.H) * (a.r ? 2 : 1);
+    if (4 * stage <= kSmemTwo) launch_staged(norm_fwd_ring_kernel<T, WINDOW, QUANT, 4>, a, 4 * stage, s);
+    else if (2 * stage <= kSmemOne) launch_staged(norm_fwd_ring_kernel<T, WINDOW, QUANT, 2>, a, 2 * stage, s);
+    else return false;
+    return true;
+}
+
 template <typename T, int V, int QUANT>
 void launch_fwd_width(const FwdArgs<T>& a, cudaStream_t s)
 {
     constexpr int P = 32 / V;                // pieces of 32 values
+    constexpr bool WHOLE = V * sizeof(T) == 16, ODD = V * sizeof(T) == 2;
     const int rows = QUANT == MOE_NORM_MXFP8 ? (a.rows + 127) / 128 * 128 : a.rows;
     const int warps = (rows + kNormThreads / 32 - 1) / (kNormThreads / 32);
-    if (a.H <= 256) norm_fwd_kernel<T, V, P / 4, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
-    else if (a.H <= 1024) norm_fwd_kernel<T, V, P, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
-    else if (a.rows <= kFewRows && a.H <= 8192) {
-        // few rows: a thread per eight values shortens each row's own chain
-        if (a.H <= 4096) norm_fwd_kernel<T, V, P / 4, 512, QUANT, true><<<rows, 512, 0, s>>>(a);
-        else norm_fwd_kernel<T, V, P / 4, 1024, QUANT, true><<<rows, 1024, 0, s>>>(a);
+    if (a.H <= 256) return norm_fwd_kernel<T, V, P / 4, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
+    if (a.H <= 512) return norm_fwd_kernel<T, V, P / 2, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
+    if (a.H <= 1024) return norm_fwd_kernel<T, V, P / 4, 128, QUANT><<<rows, 128, 0, s>>>(a);
+    if (a.rows <= kFewRows && a.H <= 4096) return norm_fwd_kernel<T, V, P / 4, 512, QUANT, true><<<rows, 512, 0, s>>>(a);
+    if (a.rows <= kFewRows && a.H <= 8192) return norm_fwd_kernel<T, V, P / 4, 1024, QUANT, true><<<rows, 1024, 0, s>>>(a);
+    if constexpr (!ODD) {                    // single 2-byte values are staged from here on
+        if (a.H <= 2048) return norm_fwd_kernel<T, V, P / 4, 256, QUANT><<<rows, 256, 0, s>>>(a);
+        if (a.H <= 4096) return norm_fwd_kernel<T, V, P / 2, 256, QUANT><<<rows, 256, 0, s>>>(a);
+        if (a.H <= 8192) {
+            if constexpr (sizeof(T) == 2) return norm_fwd_kernel<T, V, P, 256, QUANT><<<rows, 256, 0, s>>>(a);
+            else return norm_fwd_kernel<T, V, P / 2, 512, QUANT><<<rows, 512, 0, s>>>(a);
+        }
     }
-    else if (a.H <= 2048) norm_fwd_kernel<T, V, P / 4, 256, QUANT><<<rows, 256, 0, s>>>(a);
-    else if (a.H <= 4096) norm_fwd_kernel<T, V, P / 2, 256, QUANT><<<rows, 256, 0, s>>>(a);
-    else if (a.H <= 8192) norm_fwd_kernel<T, V, P, 256, QUANT><<<rows, 256, 0, s>>>(a);
-    else if (a.H <= 16384) norm_fwd_kernel<T, V, P, 512, QUANT><<<rows, 512, 0, s>>>(a);
-    else norm_fwd_loop_kernel<T, V, QUANT><<<rows, kNormThreads, 0, s>>>(a);
+    if (!launch_fwd_ring<T, !WHOLE, QUANT>(a, s)) norm_fwd_loop_kernel<T, V, QUANT><<<rows, kNormThreads, 0, s>>>(a);
 }
 
 template <typename T, int QUANT>
@@ -489,7 +711,8 @@ cudaError_t launch_fwd(const FwdArgs<T>& a, int bytes, cudaStream_t s)
     if (bytes == 16) launch_fwd_width<T, V16, QUANT>(a, s);
     if constexpr (QUANT == MOE_NORM_PLAIN) {
         if (bytes == 4) launch_fwd_width<T, 4 / (int)sizeof(T), QUANT>(a, s);
-        else if (bytes == 2) launch_fwd_width<T, 1, QUANT>(a, s);
+        if constexpr (sizeof(T) == 2)
+            if (bytes == 2) launch_fwd_width<T, 1, QUANT>(a, s);
     }
     count_launches();
     return cudaGetLastError();
@@ -543,6 +766,16 @@ void launch_bwd_width(const BwdArgs<T>& a, int parts, cudaStream_t s)
         if (a.H <= 8192 || (a.H <= 16384 && sizeof(T) == 2))
             return launch_ring<T, V, sizeof(T) == 2 ? P : P / 2, 512, 512>(a, parts, s);
     }
+    // any alignment, as far as two stages and dw fit shared memory
+    if constexpr (V * sizeof(T) < 16) {
+        const int smem = 2 * Staged<T, true>::row_bytes(a.H) * (a.dh ? 3 : 2) + a.H * (int)sizeof(float);
+        if (smem <= kSmemOne) {
+            auto kernel = norm_bwd_window_kernel<T, 2>;
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+            kernel<<<parts, kWideThreads, smem, s>>>(a);
+            return;
+        }
+    }
     norm_bwd_loop_kernel<T, V><<<parts, kNormThreads, 0, s>>>(a);
 }
 
@@ -564,7 +797,7 @@ moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cud
     if (rows > 0) {
         if (bytes == 16) launch_bwd_width<T, 16 / (int)sizeof(T)>(a, parts, s);
         else if (bytes == 4) launch_bwd_width<T, 4 / (int)sizeof(T)>(a, parts, s);
-        else launch_bwd_width<T, 1>(a, parts, s);
+        else if constexpr (sizeof(T) == 2) launch_bwd_width<T, 1>(a, parts, s);
         count_launches();
     }
     if (g.dweight) {

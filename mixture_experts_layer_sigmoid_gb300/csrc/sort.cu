@@ -206,6 +206,8 @@ cudaError_t launch_index(int n, int E, int align, const int32_t* topk, int32_t* 
 
 // ------------------------------------------------------------------ rows
 constexpr int kMoveThreads = 128;
+// A row of at most two pieces per lane goes to a warp, four tokens to a block.
+constexpr int kNarrowPieces = 2;
 // Up to this many tokens a block per token leaves SMs idle: rows are then cut
 // into column parts (or, for the gradient's dot products, blocks are larger).
 constexpr int kFewTokens = 1216;
@@ -240,21 +242,28 @@ __device__ __forceinline__ int slot_row(const IndexArgs& ix, int t, int j)
     return r < ix.rows ? r : -1;
 }
 
-// Blocks [0, T): token t's row to its k rows. Blocks from T on: padding rows.
-template <typename T, int V, int KM>
+// Blocks of the tokens with GROUP threads a token.
+template <int GROUP>
+__host__ __device__ constexpr int token_blocks(int T) { return (T + kMoveThreads / GROUP - 1) / (kMoveThreads / GROUP); }
+
+// The first blocks: a token's row to its k rows, GROUP threads a token. The
+// blocks after them: padding rows.
+template <typename T, int V, int KM, int GROUP>
 __global__ void __launch_bounds__(kMoveThreads)
 sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __restrict__ Xp, long long ldp)
 {
-    if (blockIdx.x >= (unsigned)ix.T) {
-        zero_padding<T, V>(ix, Xp, ldp, (long long)(blockIdx.x - ix.T) * kPadRows);
+    if (blockIdx.x >= (unsigned)token_blocks<GROUP>(ix.T)) {
+        zero_padding<T, V>(ix, Xp, ldp, (long long)(blockIdx.x - token_blocks<GROUP>(ix.T)) * kPadRows);
         return;
     }
-    const int t = blockIdx.x;
+    const int t = GROUP == 32 ? blockIdx.x * (kMoveThreads / 32) + threadIdx.x / 32 : blockIdx.x;
+    const int tid = threadIdx.x % GROUP;
+    if (t >= ix.T) return;
     for (int j0 = 0; j0 < ix.k; j0 += KM) {
         int row[KM];
 #pragma unroll
         for (int j = 0; j < KM; ++j) row[j] = slot_row(ix, t, j0 + j);
-        for (int c = (blockIdx.y * kMoveThreads + threadIdx.x) * V; c < ix.H; c += gridDim.y * kMoveThreads * V) {
+        for (int c = (blockIdx.y * GROUP + tid) * V; c < ix.H; c += gridDim.y * GROUP * V) {
             const Raw<T, V> q = load_raw<T, V>(x + (size_t)t * ldx + c);
 #pragma unroll
             for (int j = 0; j < KM; ++j)
@@ -265,12 +274,14 @@ sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __rest
 
 // y[t] = residual[t] + sum over the slots in order of g Yp[row]. WHOLE: k <= KM,
 // the index is read once per token.
-template <typename T, int V, int KM, bool WHOLE>
+template <typename T, int V, int KM, bool WHOLE, int GROUP>
 __global__ void __launch_bounds__(kMoveThreads)
 unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const float* __restrict__ gates,
                    const T* residual, long long ldr, T* y, long long ldy)
 {
-    const int t = blockIdx.x;
+    const int t = GROUP == 32 ? blockIdx.x * (kMoveThreads / 32) + threadIdx.x / 32 : blockIdx.x;
+    const int tid = threadIdx.x % GROUP;
+    if (t >= ix.T) return;
     int row[KM];
     float g[KM];
     auto index = [&](int j0) {
@@ -281,7 +292,7 @@ unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const 
         }
     };
     if (WHOLE) index(0);
-    for (int c = (blockIdx.y * kMoveThreads + threadIdx.x) * V; c < ix.H; c += gridDim.y * kMoveThreads * V) {
+    for (int c = (blockIdx.y * GROUP + tid) * V; c < ix.H; c += gridDim.y * GROUP * V) {
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
@@ -307,19 +318,23 @@ unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const 
     }
 }
 
-// Blocks [0, T): dYp[row_j] = g_j dY[t] and dg_j = <dY[t], Yp[row_j]>.
-// Blocks from T on: padding rows.
-template <typename T, int V, int KM, int NT, bool DG>
+// The first blocks: dYp[row_j] = g_j dY[t] and dg_j = <dY[t], Yp[row_j]>, GROUP
+// (a warp, or NT) threads a token. The blocks after them: padding rows.
+template <typename T, int V, int KM, int NT, int GROUP, bool DG>
 __global__ void __launch_bounds__(NT, NT == kMoveThreads ? 6 : 1)
 unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const T* Yp, long long ldp,
                   const float* __restrict__ gates, T* dYp, long long ldd, float* __restrict__ dgates)
 {
-    if (blockIdx.x >= (unsigned)ix.T) {
-        zero_padding<T, V>(ix, dYp, ldd, (long long)(blockIdx.x - ix.T) * kPadRows);
+    constexpr int TOKENS = NT / GROUP;       // of a block
+    const int tb = (ix.T + TOKENS - 1) / TOKENS;
+    if (blockIdx.x >= (unsigned)tb) {
+        zero_padding<T, V>(ix, dYp, ldd, (long long)(blockIdx.x - tb) * kPadRows);
         return;
     }
     __shared__ float red[NT / 32][KM];
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x % GROUP;
+    const int t = blockIdx.x * TOKENS + threadIdx.x / GROUP;
+    if (t >= ix.T) return;                   // a block, or whole warps that meet no barrier
     for (int j0 = 0; j0 < ix.k; j0 += KM) {
         int row[KM];
         float g[KM], dot[KM];
@@ -329,7 +344,7 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
             g[j] = gates && j0 + j < ix.k ? gates[(size_t)t * ix.k + j0 + j] : 1.f;
             dot[j] = 0.f;
         }
-        for (int c = threadIdx.x * V; c < ix.H; c += NT * V) {
+        for (int c = tid * V; c < ix.H; c += GROUP * V) {
             float d[V];
             load_vec<T, V>(dY + (size_t)t * lddy + c, d);
             // four rows' loads at a time: with all eight in flight fewer blocks fit,
@@ -360,20 +375,23 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
             }
         }
         if constexpr (DG) {
-            __syncthreads();                 // red of the previous slots is read
+            if constexpr (GROUP != 32) __syncthreads();      // red of the previous slots is read
 #pragma unroll
             for (int j = 0; j < KM; ++j) {
                 float s = dot[j];
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-                if (lane == 0) red[warp][j] = s;
+                if (GROUP != 32 && lane == 0) red[warp][j] = s;
+                if (GROUP == 32 && lane == 0 && j0 + j < ix.k) dgates[(size_t)t * ix.k + j0 + j] = s;
             }
-            __syncthreads();
-            if (threadIdx.x < KM && j0 + (int)threadIdx.x < ix.k) {
-                float s = 0.f;
+            if constexpr (GROUP != 32) {
+                __syncthreads();
+                if (threadIdx.x < KM && j0 + (int)threadIdx.x < ix.k) {
+                    float s = 0.f;
 #pragma unroll
-                for (int w = 0; w < NT / 32; ++w) s += red[w][threadIdx.x];
-                dgates[(size_t)t * ix.k + j0 + threadIdx.x] = s;
+                    for (int w = 0; w < NT / 32; ++w) s += red[w][threadIdx.x];
+                    dgates[(size_t)t * ix.k + j0 + threadIdx.x] = s;
+                }
             }
         }
     }
@@ -394,18 +412,27 @@ template <typename T, typename F>
 void with_width(int bytes, F&& f)
 {
     if (bytes == 16) f(std::integral_constant<int, 16 / (int)sizeof(T)>{});
+    else if (bytes == 8) f(std::integral_constant<int, 8 / (int)sizeof(T)>{});
     else if (bytes == 4) f(std::integral_constant<int, 4 / (int)sizeof(T)>{});
-    else f(std::integral_constant<int, 1>{});
+    else if constexpr (sizeof(T) == 2) f(std::integral_constant<int, 1>{});
 }
 
 IndexArgs index_args(const moe_sorted_t& s)
 {
     return IndexArgs{s.T, s.k, s.H, s.rows, s.row_of, s.slot_of, s.in_use};
 }
-unsigned move_grid(const moe_sorted_t& s)
+// Blocks of a launch with GROUP threads a token, padding included.
+unsigned move_grid(const moe_sorted_t& s, int token_blocks)
 {
-    return (unsigned)(s.T + (s.slot_of ? (s.rows + kPadRows - 1) / kPadRows : 0));
+    return (unsigned)(token_blocks + (s.slot_of ? (s.rows + kPadRows - 1) / kPadRows : 0));
 }
+// Whether a token's row goes to a warp: few pieces, and enough tokens that the
+// larger blocks are not needed to fill the SMs.
+bool narrow(const moe_sorted_t& s, int V) { return s.H <= 32 * V * kNarrowPieces && s.T >= kFewTokens; }
+
+using One = std::integral_constant<int, 32>;
+using Block = std::integral_constant<int, kMoveThreads>;
+
 // Column parts of a launch whose blocks take V values per thread at a time.
 unsigned column_parts(const moe_sorted_t& s, int V)
 {
@@ -418,11 +445,17 @@ template <typename T>
 void sort_rows(const moe_sorted_t& ix, const void* x, long long ldx, void* Xp, long long ldp, cudaStream_t s)
 {
     const long long st[] = {ldx, ldp};
-    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, 2), [&](auto v) {
+    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, 2, true), [&](auto v) {
         with_slots(ix.k, [&](auto km) {
             constexpr int V = decltype(v)::value;
-            sort_rows_kernel<T, V, decltype(km)::value><<<dim3(move_grid(ix), column_parts(ix, V)), kMoveThreads, 0, s>>>(
-                index_args(ix), static_cast<const T*>(x), ldx, static_cast<T*>(Xp), ldp);
+            auto launch = [&](auto group) {
+                constexpr int G = decltype(group)::value;
+                sort_rows_kernel<T, V, decltype(km)::value, G>
+                    <<<dim3(move_grid(ix, token_blocks<G>(ix.T)), column_parts(ix, V)), kMoveThreads, 0, s>>>(
+                        index_args(ix), static_cast<const T*>(x), ldx, static_cast<T*>(Xp), ldp);
+            };
+            if (narrow(ix, V)) launch(One{});
+            else launch(Block{});
         });
     });
 }
@@ -432,18 +465,23 @@ void unsort_rows(const moe_sorted_t& ix, const void* Yp, long long ldp, const fl
                  long long ldr, void* y, long long ldy, cudaStream_t s)
 {
     const long long st[] = {ldp, ldy, ldr};
-    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, residual ? 3 : 2), [&](auto v) {
+    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, residual ? 3 : 2, true), [&](auto v) {
         with_slots(ix.k, [&](auto km) {
-            constexpr int V = decltype(v)::value;
-            constexpr int KM = decltype(km)::value;
-            auto launch = [&](auto whole) {
-                unsort_rows_kernel<T, V, KM, decltype(whole)::value>
-                    <<<dim3(ix.T, column_parts(ix, V)), kMoveThreads, 0, s>>>(
+            constexpr int V = decltype(v)::value, KM = decltype(km)::value;
+            auto launch = [&](auto whole, auto group) {
+                constexpr int G = decltype(group)::value;
+                unsort_rows_kernel<T, V, KM, decltype(whole)::value, G>
+                    <<<dim3(token_blocks<G>(ix.T), column_parts(ix, V)), kMoveThreads, 0, s>>>(
                         index_args(ix), static_cast<const T*>(Yp), ldp, gates, static_cast<const T*>(residual), ldr,
                         static_cast<T*>(y), ldy);
             };
-            if (ix.k <= KM) launch(std::true_type{});
-            else if constexpr (KM == kMaxSlots) launch(std::false_type{});
+            if (ix.k > KM) {
+                if constexpr (KM == kMaxSlots) launch(std::false_type{}, Block{});
+            } else if (narrow(ix, V)) {
+                launch(std::true_type{}, One{});
+            } else {
+                launch(std::true_type{}, Block{});
+            }
         });
     });
 }
@@ -453,20 +491,21 @@ void unsort_bwd(const moe_sorted_t& ix, const void* dY, long long lddy, const vo
                 const float* gates, void* dYp, long long ldd, float* dgates, cudaStream_t s)
 {
     const long long st[] = {lddy, ldd, ldp};
-    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, dgates ? 3 : 2), [&](auto v) {
+    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, dgates ? 3 : 2, true), [&](auto v) {
         with_slots(ix.k, [&](auto km) {
             constexpr int V = decltype(v)::value, KM = decltype(km)::value;
-            const T* d = static_cast<const T*>(dY);
-            const T* y = static_cast<const T*>(Yp);
-            T* o = static_cast<T*>(dYp);
-            auto launch = [&](auto nt, auto dg) {
-                constexpr int NT = decltype(nt)::value;
-                unsort_bwd_kernel<T, V, KM, NT, decltype(dg)::value><<<move_grid(ix), NT, 0, s>>>(
-                    index_args(ix), d, lddy, y, ldp, gates, o, ldd, dgates);
+            auto launch = [&](auto nt, auto group, auto dg) {
+                constexpr int NT = decltype(nt)::value, G = decltype(group)::value;
+                unsort_bwd_kernel<T, V, KM, NT, G, decltype(dg)::value>
+                    <<<move_grid(ix, (ix.T + NT / G - 1) / (NT / G)), NT, 0, s>>>(
+                        index_args(ix), static_cast<const T*>(dY), lddy, static_cast<const T*>(Yp), ldp, gates,
+                        static_cast<T*>(dYp), ldd, dgates);
             };
-            if (!dgates) launch(std::integral_constant<int, kMoveThreads>{}, std::false_type{});
-            else if (ix.T < kFewTokens / 2) launch(std::integral_constant<int, 512>{}, std::true_type{});
-            else launch(std::integral_constant<int, kMoveThreads>{}, std::true_type{});
+            using Large = std::integral_constant<int, 512>;
+            if (!dgates) launch(Block{}, Block{}, std::false_type{});
+            else if (narrow(ix, V)) launch(Block{}, One{}, std::true_type{});
+            else if (ix.T < kFewTokens / 2) launch(Large{}, Large{}, std::true_type{});
+            else launch(Block{}, Block{}, std::true_type{});
         });
     });
 }
@@ -541,7 +580,7 @@ moe_status_t moe_sort_rows(const moe_sorted_t* index, const void* x, long long l
     if (ix.T > 0 && !x) return MOE_ERR_INVALID_ARG;
     if ((ix.rows > 0 && !Xp) || ldx < ix.H || ldp < ix.H) return MOE_ERR_INVALID_ARG;
     if (!is_aligned16(x) || !is_aligned16(Xp)) return MOE_ERR_MISALIGNED;
-    if (move_grid(ix) == 0 || ix.rows == 0) return MOE_OK;
+    if (ix.rows == 0 || (ix.T == 0 && !ix.slot_of)) return MOE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (ix.dtype == MOE_FP32) sort_rows<float>(ix, x, ldx, Xp, ldp, s);
     else sort_rows<__nv_bfloat16>(ix, x, ldx, Xp, ldp, s);
@@ -580,7 +619,7 @@ moe_status_t moe_unsort_rows_backward(const moe_sorted_t* index, const void* dY,
     const void* ptrs[] = {dY, Yp, gates, dYp, dgates};
     for (const void* p : ptrs)
         if (!is_aligned16(p)) return MOE_ERR_MISALIGNED;
-    if (move_grid(ix) == 0) return MOE_OK;
+    if (ix.T == 0 && (ix.rows == 0 || !ix.slot_of)) return MOE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (ix.dtype == MOE_FP32) unsort_bwd<float>(ix, dY, lddy, Yp, ldp, gates, dYp, ldd, dgates, s);
     else unsort_bwd<__nv_bfloat16>(ix, dY, lddy, Yp, ldp, gates, dYp, ldd, dgates, s);
