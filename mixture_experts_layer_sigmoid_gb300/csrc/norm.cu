@@ -22,8 +22,9 @@ constexpr int kNormParts = 304;
 // Up to one row per SM the forward gives a row more threads.
 constexpr int kFewRows = 152;
 
-// Sum of v over the block's NT threads, the same order on every call; `red`
-// holds NT / 32 floats and may be reused after the next __syncthreads.
+// Sum of v over the block's threads (at most NT; NT = 32: the warp's), the same
+// order on every call; `red` holds NT / 32 floats and may be reused after the
+// next __syncthreads.
 template <int NT>
 __device__ __forceinline__ float block_sum(float v, float* red)
 {
@@ -33,7 +34,7 @@ __device__ __forceinline__ float block_sum(float v, float* red)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane == 0) red[warp] = v;
     __syncthreads();
-    float s = lane < NT / 32 ? red[lane] : 0.f;
+    float s = lane < (int)blockDim.x / 32 ? red[lane] : 0.f;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     return s;
@@ -146,11 +147,10 @@ __device__ __forceinline__ void quantise(const float (&v)[V], bool act, int row,
 
 // The scale bytes of a row past the last one in the last 128-row tile (those
 // rows' groups run beside the others).
-template <int GROUP>
-__device__ __forceinline__ void zero_scale_row(uint8_t* scales, long long row, int rows, int tid, int H)
+__device__ __forceinline__ void zero_scale_row(uint8_t* scales, long long row, int rows, int tid, int step, int H)
 {
     if (row >= ((long long)rows + 127) / 128 * 128) return;
-    for (int kb = tid; kb < H / 128; kb += GROUP)
+    for (int kb = tid; kb < H / 128; kb += step)
         *reinterpret_cast<uint32_t*>(scales + ((size_t)(row >> 7) * (H / 128) + kb) * 512 +
                                      atom_byte(row & 127, 0)) = 0u;
 }
@@ -164,7 +164,7 @@ norm_fwd_loop_kernel(FwdArgs<T> a)
     __shared__ float red[kNormThreads / 32];
     const int row = blockIdx.x;
     if (QUANT == MOE_NORM_MXFP8 && row >= a.rows) {
-        zero_scale_row<kNormThreads>(static_cast<uint8_t*>(a.scales), row, a.rows, threadIdx.x, a.H);
+        zero_scale_row(static_cast<uint8_t*>(a.scales), row, a.rows, threadIdx.x, kNormThreads, a.H);
         return;
     }
     const T* x = a.x + (size_t)row * a.ldx;
@@ -206,9 +206,9 @@ norm_fwd_loop_kernel(FwdArgs<T> a)
     }
 }
 
-// One row per group of GROUP threads (a warp, or the block), held in registers
-// between the sum and the output: each value is read once. N pieces of V values
-// per thread cover the row, so H <= GROUP * N * V.
+// One row per group (GROUP = 32: a warp; else the block, of at most GROUP
+// threads), held in registers between the sum and the output: each value is
+// read once. N pieces of V values per thread cover the row.
 // AHEAD fetches the weights with the row, for launches of few rows, whose time
 // is the chain of loads.
 template <typename T, int V, int N, int GROUP, int QUANT, bool AHEAD = false>
@@ -218,10 +218,11 @@ norm_fwd_kernel(FwdArgs<T> a)
     constexpr int NT = GROUP == 32 ? kNormThreads : GROUP;
     __shared__ float red[NT / 32];
     const int tid = GROUP == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const int step = GROUP == 32 ? 32 : blockDim.x;
     const long long row = GROUP == 32 ? (long long)blockIdx.x * (NT / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.rows) {                     // whole groups leave together
         if constexpr (QUANT == MOE_NORM_MXFP8)
-            zero_scale_row<GROUP>(static_cast<uint8_t*>(a.scales), row, a.rows, tid, a.H);
+            zero_scale_row(static_cast<uint8_t*>(a.scales), row, a.rows, tid, step, a.H);
         return;
     }
     const T* x = a.x + row * a.ldx;
@@ -229,7 +230,7 @@ norm_fwd_kernel(FwdArgs<T> a)
     Raw<T, V> qx[N], qr[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (tid + i * GROUP) * V;
+        const int c = (tid + i * step) * V;
         if (c < a.H) {
             qx[i] = load_raw<T, V>(x + c);
             if (r) qr[i] = load_raw<T, V>(r + c);
@@ -239,7 +240,7 @@ norm_fwd_kernel(FwdArgs<T> a)
     if constexpr (AHEAD) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (tid + i * GROUP) * V;
+            const int c = (tid + i * step) * V;
             if (c < a.H) load_f32<V>(a.w + c, wa[i]);
         }
     }
@@ -247,7 +248,7 @@ norm_fwd_kernel(FwdArgs<T> a)
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const bool act = (tid + i * GROUP) * V < a.H;
+        const bool act = (tid + i * step) * V < a.H;
         if (act) {
             unpack<T, V>(qx[i], v[i]);
             if (r) {
@@ -267,7 +268,7 @@ norm_fwd_kernel(FwdArgs<T> a)
     if (tid == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (tid + i * GROUP) * V;
+        const int c = (tid + i * step) * V;
         const bool act = c < a.H;
         if (act) {
             float w[V];
@@ -355,7 +356,7 @@ norm_fwd_ring_kernel(FwdArgs<T> a)
     copy_wait<0>();
     if constexpr (QUANT == MOE_NORM_MXFP8)
         for (long long row = (long long)a.rows + blockIdx.x; row < ((long long)a.rows + 127) / 128 * 128; row += gridDim.x)
-            zero_scale_row<kWideThreads>(static_cast<uint8_t*>(a.scales), row, a.rows, tid, a.H);
+            zero_scale_row(static_cast<uint8_t*>(a.scales), row, a.rows, tid, kWideThreads, a.H);
 }
 
 template <typename T> struct BwdArgs {
@@ -659,26 +660,38 @@ norm_dweight_kernel(const float* __restrict__ part, int nparts, int H, float* __
 
 int norm_parts(int rows) { return rows < kNormParts ? rows : kNormParts; }
 
-// Shared memory that leaves room for a second block on the SM, and for one.
-constexpr int kSmemTwo = 108 * 1024, kSmemOne = 220 * 1024;
+// Shared memory of an SM's blocks together, and of one.
+constexpr int kSmemAll = 224 * 1024, kSmemOne = 220 * 1024;
+constexpr int kSms = 152;
 
-template <typename K, typename A>
-void launch_staged(K kernel, const A& a, int smem, cudaStream_t s)
-{
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
-    const int blocks = smem <= kSmemTwo ? kNormParts : kNormParts / 2;
-    kernel<<<a.rows < blocks ? a.rows : blocks, kWideThreads, smem, s>>>(a);
-}
-
-// The forward's ring; false if two stages of a row do not fit.
+// The forward's ring, up to four blocks on an SM: four stages a block where
+// sixteen rows fit, else two; false if two do not fit one block.
 template <typename T, bool WINDOW, int QUANT>
 bool launch_fwd_ring(const FwdArgs<T>& a, cudaStream_t s)
 {
     const int stage = Staged<T, WINDOW>::row_bytes(a.H) * (a.r ? 2 : 1);
-    if (4 * stage <= kSmemTwo) launch_staged(norm_fwd_ring_kernel<T, WINDOW, QUANT, 4>, a, 4 * stage, s);
-    else if (2 * stage <= kSmemOne) launch_staged(norm_fwd_ring_kernel<T, WINDOW, QUANT, 2>, a, 2 * stage, s);
+    auto launch = [&](auto kernel, int smem) {
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+        const int fit = kSmemAll / (smem + 1280);
+        const int blocks = kSms * (fit < 1 ? 1 : (fit > 4 ? 4 : fit));
+        kernel<<<a.rows < blocks ? a.rows : blocks, kWideThreads, smem, s>>>(a);
+    };
+    if (16 * stage <= kSmemAll) launch(norm_fwd_ring_kernel<T, WINDOW, QUANT, 4>, 4 * stage);
+    else if (2 * stage <= kSmemOne) launch(norm_fwd_ring_kernel<T, WINDOW, QUANT, 2>, 2 * stage);
     else return false;
     return true;
+}
+
+// The held kernel with N pieces per thread and as many threads as that takes.
+template <typename T, int V, int N, int GROUP, int QUANT, bool AHEAD = false>
+void launch_held(const FwdArgs<T>& a, int rows, cudaStream_t s)
+{
+    if constexpr (GROUP == 32) {
+        norm_fwd_kernel<T, V, N, 32, QUANT><<<(rows + kNormThreads / 32 - 1) / (kNormThreads / 32), kNormThreads, 0, s>>>(a);
+    } else {
+        const int pieces = (a.H + V - 1) / V, threads = (pieces + N - 1) / N;
+        norm_fwd_kernel<T, V, N, GROUP, QUANT, AHEAD><<<rows, (threads + 31) / 32 * 32, 0, s>>>(a);
+    }
 }
 
 template <typename T, int V, int QUANT>
@@ -687,18 +700,17 @@ void launch_fwd_width(const FwdArgs<T>& a, cudaStream_t s)
     constexpr int P = 32 / V;                // pieces of 32 values
     constexpr bool WHOLE = V * sizeof(T) == 16, ODD = V * sizeof(T) == 2;
     const int rows = QUANT == MOE_NORM_MXFP8 ? (a.rows + 127) / 128 * 128 : a.rows;
-    const int warps = (rows + kNormThreads / 32 - 1) / (kNormThreads / 32);
-    if (a.H <= 256) return norm_fwd_kernel<T, V, P / 4, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
-    if (a.H <= 512) return norm_fwd_kernel<T, V, P / 2, 32, QUANT><<<warps, kNormThreads, 0, s>>>(a);
-    if (a.H <= 1024) return norm_fwd_kernel<T, V, P / 4, 128, QUANT><<<rows, 128, 0, s>>>(a);
-    if (a.rows <= kFewRows && a.H <= 4096) return norm_fwd_kernel<T, V, P / 4, 512, QUANT, true><<<rows, 512, 0, s>>>(a);
-    if (a.rows <= kFewRows && a.H <= 8192) return norm_fwd_kernel<T, V, P / 4, 1024, QUANT, true><<<rows, 1024, 0, s>>>(a);
+    if (a.H <= 256) return launch_held<T, V, P / 4, 32, QUANT>(a, rows, s);
+    if (a.H <= 512) return launch_held<T, V, P / 2, 32, QUANT>(a, rows, s);
+    // few rows: a thread per eight values shortens each row's own chain
+    if (a.H <= 8192 && a.rows <= kFewRows) return launch_held<T, V, P / 4, 1024, QUANT, true>(a, rows, s);
+    if (a.H <= 1024) return launch_held<T, V, P / 4, 128, QUANT>(a, rows, s);
     if constexpr (!ODD) {                    // single 2-byte values are staged from here on
-        if (a.H <= 2048) return norm_fwd_kernel<T, V, P / 4, 256, QUANT><<<rows, 256, 0, s>>>(a);
-        if (a.H <= 4096) return norm_fwd_kernel<T, V, P / 2, 256, QUANT><<<rows, 256, 0, s>>>(a);
+        if (a.H <= 2048) return launch_held<T, V, P / 4, 256, QUANT>(a, rows, s);
+        if (a.H <= 4096) return launch_held<T, V, P / 2, 256, QUANT>(a, rows, s);
         if (a.H <= 8192) {
-            if constexpr (sizeof(T) == 2) return norm_fwd_kernel<T, V, P, 256, QUANT><<<rows, 256, 0, s>>>(a);
-            else return norm_fwd_kernel<T, V, P / 2, 512, QUANT><<<rows, 512, 0, s>>>(a);
+            if constexpr (sizeof(T) == 2) return launch_held<T, V, P, 256, QUANT>(a, rows, s);
+            else return launch_held<T, V, P / 2, 512, QUANT>(a, rows, s);
         }
     }
     if (!launch_fwd_ring<T, !WHOLE, QUANT>(a, s)) norm_fwd_loop_kernel<T, V, QUANT><<<rows, kNormThreads, 0, s>>>(a);

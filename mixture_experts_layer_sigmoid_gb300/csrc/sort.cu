@@ -22,41 +22,46 @@ constexpr int kSortMaxAlign = 4096;
 constexpr int kIndexThreads = 1024;
 constexpr int kIndexWarps = kIndexThreads / 32;
 
-// Expert of slot i < n, or -1 for a dropped slot or one past the end.
-__device__ __forceinline__ int slot_expert(const int32_t* topk, int i, int n, int E)
-{
-    if (i >= n) return -1;
-    const int e = topk[i];
-    return (unsigned)e < (unsigned)E ? e : -1;
-}
+// Four groups of slots for a warp while there are few; one block up to eight
+// warps, where a cluster's barriers cost more than they save, else clusters of
+// eight: one for each 16384 slots, at most 16.
+constexpr int kIndexOneBlock = 1024;
+constexpr int kIndexCluster = 8;
+constexpr int kIndexSmem = 148 * 1024;  // 16 warps' pairs of 1024 experts, or 32 of 512, and the rest
+
+// What topk says for slot i < n, or -1 past the end. Dropped slots are told
+// apart where the value is used, so that loads ahead of that stay in flight.
+__device__ __forceinline__ int slot_expert(const int32_t* topk, int i, int n) { return i < n ? topk[i] : -1; }
 
 // The blocks of a cluster. Each warp takes a run of consecutive slots: it
 // counts its slots of each expert, the counts are summed over warps, blocks
 // (through distributed shared memory) and experts, and it then goes over its
-// slots again in order, 32 at a time; lanes with the same expert find one
-// another by one ballot per bit of the expert's number (a match instruction
-// took 8x as long), so a slot's rank needs no atomic and the order is the
-// slots' own. With several clusters each counts everything, and a run's second
+// slots again in order, 32 at a time: each lane sets its bit in its expert's
+// word, so lanes with the same expert see one another there and a slot's rank
+// follows the slots' own order (one ballot per bit of the expert's number, or a
+// match instruction, took 3 to 8 times as long). With several clusters each counts everything, and a run's second
 // part is done by one of them: the scattered stores of slot_of, about one a
-// cycle and SM, are what takes longest. Shared memory: `warps` x E counters,
-// the block's E totals and the E padding ranges.
+// cycle and SM, are what takes longest. Shared memory: `warps` x E counters
+// with their lane words, the block's E totals, the E bases and padding ranges.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kIndexThreads)
-sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, int E, int bits, int align,
+sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, int E, int align,
                   int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ row_of,
                   int32_t* __restrict__ slot_of, int rows)
 {
-    extern __shared__ int hist[];            // [warps][E], [E], [E][2]
+    extern __shared__ int2 hist[];           // [warps][E] of (count, lanes), [E] int2, [E], [E]
     __shared__ int wsum[kIndexWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
-    const int rank = (int)ptx::cluster_ctarank(), cluster = (int)ptx::cluster_id_x();
-    const int clusters = (int)ptx::nclusters_x(), blocks = gridDim.x / clusters;
+    const int rank = CLUSTER ? (int)ptx::cluster_ctarank() : 0, cluster = CLUSTER ? (int)ptx::cluster_id_x() : 0;
+    const int clusters = CLUSTER ? (int)ptx::nclusters_x() : 1, blocks = gridDim.x / clusters;
     const long long lo = ((long long)rank * warps + warp) * per;      // slots [lo, lo + per) of this warp
     const long long left = n - lo;
     const int mine_n = warp < warps && left > 0 ? (left < per ? (int)left : per) : 0;
-    int* mine = hist + warp * E;
-    int* tot = hist + warps * E;
-    int2* pad = reinterpret_cast<int2*>(tot + E + (E * (warps + 1) & 1));
-    for (int i = tid; i < warps * E; i += nt) hist[i] = 0;
+    int2* mine = hist + warp * E;
+    int2* pad = hist + warps * E;
+    int* tot = reinterpret_cast<int*>(pad + E);
+    int* base = tot + E;
+    for (int i = tid; i < warps * E; i += nt) hist[i] = make_int2(0, 0);
     __syncthreads();
     // U groups of 32 slots are loaded together; the second part's first groups
     // are its last here
@@ -64,7 +69,7 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
     int next[U];
     auto load = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = slot_expert(topk + lo, i + 32 * u + lane, mine_n, E);
+        for (int u = 0; u < U; ++u) next[u] = slot_expert(topk + lo, i + 32 * u + lane, mine_n);
     };
     load(0);
     for (int i = 0; i < mine_n; i += 32 * U) {
@@ -74,30 +79,37 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
         load(i + 32 * U < mine_n ? i + 32 * U : 0);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (ex[u] >= 0) atomicAdd(mine + ex[u], 1);      // integers: the order does not matter
+            if ((unsigned)ex[u] < (unsigned)E) atomicAdd(&mine[ex[u]].x, 1);    // integers: the order does not matter
     }
     __syncthreads();
     // thread e: counts of expert e -> each warp's base among the block's slots
-    if (tid < E) {
-        int total = 0;
-#pragma unroll 4
-        for (int w = 0; w < warps; ++w) {
-            const int c = hist[w * E + tid];
-            hist[w * E + tid] = total;
-            total += c;
-        }
-        tot[tid] = total;
-    }
-    ptx::cluster_sync();
     int total = 0, below = 0;
     if (tid < E) {
-        const uint32_t at = ptx::smem_u32(tot + tid);
-#pragma unroll 4
-        for (int r = 0; r < blocks; ++r) {
-            int c;
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(ptx::mapa_shared(at, r)) : "memory");
-            total += c;
-            below += r < rank ? c : 0;
+        constexpr int B = 8;                 // counters read together
+        for (int w0 = 0; w0 < warps; w0 += B) {
+            int c[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i) c[i] = w0 + i < warps ? hist[(w0 + i) * E + tid].x : 0;
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if (w0 + i < warps) hist[(w0 + i) * E + tid].x = total;
+                total += c[i];
+            }
+        }
+        if constexpr (CLUSTER) tot[tid] = total;
+    }
+    if constexpr (CLUSTER) {
+        ptx::cluster_sync();
+        if (tid < E) {
+            const uint32_t at = ptx::smem_u32(tot + tid);
+            total = 0;
+#pragma unroll
+            for (int r = 0; r < kIndexCluster; ++r) {
+                int c;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(ptx::mapa_shared(at, r)) : "memory");
+                total += c;
+                below += r < rank ? c : 0;
+            }
         }
     }
     // exclusive scan of the padded counts over the experts
@@ -110,15 +122,16 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
     }
     if (lane == 31) wsum[warp] = sum;
     __syncthreads();
-    int before = 0, used = 0;
-    for (int w = 0; w < nt / 32; ++w) {
-        before += w < warp ? wsum[w] : 0;
-        used += wsum[w];
+    // the warps' sums: those below this warp's, and all
+    int used = lane < nt / 32 ? wsum[lane] : 0, before = lane < warp ? used : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        used += __shfl_xor_sync(0xffffffffu, used, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
     }
     const int off = before + sum - padded;
     if (tid < E) {
-#pragma unroll 4
-        for (int w = 0; w < warps; ++w) hist[w * E + tid] += off + below;
+        base[tid] = off + below;
         if (blockIdx.x == 0) {
             counts[tid] = total;
             offsets[tid] = off;
@@ -129,79 +142,69 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
     __syncthreads();
     for (int i = 0; i < mine_n && warp % clusters == cluster; i += 32 * U) {
         int ex[U];
-        unsigned peers[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            ex[u] = next[u];
-            peers[u] = __ballot_sync(0xffffffffu, ex[u] >= 0);
-        }
+        for (int u = 0; u < U; ++u) ex[u] = next[u];
         load(i + 32 * U);
-        for (int b = 0; b < bits; ++b) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool one = ex[u] >> b & 1;
-                const unsigned m = __ballot_sync(0xffffffffu, one);
-                peers[u] &= one ? m : ~m;
-            }
-        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            int row = -1;
-            if (ex[u] >= 0) row = mine[ex[u]] + __popc(peers[u] & ((1u << lane) - 1));
-            __syncwarp();
-            if (ex[u] >= 0 && lane == __ffs(peers[u]) - 1) mine[ex[u]] += __popc(peers[u]);
-            __syncwarp();
             const int s = i + 32 * u + lane;
+            if (s - lane >= mine_n) break;
+            const bool live = (unsigned)ex[u] < (unsigned)E;
+            if (live) atomicOr(&mine[ex[u]].y, 1 << lane);
+            __syncwarp();
+            int row = -1;
+            int2 m = make_int2(0, 0);
+            if (live) {
+                m = mine[ex[u]];
+                row = base[ex[u]] + m.x + __popc(m.y & ((1u << lane) - 1));
+            }
+            __syncwarp();
+            if (live && lane == __ffs(m.y) - 1) mine[ex[u]] = make_int2(m.x + __popc(m.y), 0);
+            __syncwarp();
             if (s < mine_n) {
                 row_of[lo + s] = row;
-                if (row >= 0) slot_of[row] = (int)(lo + s);
+                if (live) slot_of[row] = (int)(lo + s);
             }
         }
     }
     // a warp per segment's padding, and the rows after the last segment
-    for (int e = blockIdx.x * (nt / 32) + warp; e < E; e += gridDim.x * (nt / 32))
+    for (int e = blockIdx.x * (nt / 32) + warp; e < E && align > 1; e += gridDim.x * (nt / 32))
         for (int r = pad[e].x + lane; r < pad[e].y; r += 32) slot_of[r] = -1;
     for (long long r = used + (long long)blockIdx.x * nt + tid; r < rows; r += gridDim.x * nt) slot_of[r] = -1;
-    ptx::cluster_sync();                     // no block leaves while another may read its totals
+    if constexpr (CLUSTER) ptx::cluster_sync();          // no block leaves while another may read its totals
 }
-
-// Four groups of slots for a warp while there are few; one block up to eight
-// warps, where a cluster's barriers cost more than they save, else clusters of
-// eight: one for each 16384 slots, at most 16.
-constexpr int kIndexOneBlock = 1024;
-constexpr int kIndexCluster = 8;
 
 cudaError_t launch_index(int n, int E, int align, const int32_t* topk, int32_t* counts, int32_t* offsets,
                          int32_t* row_of, int32_t* slot_of, int rows, cudaStream_t s)
 {
     const int blocks = n <= kIndexOneBlock ? 1 : kIndexCluster;
     const int groups = (n + 31) / 32;
+    const int most = E <= 512 ? kIndexWarps : kIndexWarps / 2;       // of (count, lanes) pairs in shared memory
     int warps = (groups + 4 * blocks - 1) / (4 * blocks);
-    warps = warps < 1 ? 1 : (warps > kIndexWarps ? kIndexWarps : warps);
+    warps = warps < 1 ? 1 : (warps > most ? most : warps);
     const int per = (groups + blocks * warps - 1) / (blocks * warps) * 32;
-    const int threads = 32 * warps > E ? 32 * warps : (E + 31) / 32 * 32;
-    int bits = 0;
-    while (1 << bits < E) ++bits;
-    const size_t smem = (size_t)(warps + 3) * E * sizeof(int) + 8;
+    // threads for the experts, and for the padding
+    const int threads = align > 1 || E > 512 ? kIndexThreads : (32 * warps > E ? 32 * warps : (E + 31) / 32 * 32);
+    const size_t smem = (size_t)E * ((warps + 1) * sizeof(int2) + 2 * sizeof(int));
+    auto kernel = blocks == 1 ? sort_index_kernel<false> : sort_index_kernel<true>;
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(sort_index_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (kIndexWarps + 3) * kSortMaxE * (int)sizeof(int) + 8);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kIndexSmem);
         if (e != cudaSuccess) return e;
     }
+    const int clusters = blocks == 1 || n < 32768 ? 1 : (n >= 16 * 16384 ? 16 : n / 16384);
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = blocks;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    const int clusters = blocks == 1 || n < 32768 ? 1 : (n >= 16 * 16384 ? 16 : n / 16384);
     cfg.gridDim = dim3(blocks * clusters);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sort_index_kernel, topk, n, per, warps, E, bits, align, counts, offsets, row_of,
-                              slot_of, rows);
+    cfg.numAttrs = blocks == 1 ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, topk, n, per, warps, E, align, counts, offsets, row_of, slot_of, rows);
 }
 
 // ------------------------------------------------------------------ rows
