@@ -12,6 +12,8 @@
 #include "ptx.cuh"
 #include "rowvec.cuh"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -81,10 +83,10 @@ struct Staged {
             else copy_async<16>(dst + at, src + at);
         }
     }
-    // values [c, c + V) of the row staged at buf
-    static __device__ __forceinline__ void get(const unsigned char* buf, int phase, int c, float (&v)[V])
+    // the V values at `at` bytes from buf
+    static __device__ __forceinline__ void get(const unsigned char* buf, int at, float (&v)[V])
     {
-        unpack<T, V>(*reinterpret_cast<const Raw<T, V>*>(buf + phase + c * (int)sizeof(T)), v);
+        unpack<T, V>(*reinterpret_cast<const Raw<T, V>*>(buf + at), v);
     }
 };
 
@@ -286,20 +288,21 @@ norm_fwd_kernel(FwdArgs<T> a)
 // a ring of S staged rows. Without WINDOW a thread reads back only what it
 // copied itself, so the row's sum is the only barrier.
 constexpr int kWideThreads = 512;
-template <typename T, bool WINDOW, int QUANT, int S>
-__global__ void __launch_bounds__(kWideThreads)
+template <typename T, bool WINDOW, bool RES, int QUANT, int S>
+__global__ void __launch_bounds__(kWideThreads, 3)
 norm_fwd_ring_kernel(FwdArgs<T> a)
 {
     using R = Staged<T, WINDOW>;
     constexpr int V = R::V;
+    constexpr int U = WINDOW ? 4 : 2;        // pieces together; more would spill at three blocks an SM
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float red[2][kWideThreads / 32];
     const int tid = threadIdx.x;
-    const int rb = R::row_bytes(a.H), sb = a.r ? 2 * rb : rb;
+    const int rb = R::row_bytes(a.H), sb = RES ? 2 * rb : rb;
     auto fetch = [&](int stage, long long row) {
         if (row < a.rows) {
             R::template fetch<kWideThreads>(ring + stage * sb, a.x + row * a.ldx, a.H, tid);
-            if (a.r) R::template fetch<kWideThreads>(ring + stage * sb + rb, a.r + row * a.ldr, a.H, tid);
+            if constexpr (RES) R::template fetch<kWideThreads>(ring + stage * sb + rb, a.r + row * a.ldr, a.H, tid);
         }
         copy_commit();
     };
@@ -308,46 +311,54 @@ norm_fwd_ring_kernel(FwdArgs<T> a)
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         copy_wait<S - 1>();
         if constexpr (WINDOW) __syncthreads();
+        constexpr int SIZE = (int)sizeof(T);
         const unsigned char* bx = ring + stage * sb;
-        const unsigned char* br = bx + rb;
-        const int px = R::phase(a.x + row * a.ldx), pr = a.r ? R::phase(a.r + row * a.ldr) : 0;
-        auto value = [&](int c, float (&v)[V]) {
-            R::get(bx, px, c, v);
-            if (a.r) {
+        bx += R::phase(a.x + row * a.ldx) + tid * (V * SIZE);
+        const unsigned char* br = bx;
+        if constexpr (RES) br = ring + stage * sb + rb + R::phase(a.r + row * a.ldr) + tid * (V * SIZE);
+        // values of the thread's i-th piece
+        auto value = [&](int i, float (&v)[V]) {
+            R::get(bx, i * (kWideThreads * V * SIZE), v);
+            if constexpr (RES) {
                 float u[V];
-                R::get(br, pr, c, u);
+                R::get(br, i * (kWideThreads * V * SIZE), u);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] += u[i];
+                for (int j = 0; j < V; ++j) v[j] += u[j];
             }
         };
+        const int own = (a.H - tid * V + kWideThreads * V - 1) / (kWideThreads * V);   // pieces of this thread
         float ss = 0.f;
-#pragma unroll 4
-        for (int c = tid * V; c < a.H; c += kWideThreads * V) {
+#pragma unroll U
+        for (int i = 0; i < own; ++i) {
             float v[V];
-            value(c, v);
+            value(i, v);
 #pragma unroll
-            for (int i = 0; i < V; ++i) ss = fmaf(v[i], v[i], ss);
+            for (int j = 0; j < V; ++j) ss = fmaf(v[j], v[j], ss);
         }
         const float rstd = rsqrtf(block_sum<kWideThreads>(ss, red[parity]) / (float)a.H + a.eps);
         parity ^= 1;
         if (tid == 0 && a.rstd) a.rstd[row] = rstd;
-#pragma unroll 4
-        for (int c0 = 0; c0 < a.H; c0 += kWideThreads * V) {
-            const int c = c0 + tid * V;
-            const bool act = c < a.H;
-            float v[V];
+        const float* w = a.w + tid * V;
+        T* h = a.h ? a.h + row * a.ldh + tid * V : nullptr;
+        T* y = a.y ? a.y + row * a.ldy + tid * V : nullptr;
+        // 8-bit blocks are shared by lanes: every thread takes part in each step
+        const int steps = QUANT == MOE_NORM_PLAIN ? own : (a.H + kWideThreads * V - 1) / (kWideThreads * V);
+#pragma unroll U
+        for (int i = 0; i < steps; ++i) {
+            const int at = i * (kWideThreads * V);
+            const bool act = QUANT == MOE_NORM_PLAIN || i < own;
+            float v[V], wv[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = 0.f;
+            for (int j = 0; j < V; ++j) v[j] = 0.f;
             if (act) {
-                float w[V];
-                value(c, v);
-                if (a.h) store_vec<T, V>(a.h + row * a.ldh + c, v);
-                load_f32<V>(a.w + c, w);
+                value(i, v);
+                if (RES && h) store_vec<T, V>(h + at, v);
+                load_f32<V>(w + at, wv);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = v[i] * rstd * w[i];
-                if (a.y) store_vec<T, V>(a.y + row * a.ldy + c, v);
+                for (int j = 0; j < V; ++j) v[j] = v[j] * rstd * wv[j];
+                if (QUANT == MOE_NORM_PLAIN || y) store_vec<T, V>(y + at, v);
             }
-            if constexpr (QUANT != MOE_NORM_PLAIN) quantise<QUANT, V>(v, act, (int)row, c, a.H, a.codes, a.scales);
+            if constexpr (QUANT != MOE_NORM_PLAIN) quantise<QUANT, V>(v, act, (int)row, at + tid * V, a.H, a.codes, a.scales);
         }
         if constexpr (WINDOW) __syncthreads();          // the stage is read
         fetch(stage, row + (long long)S * gridDim.x);
@@ -368,11 +379,12 @@ template <typename T> struct BwdArgs {
 
 // Block b takes rows b, b + gridDim.x, ...; each thread always holds the same
 // columns, so it adds its rows' dy n into part[b] alone.
+constexpr int kLoopThreads = 1024;
 template <typename T, int V>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kLoopThreads)
 norm_bwd_loop_kernel(BwdArgs<T> a)
 {
-    __shared__ float red[kNormThreads / 32];
+    __shared__ float red[kLoopThreads / 32];
     float* part = a.part ? a.part + (size_t)blockIdx.x * a.H : nullptr;
     for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T* dy = a.dy + (size_t)row * a.lddy;
@@ -381,7 +393,7 @@ norm_bwd_loop_kernel(BwdArgs<T> a)
         T* dx = a.dx + (size_t)row * a.lddx;
         const float rstd = a.rstd[row];
         float d = 0.f;
-        for (int c = threadIdx.x * V; c < a.H; c += kNormThreads * V) {
+        for (int c = threadIdx.x * V; c < a.H; c += kLoopThreads * V) {
             float g[V], v[V], w[V];
             load_vec<T, V>(dy + c, g);
             load_vec<T, V>(h + c, v);
@@ -390,8 +402,8 @@ norm_bwd_loop_kernel(BwdArgs<T> a)
             for (int i = 0; i < V; ++i) d = fmaf(g[i] * w[i], v[i], d);
         }
         __syncthreads();                       // red of the previous row is read
-        const float m = block_sum<kNormThreads>(d, red) * rstd / (float)a.H;
-        for (int c = threadIdx.x * V; c < a.H; c += kNormThreads * V) {
+        const float m = block_sum<kLoopThreads>(d, red) * rstd / (float)a.H;
+        for (int c = threadIdx.x * V; c < a.H; c += kLoopThreads * V) {
             float g[V], v[V], w[V], o[V], p[V];
             load_vec<T, V>(dy + c, g);
             load_vec<T, V>(h + c, v);
@@ -565,7 +577,7 @@ norm_bwd_kernel(BwdArgs<T> a)
 
 // The same for rows of any alignment and width, staged whole (as in the
 // forward's ring); dw is summed in shared memory, each column by one thread.
-template <typename T, int S>
+template <typename T, bool DH, int S>
 __global__ void __launch_bounds__(kWideThreads)
 norm_bwd_window_kernel(BwdArgs<T> a)
 {
@@ -573,20 +585,19 @@ norm_bwd_window_kernel(BwdArgs<T> a)
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float red[2][kWideThreads / 32];
     const int tid = threadIdx.x;
-    const int rb = R::row_bytes(a.H), sb = (a.dh ? 3 : 2) * rb;
+    const int rb = R::row_bytes(a.H), sb = (DH ? 3 : 2) * rb;
     float* dw = reinterpret_cast<float*>(ring + S * sb);
     auto fetch = [&](int stage, long long row) {
         if (row < a.rows) {
             unsigned char* to = ring + stage * sb;
             R::template fetch<kWideThreads>(to, a.dy + row * a.lddy, a.H, tid);
             R::template fetch<kWideThreads>(to + rb, a.h + row * a.ldh, a.H, tid);
-            if (a.dh) R::template fetch<kWideThreads>(to + 2 * rb, a.dh + row * a.lddh, a.H, tid);
+            if constexpr (DH) R::template fetch<kWideThreads>(to + 2 * rb, a.dh + row * a.lddh, a.H, tid);
         }
         copy_commit();
     };
     for (int s = 0; s < S; ++s) fetch(s, (long long)blockIdx.x + (long long)s * gridDim.x);
-    if (a.part)
-        for (int c = tid; c < a.H; c += kWideThreads) dw[c] = 0.f;
+    for (int c = tid; c < a.H; c += kWideThreads) dw[c] = 0.f;
     ptx::griddep_launch_dependents();
     int stage = 0, parity = 0;
     float rstd = blockIdx.x < (unsigned)a.rows ? a.rstd[blockIdx.x] : 0.f;
@@ -594,36 +605,39 @@ norm_bwd_window_kernel(BwdArgs<T> a)
         const float next = row + gridDim.x < a.rows ? a.rstd[row + gridDim.x] : 0.f;
         copy_wait<S - 1>();
         __syncthreads();
-        const unsigned char* bg = ring + stage * sb;
-        const unsigned char* bh = bg + rb;
-        const unsigned char* bd = bh + rb;
-        const int pg = R::phase(a.dy + row * a.lddy), ph = R::phase(a.h + row * a.ldh);
-        const int pd = a.dh ? R::phase(a.dh + row * a.lddh) : 0;
+        constexpr int STEP = kWideThreads * (int)sizeof(T);
+        const unsigned char* at = ring + stage * sb + tid * (int)sizeof(T);
+        const unsigned char* bg = at + R::phase(a.dy + row * a.lddy);
+        const unsigned char* bh = at + rb + R::phase(a.h + row * a.ldh);
+        const unsigned char* bd = DH ? at + 2 * rb + R::phase(a.dh + row * a.lddh) : at;
+        const float* w = a.w + tid;
+        const int own = (a.H - tid + kWideThreads - 1) / kWideThreads;     // values of this thread
         float d = 0.f;
 #pragma unroll 4
-        for (int c = tid; c < a.H; c += kWideThreads) {
+        for (int i = 0; i < own; ++i) {
             float g[1], v[1];
-            R::get(bg, pg, c, g);
-            R::get(bh, ph, c, v);
-            d = fmaf(g[0] * a.w[c], v[0], d);
+            R::get(bg, i * STEP, g);
+            R::get(bh, i * STEP, v);
+            d = fmaf(g[0] * w[i * kWideThreads], v[0], d);
         }
         const float m = block_sum<kWideThreads>(d, red[parity]) * rstd / (float)a.H;
         parity ^= 1;
-        T* dx = a.dx + row * a.lddx;
+        T* dx = a.dx + row * a.lddx + tid;
+        float* dwt = dw + tid;
 #pragma unroll 4
-        for (int c = tid; c < a.H; c += kWideThreads) {
+        for (int i = 0; i < own; ++i) {
             float g[1], v[1], o[1];
-            R::get(bg, pg, c, g);
-            R::get(bh, ph, c, v);
+            R::get(bg, i * STEP, g);
+            R::get(bh, i * STEP, v);
             const float n = v[0] * rstd;
-            o[0] = rstd * fmaf(-n, m, g[0] * a.w[c]);
-            if (a.part) dw[c] = fmaf(g[0], n, dw[c]);
-            if (a.dh) {
+            o[0] = rstd * fmaf(-n, m, g[0] * w[i * kWideThreads]);
+            dwt[i * kWideThreads] = fmaf(g[0], n, dwt[i * kWideThreads]);
+            if constexpr (DH) {
                 float u[1];
-                R::get(bd, pd, c, u);
+                R::get(bd, i * STEP, u);
                 o[0] += u[0];
             }
-            store_vec<T, 1>(dx + c, o);
+            store_vec<T, 1>(dx + i * kWideThreads, o);
         }
         __syncthreads();                                  // the stage is read
         fetch(stage, row + (long long)S * gridDim.x);
@@ -664,8 +678,9 @@ int norm_parts(int rows) { return rows < kNormParts ? rows : kNormParts; }
 constexpr int kSmemAll = 224 * 1024, kSmemOne = 220 * 1024;
 constexpr int kSms = 152;
 
-// The forward's ring, up to four blocks on an SM: four stages a block where
-// sixteen rows fit, else two; false if two do not fit one block.
+// The forward's ring, up to three blocks on an SM (their registers allow no
+// more): four stages a block where twelve rows fit, else two; false if two do
+// not fit one block.
 template <typename T, bool WINDOW, int QUANT>
 bool launch_fwd_ring(const FwdArgs<T>& a, cudaStream_t s)
 {
@@ -673,13 +688,17 @@ bool launch_fwd_ring(const FwdArgs<T>& a, cudaStream_t s)
     auto launch = [&](auto kernel, int smem) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
         const int fit = kSmemAll / (smem + 1280);
-        const int blocks = kSms * (fit < 1 ? 1 : (fit > 4 ? 4 : fit));
+        const int blocks = kSms * (fit < 1 ? 1 : (fit > 3 ? 3 : fit));
         kernel<<<a.rows < blocks ? a.rows : blocks, kWideThreads, smem, s>>>(a);
     };
-    if (16 * stage <= kSmemAll) launch(norm_fwd_ring_kernel<T, WINDOW, QUANT, 4>, 4 * stage);
-    else if (2 * stage <= kSmemOne) launch(norm_fwd_ring_kernel<T, WINDOW, QUANT, 2>, 2 * stage);
-    else return false;
-    return true;
+    auto staged = [&](auto res) {
+        constexpr bool RES = decltype(res)::value;
+        if (12 * stage + 3 * 1280 <= kSmemAll) launch(norm_fwd_ring_kernel<T, WINDOW, RES, QUANT, 4>, 4 * stage);
+        else if (2 * stage <= kSmemOne) launch(norm_fwd_ring_kernel<T, WINDOW, RES, QUANT, 2>, 2 * stage);
+        else return false;
+        return true;
+    };
+    return a.r ? staged(std::true_type{}) : staged(std::false_type{});
 }
 
 // The held kernel with N pieces per thread and as many threads as that takes.
@@ -782,13 +801,13 @@ void launch_bwd_width(const BwdArgs<T>& a, int parts, cudaStream_t s)
     if constexpr (V * sizeof(T) < 16) {
         const int smem = 2 * Staged<T, true>::row_bytes(a.H) * (a.dh ? 3 : 2) + a.H * (int)sizeof(float);
         if (smem <= kSmemOne) {
-            auto kernel = norm_bwd_window_kernel<T, 2>;
+            auto kernel = a.dh ? norm_bwd_window_kernel<T, true, 2> : norm_bwd_window_kernel<T, false, 2>;
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
             kernel<<<parts, kWideThreads, smem, s>>>(a);
             return;
         }
     }
-    norm_bwd_loop_kernel<T, V><<<parts, kNormThreads, 0, s>>>(a);
+    norm_bwd_loop_kernel<T, V><<<parts, kLoopThreads, 0, s>>>(a);
 }
 
 template <typename T>
