@@ -74,6 +74,11 @@ def _vec(t, name, n, dtype, like):
     return t.data_ptr()
 
 
+def _like(x, ldx):
+    """A new contiguous matrix of x's shape and type."""
+    return _torch.empty_like(x) if ldx == x.shape[1] else _torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -99,16 +104,20 @@ def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quant: int = MO
         a.ldr = _act(residual, "residual", shape, x)
         a.residual = residual.data_ptr()
         if h is None:
-            h = t.empty_like(x) if ldx == H else t.empty(shape, dtype=x.dtype, device=x.device)
-        a.ldh = _act(h, "h", shape, x)
+            h = _like(x, ldx)
+            a.ldh = H
+        else:
+            a.ldh = _act(h, "h", shape, x)
         a.h = h.data_ptr()
         out["h"] = h
     elif h is not None:
         raise ValueError("h: without a residual there is no sum to store")
     if want_y or y is not None or quant == MOE_NORM_PLAIN:
         if y is None:
-            y = t.empty_like(x) if ldx == H else t.empty(shape, dtype=x.dtype, device=x.device)
-        a.ldy = _act(y, "y", shape, x)
+            y = _like(x, ldx)
+            a.ldy = H
+        else:
+            a.ldy = _act(y, "y", shape, x)
         a.y = y.data_ptr()
         out["y"] = y
     if want_rstd:
@@ -143,8 +152,10 @@ def add_rms_norm_backward(dy, h, rstd, weight, dh=None, *, dx=None, want_dweight
         a.lddh = _act(dh, "dh", shape, dy)
         a.dh = dh.data_ptr()
     if dx is None:
-        dx = t.empty_like(dy) if lddy == H else t.empty(shape, dtype=dy.dtype, device=dy.device)
-    a.lddx = _act(dx, "dx", shape, dy)
+        dx = _like(dy, lddy)
+        a.lddx = H
+    else:
+        a.lddx = _act(dx, "dx", shape, dy)
     a.dx = dx.data_ptr()
     dweight = None
     if want_dweight:
@@ -167,18 +178,17 @@ def sort_index(topk, E: int, align: int = 1) -> Dict[str, object]:
     if not topk.is_cuda or topk.dim() != 2 or topk.dtype != t.int32 or not topk.is_contiguous():
         raise ValueError("topk: a contiguous T x k int32 CUDA tensor is needed")
     T, k = topk.shape
-    rows = moe_sort_rows_cap(T, k, E, align)
-    # one allocation; every part starts on a 16-byte boundary
-    at = [0, (E + 3) & ~3]
-    at.append(at[1] + ((E + 4) & ~3))
-    at.append(at[2] + ((T * k + 3) & ~3))
-    buf = t.empty(at[3] + rows, dtype=t.int32, device=topk.device)
-    ix = {"counts": buf[:E], "offsets": buf[at[1]:at[1] + E + 1], "row_of": buf[at[2]:at[2] + T * k].view(T, k),
-          "slot_of": buf[at[3]:]}
-    p = buf.data_ptr()
-    _call("moe_sort_index", topk.get_device(), lib.moe_sort_index, T, k, E, align, topk.data_ptr(), p, p + 4 * at[1],
-          p + 4 * at[2], p + 4 * at[3], rows)
-    return ix
+    n = T * k
+    if n == 0 or E < 1 or align < 1:
+        rows = moe_sort_rows_cap(T, k, E, align)
+    else:                                    # the same, without the call
+        rows = -(-(n + min(E, n) * (align - 1)) // align) * align
+    dev, i32 = topk.device, t.int32
+    counts, offsets = t.empty(E, dtype=i32, device=dev), t.empty(E + 1, dtype=i32, device=dev)
+    row_of, slot_of = t.empty_like(topk), t.empty(rows, dtype=i32, device=dev)
+    _call("moe_sort_index", topk.get_device(), lib.moe_sort_index, T, k, E, align, topk.data_ptr(), counts.data_ptr(),
+          offsets.data_ptr(), row_of.data_ptr(), slot_of.data_ptr(), rows)
+    return {"counts": counts, "offsets": offsets, "row_of": row_of, "slot_of": slot_of}
 
 
 def _sorted(index, H, dtype, like, rows, padding=True):
