@@ -417,8 +417,8 @@ moe_status_t moe_update_bias(int E, const int32_t* counts, float rate, float* b,
  * clipping. Conventions as above, and:
  *   - they need no plan; they run on the calling thread's current device, on
  *     which the pointers and the stream must live;
- *   - "act" values are fp32 (MOE_FP32) or bf16 (MOE_BF16); any width H >= 1 is
- *     accepted; row strides (ld*) count elements and are at least H;
+ *   - "act" values are fp32 (MOE_FP32) or bf16 (MOE_BF16); any width H from
+ *     1 to 2^20 is accepted; row strides (ld*) count elements and are at least H;
  *   - zero rows, tokens or tensors are accepted: nothing is read, outputs
  *     that do not depend on rows (weight gradients, counts, the norm) are
  *     written, and the pointers of empty tensors may be NULL;

@@ -842,6 +842,7 @@ moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cud
 
 bool act_dtype(int dtype) { return dtype == MOE_FP32 || dtype == MOE_BF16; }
 constexpr int kNormMaxH = 1 << 20;
+constexpr int kNormMaxRows = 0x7FFFFF00;     // rounded up to a tile of 128 it is still an int
 
 }  // namespace
 }  // namespace moe
@@ -851,7 +852,7 @@ using namespace moe;
 moe_status_t moe_add_rms_norm(int rows, int H, int dtype, int quant, float eps,
                               const moe_norm_fwd_args_t* args, moe_stream_t stream)
 {
-    if (!args || rows < 0 || H < 1 || H > kNormMaxH || !act_dtype(dtype) || quant < MOE_NORM_PLAIN ||
+    if (!args || rows < 0 || rows > kNormMaxRows || H < 1 || H > kNormMaxH || !act_dtype(dtype) || quant < MOE_NORM_PLAIN ||
         quant > MOE_NORM_MXFP8 || !(eps >= 0.f) || eps - eps != 0.f)
         return MOE_ERR_INVALID_ARG;
     const moe_norm_fwd_args_t& g = *args;
@@ -871,7 +872,7 @@ moe_status_t moe_add_rms_norm(int rows, int H, int dtype, int quant, float eps,
 
 moe_status_t moe_norm_workspace_size(int rows, int H, size_t* ws_bytes)
 {
-    if (!ws_bytes || rows < 0 || H < 1 || H > kNormMaxH) return MOE_ERR_INVALID_ARG;
+    if (!ws_bytes || rows < 0 || rows > kNormMaxRows || H < 1 || H > kNormMaxH) return MOE_ERR_INVALID_ARG;
     *ws_bytes = (size_t)norm_parts(rows) * H * sizeof(float);
     return MOE_OK;
 }
@@ -879,7 +880,7 @@ moe_status_t moe_norm_workspace_size(int rows, int H, size_t* ws_bytes)
 moe_status_t moe_add_rms_norm_backward(int rows, int H, int dtype, const moe_norm_bwd_args_t* args,
                                        void* ws, size_t ws_bytes, moe_stream_t stream)
 {
-    if (!args || rows < 0 || H < 1 || H > kNormMaxH || !act_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    if (!args || rows < 0 || rows > kNormMaxRows || H < 1 || H > kNormMaxH || !act_dtype(dtype)) return MOE_ERR_INVALID_ARG;
     const moe_norm_bwd_args_t& g = *args;
     if (!g.weight || (rows > 0 && (!g.dy || !g.h || !g.rstd || !g.dx))) return MOE_ERR_INVALID_ARG;
     if (g.lddy < H || g.ldh < H || g.lddx < H || (g.dh && g.lddh < H)) return MOE_ERR_INVALID_ARG;

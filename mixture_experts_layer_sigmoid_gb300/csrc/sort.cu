@@ -17,6 +17,7 @@ namespace {
 constexpr int kSortMaxK = 32;
 constexpr int kSortMaxE = 1024;
 constexpr int kSortMaxAlign = 4096;
+constexpr int kSortMaxH = 1 << 20;
 
 // ------------------------------------------------------------------ index
 constexpr int kIndexThreads = 1024;
@@ -528,7 +529,7 @@ bool sort_args_ok(int T, int k, int E, int align)
 // The checks that the movers share; MOE_OK if the index can be used.
 moe_status_t check_index(const moe_sorted_t* ix, bool writes_rows)
 {
-    if (!ix || ix->T < 0 || ix->k < 1 || ix->k > kSortMaxK || ix->H < 1 || ix->rows < 0 ||
+    if (!ix || ix->T < 0 || ix->k < 1 || ix->k > kSortMaxK || ix->H < 1 || ix->H > kSortMaxH || ix->rows < 0 ||
         ix->rows >= (1ll << 31) - 1 || (long long)ix->T * ix->k >= (1ll << 31) - 1 ||
         (ix->dtype != MOE_FP32 && ix->dtype != MOE_BF16))
         return MOE_ERR_INVALID_ARG;

@@ -163,6 +163,8 @@ def add_rms_norm_backward(dy, h, rstd, weight, dh=None, *, dx=None, want_dweight
         a.dweight = dweight.data_ptr()
         if ws is None:
             ws = t.empty(moe_norm_workspace_size(rows, H), dtype=t.uint8, device=dy.device)
+        elif ws.get_device() != dy.get_device() or not ws.is_contiguous():
+            raise ValueError("ws: contiguous scratch on dy's device is needed")
     _call("moe_add_rms_norm_backward", dy.get_device(), lib.moe_add_rms_norm_backward, rows, H, _dtypes[dy.dtype],
           ctypes.byref(a), _p(ws), 0 if ws is None else ws.numel() * ws.element_size())
     return dx, dweight
@@ -199,8 +201,10 @@ def _sorted(index, H, dtype, like, rows, padding=True):
     s = moe_sorted_t(row_of.shape[0], row_of.shape[1], H, _dtypes[dtype], rows, row_of.data_ptr())
     if padding and slot_of is not None:
         offsets = index["offsets"]
-        if slot_of.numel() < rows or slot_of.dtype != t.int32 or offsets.dtype != t.int32:
-            raise ValueError(f"slot_of: int32 for each of the {rows} rows is needed")
+        dev = like.get_device()
+        if (slot_of.numel() < rows or slot_of.dtype != t.int32 or offsets.dtype != t.int32 or slot_of.get_device() != dev or
+                offsets.get_device() != dev or not slot_of.is_contiguous() or not offsets.is_contiguous()):
+            raise ValueError(f"slot_of, offsets: contiguous int32 on the rows' device, for each of the {rows} rows")
         s.slot_of = slot_of.data_ptr()
         s.in_use = offsets.data_ptr() + 4 * (offsets.numel() - 1)
     return s
@@ -290,6 +294,8 @@ def clip_grad_norm(grads: Sequence, max_norm: float, outs: Optional[Sequence] = 
     table = array.array("q", [v for entry in zip(ptrs, to, ns, kinds) for v in entry])
     if ws is None:
         ws = t.empty(moe_clip_workspace_size(len(grads)), dtype=t.uint8, device=grads[0].device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: contiguous scratch on the gradients' device is needed")
     norm = t.empty((), dtype=t.float32, device=grads[0].device)
     _call("moe_clip_grad_norm", dev, lib.moe_clip_grad_norm, len(grads), table.buffer_info()[0], max_norm,
           norm.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())

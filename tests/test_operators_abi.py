@@ -27,7 +27,7 @@ def norm_args(**kw):
     (dict(x=None), {}, ARG), (dict(weight=None), {}, ARG), (dict(y=None), {}, ARG), (dict(codes=P), {}, ARG),
     (dict(scales=P), {}, ARG), (dict(h=P), {}, ARG), (dict(ldx=255), {}, ARG), (dict(ldy=0), {}, ARG),
     (dict(residual=P, ldr=100), {}, ARG), (dict(residual=P, h=P, ldh=-256), {}, ARG),
-    ({}, dict(rows=-1), ARG), ({}, dict(H=0), ARG), ({}, dict(H=(1 << 20) + 1), ARG), ({}, dict(dtype=2), ARG),
+    ({}, dict(rows=-1), ARG), ({}, dict(rows=2 ** 31 - 1), ARG), ({}, dict(H=0), ARG), ({}, dict(H=(1 << 20) + 1), ARG), ({}, dict(dtype=2), ARG),
     ({}, dict(dtype=-1), ARG), ({}, dict(quant=3), ARG), ({}, dict(quant=-1), ARG), ({}, dict(eps=-1e-6), ARG),
     ({}, dict(eps=float("nan")), ARG), ({}, dict(eps=float("inf")), ARG), ({}, dict(quant=1), ARG),
     (dict(codes=P), dict(quant=1), ARG), (dict(scales=P), dict(quant=2), ARG),
@@ -110,7 +110,7 @@ def sorted_args(**kw):
 
 
 @pytest.mark.parametrize("change,want", [
-    (dict(T=-1), ARG), (dict(k=0), ARG), (dict(k=33), ARG), (dict(H=0), ARG), (dict(dtype=2), ARG), (dict(rows=-1), ARG),
+    (dict(T=-1), ARG), (dict(k=0), ARG), (dict(k=33), ARG), (dict(H=0), ARG), (dict(H=(1 << 20) + 1), ARG), (dict(dtype=2), ARG), (dict(rows=-1), ARG),
     (dict(rows=1 << 31), ARG), (dict(row_of=None), ARG), (dict(row_of=P + 4), ALIGN),
     (dict(T=1 << 30, k=2), ARG)])
 def test_movers_refuse_a_bad_index(lib, change, want):
