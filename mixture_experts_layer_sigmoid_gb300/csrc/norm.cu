@@ -732,6 +732,14 @@ void launch_fwd_width(const FwdArgs<T>& a, cudaStream_t s)
             else return launch_held<T, V, P / 2, 512, QUANT>(a, rows, s);
         }
     }
+    if constexpr (WHOLE) {
+        // 4000 x 13568 bf16 with residual: 65.0 us, 67.2 with 512 threads, 69.5 in the ring;
+        // 4000 x 16384 to blockwise codes: 79 us with 512 threads, 108 with 1024, 106 in the ring
+        if (a.H <= 16384) {
+            if constexpr (QUANT == MOE_NORM_PLAIN) return launch_held<T, V, P / 2, 1024, QUANT>(a, rows, s);
+            else return launch_held<T, V, P, 512, QUANT>(a, rows, s);
+        }
+    }
     if (!launch_fwd_ring<T, !WHOLE, QUANT>(a, s)) norm_fwd_loop_kernel<T, V, QUANT><<<rows, kNormThreads, 0, s>>>(a);
 }
 
@@ -771,9 +779,9 @@ moe_status_t fwd(int rows, int H, int quant, float eps, const moe_norm_fwd_args_
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Whether the backward gives a row to a warp: narrow rows, and enough of them
-// that every warp has one (else the block's threads share the row's chain).
-bool warp_rows(int rows, int H) { return H <= 256 || (H <= 1024 && rows >= 8 * kNormParts); }
+// Widths of which the backward gives a row to a warp: 32768 x 512 bf16 takes 26
+// us with a warp and 54 with a block per row, 400 x 512 4.3 and 4.8 us.
+constexpr int kWarpH = 1024;
 
 template <typename T, int V, int N, int GROUP, int NT>
 void launch_ring(const BwdArgs<T>& a, int parts, cudaStream_t s)
@@ -790,7 +798,7 @@ void launch_bwd_width(const BwdArgs<T>& a, int parts, cudaStream_t s)
     if constexpr (V * sizeof(T) >= 4) {
         constexpr int P = 32 / V;            // pieces of 32 values
         if (a.H <= 256) return launch_ring<T, V, P / 4, 32, 256>(a, parts, s);
-        if (warp_rows(a.rows, a.H)) return launch_ring<T, V, P, 32, 256>(a, parts, s);
+        if (a.H <= kWarpH) return launch_ring<T, V, P, 32, 256>(a, parts, s);
         if (a.H <= 2048) return launch_ring<T, V, P / 4, 256, 256>(a, parts, s);
         if (a.H <= 4096) return launch_ring<T, V, P / 2, 256, 256>(a, parts, s);
         if (a.H <= 8192 && sizeof(T) == 2) return launch_ring<T, V, P, 256, 256>(a, parts, s);
@@ -824,7 +832,7 @@ moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cud
     st[n++] = g.lddx;
     const int bytes = access_bytes(H, (int)sizeof(T), st, n);
     // a block of the warp-a-row kernel takes eight rows at a time
-    const int parts = norm_parts(warp_rows(rows, H) && bytes >= 4 ? (rows + 7) / 8 : rows);
+    const int parts = norm_parts(H <= kWarpH && bytes >= 4 ? (rows + 7) / 8 : rows);
     if (rows > 0) {
         if (bytes == 16) launch_bwd_width<T, 16 / (int)sizeof(T)>(a, parts, s);
         else if (bytes == 4) launch_bwd_width<T, 4 / (int)sizeof(T)>(a, parts, s);

@@ -224,18 +224,21 @@ struct IndexArgs {
     const int32_t* row_of; const int32_t* slot_of; const int32_t* in_use;
 };
 
-// Zeros in the padding rows among [r0, r0 + kPadRows).
+// Zeros in the padding rows among [r0, r0 + kPadRows): every warp looks at all of
+// their slots at once.
 template <typename T, int V>
 __device__ __forceinline__ void zero_padding(const IndexArgs& ix, T* buf, long long ld, long long r0)
 {
     const long long used = *ix.in_use < ix.rows ? *ix.in_use : ix.rows;
+    const int lane = threadIdx.x & 31;
+    const bool padding = lane < kPadRows && r0 + lane < ix.rows && ix.slot_of[r0 + lane] < 0 && r0 + lane < used;
     float z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) z[i] = 0.f;
-    for (long long r = r0; r < r0 + kPadRows && r < used; ++r) {
-        if (ix.slot_of[r] >= 0) continue;
+    for (unsigned m = __ballot_sync(0xffffffffu, padding); m; m &= m - 1) {
+        T* row = buf + (r0 + __ffs(m) - 1) * ld;
         for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * V; c < ix.H; c += gridDim.y * blockDim.x * V)
-            store_vec<T, V>(buf + r * ld + c, z);
+            store_vec<T, V>(row + c, z);
     }
 }
 
