@@ -112,36 +112,28 @@ __device__ __forceinline__ void quantise(const float (&v)[V], bool act, int row,
                                          uint8_t* codes, void* scales)
 {
     constexpr int BLOCK = QUANT == MOE_NORM_MXFP8 ? 32 : 128;
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) a = fmaxf(a, fabsf(v[i]));
+    float a = max_abs(v);
 #pragma unroll
     for (int off = BLOCK / V / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
     if (!act) return;
     float q[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = v[i];
     if constexpr (QUANT == MOE_NORM_MXFP8) {
         const int e = mx_exp(a);
-        const float s = mx_inv(e);                       // a power of two: exact
-#pragma unroll
-        for (int i = 0; i < V; ++i) q[i] = v[i] * s;
+        scale_vec(q, mx_inv(e));                         // a power of two: exact
         if (c % BLOCK == 0)
             static_cast<uint8_t*>(scales)[((size_t)(row >> 7) * (H / 128) + c / 128) * 512 +
                                           atom_byte(row & 127, (c / 32) & 3)] = (uint8_t)(e + 127);
     } else {
         const float t = __fdiv_rn(a, 448.f);
         const float s = t == 0.f ? 1.f : t;              // zero, or too small for a scale
-        if (s >= 0x1p-112f && s < 0x1p100f) {
-            // v / s from the rounded reciprocal and one correction of the product by
-            // its remainder (P. Markstein, IBM J. Res. Dev. 34(1), 1990): within an
-            // ulp of the quotient, nearly always equal to it, where an 8-bit code
-            // only needs 2^-5; a division per value took half of the kernel's time
-            const float r = __frcp_rn(s);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float y = v[i] * r;
-                q[i] = fmaf(fmaf(-s, y, v[i]), r, y);
-            }
-        } else {                                         // the remainder could underflow
+        if (s >= 0x1p-126f) {
+            // the quotient as a product with the rounded reciprocal: within 2^-23 of
+            // it, so a code differs from the quotient's only that near to a tie of
+            // two codes 2^-3 apart; a division per value took half of the kernel's time
+            scale_vec(q, __frcp_rn(s));
+        } else {                                         // the reciprocal could overflow
 #pragma unroll
             for (int i = 0; i < V; ++i) q[i] = __fdiv_rn(v[i], s);
         }
@@ -220,9 +212,9 @@ norm_fwd_loop_kernel(FwdArgs<T> a)
 // One row per group (GROUP = 32: a warp; else the block, of at most GROUP
 // threads), held in registers between the sum and the output: each value is
 // read once. N pieces of V values per thread cover the row.
-// 8192 x 7168 bf16 with residual: 70.7 us, 98%; 16384 x 4096 to MXFP8 codes and
-// bf16: 89.8 us, 99%. 52 and 32 registers leave four and eight blocks an SM,
-// whose loads cover one another's sums.
+// 8192 x 7168 bf16 with residual: 70.5 us, 98%; 16384 x 4096 to MXFP8 codes and
+// bf16: 89.8 us, 99%. At 48 registers five blocks of 224 threads fit an SM, and
+// their loads cover one another's sums.
 // AHEAD fetches the weights with the row, for launches of few rows, whose time
 // is the chain of loads.
 template <typename T, int V, int N, int GROUP, int QUANT, bool AHEAD = false>
@@ -241,10 +233,12 @@ norm_fwd_kernel(FwdArgs<T> a)
     }
     const T* x = a.x + row * a.ldx;
     const T* r = a.r ? a.r + row * a.ldr : nullptr;
-    Raw<T, V> qx[N], qr[N];
+    Raw<T, V> qx[N], qr[N];                  // zeros past the row's end
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = (tid + i * step) * V;
+        qx[i] = Raw<T, V>{};
+        qr[i] = Raw<T, V>{};
         if (c < a.H) {
             qx[i] = load_raw<T, V>(x + c);
             if (r) qr[i] = load_raw<T, V>(r + c);
@@ -259,26 +253,18 @@ norm_fwd_kernel(FwdArgs<T> a)
         }
     }
     float v[N][V];
-    float ss = 0.f;
+    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const bool act = (tid + i * step) * V < a.H;
-        if (act) {
-            unpack<T, V>(qx[i], v[i]);
-            if (r) {
-                float u[V];
-                unpack<T, V>(qr[i], u);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[i][j] += u[j];
-            }
+        unpack<T, V>(qx[i], v[i]);
+        if (r) {
+            float u[V];
+            unpack<T, V>(qr[i], u);
+            add_vec(v[i], u);
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            v[i][j] = act ? v[i][j] : 0.f;
-            ss = fmaf(v[i][j], v[i][j], ss);
-        }
+        add_squares(v[i], s0, s1);
     }
-    const float rstd = rsqrtf(block_sum<GROUP>(ss, red) / (float)a.H + a.eps);
+    const float rstd = rsqrtf(block_sum<GROUP>(s0 + s1, red) / (float)a.H + a.eps);
     if (tid == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -288,8 +274,8 @@ norm_fwd_kernel(FwdArgs<T> a)
             float w[V];
             if (a.h) store_vec<T, V>(a.h + row * a.ldh + c, v[i]);
             if constexpr (!AHEAD) load_f32<V>(a.w + c, w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * rstd * (AHEAD ? wa[AHEAD ? i : 0][j] : w[j]);
+            scale_vec(v[i], rstd);
+            mul_vec(v[i], AHEAD ? wa[AHEAD ? i : 0] : w);
             if (a.y) store_vec<T, V>(a.y + row * a.ldy + c, v[i]);
         }
         if constexpr (QUANT != MOE_NORM_PLAIN) quantise<QUANT, V>(v[i], act, (int)row, c, a.H, a.codes, a.scales);
@@ -299,7 +285,7 @@ norm_fwd_kernel(FwdArgs<T> a)
 // One row per block at a time, the next rows' x and residual on their way into
 // a ring of S staged rows. Without WINDOW a thread reads back only what it
 // copied itself, so the row's sum is the only barrier. 4308 x 5259 bf16 (odd
-// rows): 32.8 us, 41%, bound by issue at about 35 instructions per 32 values (77
+// rows): 32.7 us, 41%, bound by issue at about 35 instructions per 32 values (77
 // us held in registers one value at a time, whose loads were the wait).
 constexpr int kWideThreads = 512;
 template <typename T, bool WINDOW, bool RES, int QUANT, int S>
@@ -336,20 +322,18 @@ norm_fwd_ring_kernel(FwdArgs<T> a)
             if constexpr (RES) {
                 float u[V];
                 R::get(br, i * (kWideThreads * V * SIZE), u);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] += u[j];
+                add_vec(v, u);
             }
         };
         const int own = (a.H - tid * V + kWideThreads * V - 1) / (kWideThreads * V);   // pieces of this thread
-        float ss = 0.f;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll U
         for (int i = 0; i < own; ++i) {
             float v[V];
             value(i, v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) ss = fmaf(v[j], v[j], ss);
+            add_squares(v, s0, s1);
         }
-        const float rstd = rsqrtf(block_sum<kWideThreads>(ss, red[parity]) / (float)a.H + a.eps);
+        const float rstd = rsqrtf(block_sum<kWideThreads>(s0 + s1, red[parity]) / (float)a.H + a.eps);
         parity ^= 1;
         if (tid == 0 && a.rstd) a.rstd[row] = rstd;
         const float* w = a.w + tid * V;
@@ -368,8 +352,8 @@ norm_fwd_ring_kernel(FwdArgs<T> a)
                 value(i, v);
                 if (RES && h) store_vec<T, V>(h + at, v);
                 load_f32<V>(w + at, wv);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = v[j] * rstd * wv[j];
+                scale_vec(v, rstd);
+                mul_vec(v, wv);
                 if (QUANT == MOE_NORM_PLAIN || y) store_vec<T, V>(y + at, v);
             }
             if constexpr (QUANT != MOE_NORM_PLAIN) quantise<QUANT, V>(v, act, (int)row, at + tid * V, a.H, a.codes, a.scales);
@@ -746,6 +730,14 @@ void launch_fwd_width(const FwdArgs<T>& a, cudaStream_t s)
     if (a.H <= 512) return launch_held<T, V, P / 2, 32, QUANT>(a, rows, s);
     // few rows: a thread per eight values shortens each row's own chain
     if (a.H <= 8192 && a.rows <= kFewRows) return launch_held<T, V, P / 4, 1024, QUANT, true>(a, rows, s);
+    // many rows to 8-bit codes are bound by issue: more pieces per thread share what
+    // a warp does once (16384 x 2048 bf16 to MXFP8 codes 24.8 us, 30.8 with a thread
+    // per eight values; 300 x 4096 3.4 us, 4.3 with one per 32)
+    if constexpr (QUANT != MOE_NORM_PLAIN && sizeof(T) == 2)
+        if (a.rows >= 8 * kSms && a.H <= 4096) {
+            if (a.H <= 2048) return launch_held<T, V, P / 2, 256, QUANT>(a, rows, s);
+            return launch_held<T, V, P, 256, QUANT>(a, rows, s);
+        }
     if (a.H <= 1024) return launch_held<T, V, P / 4, 128, QUANT>(a, rows, s);
     if constexpr (!ODD) {                    // single 2-byte values are staged from here on
         if (a.H <= 2048) return launch_held<T, V, P / 4, 256, QUANT>(a, rows, s);

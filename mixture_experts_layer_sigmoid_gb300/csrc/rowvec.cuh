@@ -97,6 +97,83 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[V])
     store_raw<T, V>(p, pack<T, V>(v));
 }
 
+// Element-wise fp32 operations on a piece, two values to an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+// v *= w
+template <int V>
+__device__ __forceinline__ void mul_vec(float (&v)[V], const float (&w)[V])
+{
+    if constexpr (V == 1) {
+        v[0] *= w[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            uint64_t d;
+            asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(v[i], v[i + 1])), "l"(pair(w[i], w[i + 1])));
+            unpair(d, v[i], v[i + 1]);
+        }
+    }
+}
+// v *= s
+template <int V>
+__device__ __forceinline__ void scale_vec(float (&v)[V], float s)
+{
+    float w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = s;
+    mul_vec(v, w);
+}
+// v += u
+template <int V>
+__device__ __forceinline__ void add_vec(float (&v)[V], const float (&u)[V])
+{
+    if constexpr (V == 1) {
+        v[0] += u[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            uint64_t d;
+            asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(v[i], v[i + 1])), "l"(pair(u[i], u[i + 1])));
+            unpair(d, v[i], v[i + 1]);
+        }
+    }
+}
+// (s0, s1) += sums of v^2 over the even and the odd values
+template <int V>
+__device__ __forceinline__ void add_squares(const float (&v)[V], float& s0, float& s1)
+{
+    if constexpr (V == 1) {
+        s0 = fmaf(v[0], v[0], s0);
+    } else {
+        uint64_t s = pair(s0, s1);
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const uint64_t p = pair(v[i], v[i + 1]);
+            asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(s) : "l"(p));
+        }
+        unpair(s, s0, s1);
+    }
+}
+// largest magnitude
+template <int V>
+__device__ __forceinline__ float max_abs(const float (&v)[V])
+{
+    float a = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i + 1 < V; i += 2) asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(v[i]), "f"(v[i + 1]));
+    if constexpr (V % 2 == 0) a = fmaxf(a, fabsf(v[V - 1]));
+    return a;
+}
+
 // V consecutive fp32 values that start on a V-value boundary of an aligned
 // array (V = 8: two 16-byte loads; V = 2: 8 bytes)
 template <int V>
