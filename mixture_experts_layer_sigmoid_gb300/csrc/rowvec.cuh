@@ -4,8 +4,8 @@
 //
 // The access width of a launch follows from its pointers and row strides:
 // 16 bytes when every row starts on a 16-byte boundary and H is a whole number
-// of such pieces, else (sort.cu) 8 and 4 bytes on the same terms, else single
-// values.
+// of such pieces; otherwise norm.cu takes 4 bytes on the same terms, or single
+// values, and sort.cu shifts 16-byte pieces into place.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -17,7 +17,6 @@ namespace moe {
 
 template <int BYTES> struct RawOf;
 template <> struct RawOf<16> { using type = uint4; };
-template <> struct RawOf<8> { using type = uint2; };
 template <> struct RawOf<4> { using type = uint32_t; };
 template <> struct RawOf<2> { using type = uint16_t; };
 template <typename T, int V> using Raw = typename RawOf<V * (int)sizeof(T)>::type;
@@ -29,8 +28,6 @@ __device__ __forceinline__ void unpack(const Raw<T, V>& q, float (&v)[V])
         if constexpr (V == 4) {
             v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
             v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
-        } else if constexpr (V == 2) {
-            v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
         } else {
             v[0] = __uint_as_float(q);
         }
@@ -39,7 +36,6 @@ __device__ __forceinline__ void unpack(const Raw<T, V>& q, float (&v)[V])
     } else {
         uint32_t w[V / 2];
         if constexpr (V == 8) { w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w; }
-        else if constexpr (V == 4) { w[0] = q.x; w[1] = q.y; }
         else w[0] = q;
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
@@ -57,8 +53,6 @@ __device__ __forceinline__ Raw<T, V> pack(const float (&v)[V])
         if constexpr (V == 4)
             return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                               __float_as_uint(v[3]));
-        else if constexpr (V == 2)
-            return make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1]));
         else
             return __float_as_uint(v[0]);
     } else if constexpr (V == 1) {
@@ -71,7 +65,6 @@ __device__ __forceinline__ Raw<T, V> pack(const float (&v)[V])
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
         if constexpr (V == 8) return make_uint4(w[0], w[1], w[2], w[3]);
-        else if constexpr (V == 4) return make_uint2(w[0], w[1]);
         else return w[0];
     }
 }
@@ -207,13 +200,12 @@ __device__ __forceinline__ void store_f32(float* p, const float (&v)[V])
 }
 
 // Bytes of one access for rows of H values with the given strides (in
-// elements, every base pointer 16-byte aligned): 16, 8 (if `eight`), 4, or one
-// value.
-inline int access_bytes(int H, int size, const long long* strides, int n, bool eight = false)
+// elements, every base pointer 16-byte aligned): 16, 4, or one value.
+inline int access_bytes(int H, int size, const long long* strides, int n)
 {
-    for (int b : {16, 8, 4}) {
+    for (int b : {16, 4}) {
         if (b <= size) break;
-        bool ok = (b != 8 || eight) && (long long)H * size % b == 0;
+        bool ok = (long long)H * size % b == 0;
         for (int i = 0; i < n; ++i) ok = ok && strides[i] * size % b == 0;
         if (ok) return b;
     }

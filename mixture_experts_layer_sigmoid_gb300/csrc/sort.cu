@@ -63,7 +63,7 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
     __shared__ int wsum[kIndexWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
     const int rank = CLUSTER ? (int)ptx::cluster_ctarank() : 0, cluster = CLUSTER ? (int)ptx::cluster_id_x() : 0;
-    const int clusters = CLUSTER ? (int)ptx::nclusters_x() : 1, blocks = gridDim.x / clusters;
+    const int clusters = CLUSTER ? (int)ptx::nclusters_x() : 1;
     const long long lo = ((long long)rank * warps + warp) * per;      // slots [lo, lo + per) of this warp
     const long long left = n - lo;
     const int mine_n = warp < warps && left > 0 ? (left < per ? (int)left : per) : 0;
@@ -236,21 +236,77 @@ struct IndexArgs {
     const int32_t* row_of; const int32_t* slot_of; const int32_t* in_use;
 };
 
+// Pieces of 16 bytes. When every row starts on a 16-byte boundary and is a whole
+// number of them (SHIFT false) a piece moves as it lies. Else pieces are cut at
+// the destination's boundaries, and a source is read as the two aligned pieces
+// around each, shifted together. The shift is the same along a row, so it costs
+// a few instructions and no divergence. The columns before the first such piece
+// and after the last whose two source pieces lie in the row (at most three
+// pieces' worth) are moved by one lane each. 8192 x 8 rows of 4095 bf16 combine
+// in 111 us (89%; 192 in 2-byte accesses, of 4098 148 in 4-byte ones), their
+// gradient takes 273 (415, 266), 8634 x 8 rows of 3033 go out in 97 with their
+// index (145).
+template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);
+
+// How a row of H columns is cut at its own boundaries: whole pieces begin at
+// columns head, head + V, ... (n of them), `edges` columns lie around them.
+struct Cut { int head, n, edges; };
+template <typename T>
+__device__ __forceinline__ Cut cut_row(const T* row, int H)
+{
+    constexpr int V = kPiece<T>;
+    const int below = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    Cut c;
+    c.head = below ? V - below : 0;
+    c.n = H - V >= c.head + V ? (H - V - c.head) / V : 0;    // the last one's second source piece ends in the row
+    if (c.n == 0) c.head = 0;                                // a narrow row is all edges
+    c.edges = H - c.n * V;
+    return c;
+}
+// Column of the e-th edge.
+template <typename T>
+__device__ __forceinline__ int edge_column(const Cut& c, int e) { return e < c.head ? e : e + c.n * kPiece<T>; }
+
+struct Pair { uint4 lo, hi; };
+template <typename T>
+__device__ __forceinline__ Pair load_pair(const T* row, int c)
+{
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row + c) & ~(uintptr_t)15);
+    return Pair{p[0], p[1]};
+}
+// The 16 bytes at row + c out of its pair.
+template <typename T>
+__device__ __forceinline__ uint4 shifted(const Pair& q, const T* row, int c)
+{
+    const int sh = (int)(reinterpret_cast<uintptr_t>(row + c) & 15);
+    uint32_t w[8] = {q.lo.x, q.lo.y, q.lo.z, q.lo.w, q.hi.x, q.hi.y, q.hi.z, q.hi.w};
+#pragma unroll
+    for (int i = 0; i < 7; ++i) w[i] = sh & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = sh & 8 ? w[i + 2] : w[i];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = sh & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // Zeros in the padding rows among [r0, r0 + kPadRows): every warp looks at all of
 // their slots at once.
-template <typename T, int V>
+template <typename T, bool SHIFT>
 __device__ __forceinline__ void zero_padding(const IndexArgs& ix, T* buf, long long ld, long long r0)
 {
+    constexpr int V = kPiece<T>;
     const long long used = *ix.in_use < ix.rows ? *ix.in_use : ix.rows;
     const int lane = threadIdx.x & 31;
     const bool padding = lane < kPadRows && r0 + lane < ix.rows && ix.slot_of[r0 + lane] < 0 && r0 + lane < used;
-    float z[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) z[i] = 0.f;
     for (unsigned m = __ballot_sync(0xffffffffu, padding); m; m &= m - 1) {
         T* row = buf + (r0 + __ffs(m) - 1) * ld;
-        for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * V; c < ix.H; c += gridDim.y * blockDim.x * V)
-            store_vec<T, V>(row + c, z);
+        Cut cut{0, ix.H / V, 0};
+        if constexpr (SHIFT) cut = cut_row(row, ix.H);
+        for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < cut.n; i += gridDim.y * blockDim.x)
+            store_raw<T, V>(row + cut.head + i * V, make_uint4(0, 0, 0, 0));
+        if (SHIFT && blockIdx.y == 0)
+            for (int e = threadIdx.x; e < cut.edges; e += blockDim.x) store_raw<T, 1>(row + edge_column<T>(cut, e), 0);
     }
 }
 
@@ -268,26 +324,62 @@ __host__ __device__ constexpr int token_blocks(int T) { return (T + kMoveThreads
 // The first blocks: a token's row to its k rows, GROUP threads a token. The
 // blocks after them: padding rows. 16384 tokens x 8 rows of 4096 bf16 with 7.7k
 // padding rows: 197 us, 95% (nine tenths of it stores).
-template <typename T, int V, int KM, int GROUP>
+template <typename T, bool SHIFT, int KM, int GROUP>
 __global__ void __launch_bounds__(kMoveThreads)
 sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __restrict__ Xp, long long ldp)
 {
+    constexpr int V = kPiece<T>;
     if (blockIdx.x >= (unsigned)token_blocks<GROUP>(ix.T)) {
-        zero_padding<T, V>(ix, Xp, ldp, (long long)(blockIdx.x - token_blocks<GROUP>(ix.T)) * kPadRows);
+        zero_padding<T, SHIFT>(ix, Xp, ldp, (long long)(blockIdx.x - token_blocks<GROUP>(ix.T)) * kPadRows);
         return;
     }
     const int t = GROUP == 32 ? blockIdx.x * (kMoveThreads / 32) + threadIdx.x / 32 : blockIdx.x;
     const int tid = threadIdx.x % GROUP;
     if (t >= ix.T) return;
+    const T* src = x + (size_t)t * ldx;
     for (int j0 = 0; j0 < ix.k; j0 += KM) {
         int row[KM];
 #pragma unroll
         for (int j = 0; j < KM; ++j) row[j] = slot_row(ix, t, j0 + j);
-        for (int c = (blockIdx.y * GROUP + tid) * V; c < ix.H; c += gridDim.y * GROUP * V) {
-            const Raw<T, V> q = load_raw<T, V>(x + (size_t)t * ldx + c);
+        if constexpr (!SHIFT) {
+            for (int i = blockIdx.y * GROUP + tid; i < ix.H / V; i += gridDim.y * GROUP) {
+                const uint4 q = load_raw<T, V>(src + i * V);
 #pragma unroll
-            for (int j = 0; j < KM; ++j)
-                if (row[j] >= 0) store_raw<T, V>(Xp + row[j] * ldp + c, q);
+                for (int j = 0; j < KM; ++j)
+                    if (row[j] >= 0) store_raw<T, V>(Xp + row[j] * ldp + i * V, q);
+            }
+        } else {
+            for (int i = blockIdx.y * GROUP + tid; i <= ix.H / V; i += gridDim.y * GROUP) {
+                constexpr int B = KM < 4 ? KM : 4;           // rows loaded together
+#pragma unroll
+                for (int h = 0; h < KM; h += B) {
+                    Pair q[B];
+#pragma unroll
+                    for (int j = 0; j < B; ++j) {
+                        const Cut cut = cut_row(Xp + row[h + j] * ldp, ix.H);
+                        if (row[h + j] >= 0 && i < cut.n) q[j] = load_pair(src, cut.head + i * V);
+                    }
+#pragma unroll
+                    for (int j = 0; j < B; ++j) {
+                        T* dst = Xp + row[h + j] * ldp;
+                        const Cut cut = cut_row(dst, ix.H);
+                        const int c = cut.head + i * V;
+                        if (row[h + j] >= 0 && i < cut.n) store_raw<T, V>(dst + c, shifted(q[j], src, c));
+                    }
+                }
+            }
+            // lane e of a warp: the e-th edge of each of its rows
+            if (blockIdx.y == 0)
+                for (int j = tid / 32; j < KM; j += GROUP / 32) {
+                    const int r = slot_row(ix, t, j0 + j);
+                    if (r < 0) continue;
+                    T* dst = Xp + r * ldp;
+                    const Cut cut = cut_row(dst, ix.H);
+                    for (int e = tid % 32; e < cut.edges; e += 32) {
+                        const int c = edge_column<T>(cut, e);
+                        store_raw<T, 1>(dst + c, load_raw<T, 1>(src + c));
+                    }
+                }
         }
     }
 }
@@ -296,11 +388,12 @@ sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __rest
 // the index is read once per token. 8192 x 8 rows of 7168 bf16 with residual:
 // 165 us, 105% of the copy rate (mostly reads); the row numbers in 32 bits leave
 // 64 registers and seven blocks an SM (192 us with 88).
-template <typename T, int V, int KM, bool WHOLE, int GROUP>
+template <typename T, bool SHIFT, int KM, bool WHOLE, int GROUP>
 __global__ void __launch_bounds__(kMoveThreads)
 unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const float* __restrict__ gates,
                    const T* residual, long long ldr, T* y, long long ldy)
 {
+    constexpr int V = kPiece<T>;
     const int t = GROUP == 32 ? blockIdx.x * (kMoveThreads / 32) + threadIdx.x / 32 : blockIdx.x;
     const int tid = threadIdx.x % GROUP;
     if (t >= ix.T) return;
@@ -314,44 +407,82 @@ unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const 
         }
     };
     if (WHOLE) index(0);
-    for (int c = (blockIdx.y * GROUP + tid) * V; c < ix.H; c += gridDim.y * GROUP * V) {
+    T* out = y + (size_t)t * ldy;
+    const T* res_row = residual ? residual + (size_t)t * ldr : nullptr;
+    Cut cut{0, ix.H / V, 0};
+    if constexpr (SHIFT) {
+        cut = cut_row(out, ix.H);
+        if (blockIdx.y == 0)
+            for (int e = tid; e < cut.edges; e += GROUP) {
+                const int c = edge_column<T>(cut, e);
+                float v[1], acc[1] = {0.f};
+                if (residual) load_vec<T, 1>(res_row + c, acc);
+#pragma unroll 8
+                for (int j = 0; j < ix.k; ++j) {
+                    const int r = slot_row(ix, t, j);
+                    if (r < 0) continue;
+                    load_vec<T, 1>(Yp + r * ldp + c, v);
+                    acc[0] = fmaf(gates ? gates[(size_t)t * ix.k + j] : 1.f, v[0], acc[0]);
+                }
+                store_vec<T, 1>(out + c, acc);
+            }
+    }
+    for (int i = blockIdx.y * GROUP + tid; i < cut.n; i += gridDim.y * GROUP) {
+        const int c = cut.head + i * V;
         float acc[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        Raw<T, V> res;
-        if (residual) res = load_raw<T, V>(residual + (size_t)t * ldr + c);
+        for (int n = 0; n < V; ++n) acc[n] = 0.f;
+        Pair res2;
+        uint4 res;
+        if (residual) {
+            if constexpr (SHIFT) res2 = load_pair(res_row, c);
+            else res = load_raw<T, V>(res_row + c);
+        }
         for (int j0 = 0; j0 < (WHOLE ? 1 : ix.k); j0 += KM) {
             if (!WHOLE) index(j0);
-            Raw<T, V> q[KM];
+            constexpr int B = SHIFT && KM > 4 ? 4 : KM;      // rows loaded together
 #pragma unroll
-            for (int j = 0; j < KM; ++j)
-                if (row[j] >= 0) q[j] = load_raw<T, V>(Yp + row[j] * ldp + c);
-            if (j0 == 0 && residual) unpack<T, V>(res, acc);
+            for (int h = 0; h < KM; h += B) {
+                uint4 q[B];
+                Pair q2[SHIFT ? B : 1];
 #pragma unroll
-            for (int j = 0; j < KM; ++j) {
-                if (row[j] < 0) continue;
-                float v[V];
-                unpack<T, V>(q[j], v);
+                for (int j = 0; j < B; ++j)
+                    if (row[h + j] >= 0) {
+                        if constexpr (SHIFT) q2[j] = load_pair(Yp + row[h + j] * ldp, c);
+                        else q[j] = load_raw<T, V>(Yp + row[h + j] * ldp + c);
+                    }
+                if (j0 == 0 && h == 0 && residual) {
+                    if constexpr (SHIFT) res = shifted(res2, res_row, c);
+                    unpack<T, V>(res, acc);
+                }
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(g[j], v[i], acc[i]);
+                for (int j = 0; j < B; ++j) {
+                    if (row[h + j] < 0) continue;
+                    float v[V];
+                    if constexpr (SHIFT) q[j] = shifted(q2[j], Yp + row[h + j] * ldp, c);
+                    unpack<T, V>(q[j], v);
+#pragma unroll
+                    for (int n = 0; n < V; ++n) acc[n] = fmaf(g[h + j], v[n], acc[n]);
+                }
             }
         }
-        store_vec<T, V>(y + (size_t)t * ldy + c, acc);
+        store_vec<T, V>(out + c, acc);
     }
 }
 
 // The first blocks: dYp[row_j] = g_j dY[t] and dg_j = <dY[t], Yp[row_j]>, GROUP
 // (a warp, or NT) threads a token. The blocks after them: padding rows. 16384 x
 // 8 rows of 4096 bf16: 331 us with the padding, 100%.
-template <typename T, int V, int KM, int NT, int GROUP, bool DG>
+template <typename T, bool SHIFT, int KM, int NT, int GROUP, bool DG>
 __global__ void __launch_bounds__(NT, NT == kMoveThreads ? 6 : 1)
 unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const T* Yp, long long ldp,
                   const float* __restrict__ gates, T* dYp, long long ldd, float* __restrict__ dgates)
 {
+    constexpr int V = kPiece<T>;
     constexpr int TOKENS = NT / GROUP;       // of a block
     const int tb = (ix.T + TOKENS - 1) / TOKENS;
     if (blockIdx.x >= (unsigned)tb) {
-        zero_padding<T, V>(ix, dYp, ldd, (long long)(blockIdx.x - tb) * kPadRows);
+        zero_padding<T, SHIFT>(ix, dYp, ldd, (long long)(blockIdx.x - tb) * kPadRows);
         return;
     }
     __shared__ float red[NT / 32][KM];
@@ -367,33 +498,88 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
             g[j] = gates && j0 + j < ix.k ? gates[(size_t)t * ix.k + j0 + j] : 1.f;
             dot[j] = 0.f;
         }
-        for (int c = tid * V; c < ix.H; c += GROUP * V) {
-            float d[V];
-            load_vec<T, V>(dY + (size_t)t * lddy + c, d);
-            // four rows' loads at a time: with all eight in flight fewer blocks fit
-            // (347 against 339 us when this was measured)
-            constexpr int B = KM < 4 ? KM : 4;
+        const T* dy = dY + (size_t)t * lddy;
+        for (int i = tid; i < ix.H / V + (SHIFT ? 1 : 0); i += GROUP) {
+            if constexpr (!SHIFT) {
+                float d[V];
+                load_vec<T, V>(dy + i * V, d);
+                // four rows' loads at a time: with all eight in flight fewer blocks fit
+                // (347 against 339 us when this was measured)
+                constexpr int B = KM < 4 ? KM : 4;
 #pragma unroll
-            for (int h = 0; h < KM; h += B) {
-                Raw<T, V> q[B];
-                if constexpr (DG) {
-#pragma unroll
-                    for (int j = 0; j < B; ++j)
-                        if (row[h + j] >= 0) q[j] = load_raw<T, V>(Yp + row[h + j] * ldp + c);
-                }
-#pragma unroll
-                for (int j = 0; j < B; ++j) {
-                    if (row[h + j] < 0) continue;
-                    float o[V];
+                for (int h = 0; h < KM; h += B) {
+                    uint4 q[B];
                     if constexpr (DG) {
-                        float v[V];
-                        unpack<T, V>(q[j], v);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) dot[h + j] = fmaf(d[i], v[i], dot[h + j]);
+                        for (int j = 0; j < B; ++j)
+                            if (row[h + j] >= 0) q[j] = load_raw<T, V>(Yp + row[h + j] * ldp + i * V);
                     }
 #pragma unroll
-                    for (int i = 0; i < V; ++i) o[i] = g[h + j] * d[i];
-                    store_vec<T, V>(dYp + row[h + j] * ldd + c, o);
+                    for (int j = 0; j < B; ++j) {
+                        if (row[h + j] < 0) continue;
+                        float o[V];
+                        if constexpr (DG) {
+                            float v[V];
+                            unpack<T, V>(q[j], v);
+#pragma unroll
+                            for (int n = 0; n < V; ++n) dot[h + j] = fmaf(d[n], v[n], dot[h + j]);
+                        }
+#pragma unroll
+                        for (int n = 0; n < V; ++n) o[n] = g[h + j] * d[n];
+                        store_vec<T, V>(dYp + row[h + j] * ldd + i * V, o);
+                    }
+                }
+            } else {
+                constexpr int B = KM < 2 ? KM : 2;           // rows loaded together
+#pragma unroll
+                for (int h = 0; h < KM; h += B) {
+                    Pair qd[B], qy[DG ? B : 1];
+#pragma unroll
+                    for (int j = 0; j < B; ++j) {
+                        const Cut cut = cut_row(dYp + row[h + j] * ldd, ix.H);
+                        if (row[h + j] >= 0 && i < cut.n) {
+                            qd[j] = load_pair(dy, cut.head + i * V);
+                            if constexpr (DG) qy[j] = load_pair(Yp + row[h + j] * ldp, cut.head + i * V);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < B; ++j) {
+                        T* out = dYp + row[h + j] * ldd;
+                        const Cut cut = cut_row(out, ix.H);
+                        if (row[h + j] < 0 || i >= cut.n) continue;
+                        const int c = cut.head + i * V;
+                        float d[V];
+                        unpack<T, V>(shifted(qd[j], dy, c), d);
+                        if constexpr (DG) {
+                            float v[V];
+                            unpack<T, V>(shifted(qy[j], Yp + row[h + j] * ldp, c), v);
+#pragma unroll
+                            for (int n = 0; n < V; ++n) dot[h + j] = fmaf(d[n], v[n], dot[h + j]);
+                        }
+#pragma unroll
+                        for (int n = 0; n < V; ++n) d[n] *= g[h + j];
+                        store_vec<T, V>(out + c, d);
+                    }
+                }
+            }
+        }
+        if constexpr (SHIFT) {
+            // lane e of a warp: the e-th edge of each of its rows
+#pragma unroll
+            for (int j = 0; j < KM; ++j) {
+                if (row[j] < 0 || (GROUP != 32 && j % (GROUP / 32) != warp)) continue;
+                T* out = dYp + row[j] * ldd;
+                const Cut cut = cut_row(out, ix.H);
+                for (int e = lane; e < cut.edges; e += 32) {
+                    const int c = edge_column<T>(cut, e);
+                    float d[1], v[1];
+                    load_vec<T, 1>(dy + c, d);
+                    if constexpr (DG) {
+                        load_vec<T, 1>(Yp + row[j] * ldp + c, v);
+                        dot[j] = fmaf(d[0], v[0], dot[j]);
+                    }
+                    d[0] *= g[j];
+                    store_vec<T, 1>(out + c, d);
                 }
             }
         }
@@ -430,14 +616,15 @@ void with_slots(int k, F&& f)
     else if (k <= 4) f(std::integral_constant<int, 4>{});
     else f(std::integral_constant<int, kMaxSlots>{});
 }
-// Calls F with the values per access.
+// Calls F with whether rows have to be shifted: some stride or the width is not
+// a whole number of 16-byte pieces.
 template <typename T, typename F>
-void with_width(int bytes, F&& f)
+void with_shift(const moe_sorted_t& ix, std::initializer_list<long long> strides, F&& f)
 {
-    if (bytes == 16) f(std::integral_constant<int, 16 / (int)sizeof(T)>{});
-    else if (bytes == 8) f(std::integral_constant<int, 8 / (int)sizeof(T)>{});
-    else if (bytes == 4) f(std::integral_constant<int, 4 / (int)sizeof(T)>{});
-    else if constexpr (sizeof(T) == 2) f(std::integral_constant<int, 1>{});
+    bool whole = ix.H % kPiece<T> == 0;
+    for (long long ld : strides) whole = whole && ld % kPiece<T> == 0;
+    if (whole) f(std::false_type{});
+    else f(std::true_type{});
 }
 
 IndexArgs index_args(const moe_sorted_t& s)
@@ -451,15 +638,17 @@ unsigned move_grid(const moe_sorted_t& s, int token_blocks)
 }
 // Whether a token's row goes to a warp: few pieces, and enough tokens that the
 // larger blocks are not needed to fill the SMs.
-bool narrow(const moe_sorted_t& s, int V) { return s.H <= 32 * V * kNarrowPieces && s.T >= kFewTokens; }
+template <typename T>
+bool narrow(const moe_sorted_t& s) { return s.H <= 32 * kPiece<T> * kNarrowPieces && s.T >= kFewTokens; }
 
 using One = std::integral_constant<int, 32>;
 using Block = std::integral_constant<int, kMoveThreads>;
 
-// Column parts of a launch whose blocks take V values per thread at a time.
-unsigned column_parts(const moe_sorted_t& s, int V)
+// Column parts of a launch.
+template <typename T>
+unsigned column_parts(const moe_sorted_t& s)
 {
-    const int most = (s.H + kMoveThreads * V - 1) / (kMoveThreads * V);
+    const int part = kMoveThreads * kPiece<T>, most = (s.H + part - 1) / part;
     const int wanted = s.T > 0 ? (kFewTokens + s.T - 1) / s.T : 1;
     return (unsigned)(s.T >= kFewTokens ? 1 : (wanted < most ? wanted : most));
 }
@@ -467,17 +656,15 @@ unsigned column_parts(const moe_sorted_t& s, int V)
 template <typename T>
 void sort_rows(const moe_sorted_t& ix, const void* x, long long ldx, void* Xp, long long ldp, cudaStream_t s)
 {
-    const long long st[] = {ldx, ldp};
-    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, 2, true), [&](auto v) {
+    with_shift<T>(ix, {ldx, ldp}, [&](auto shift) {
         with_slots(ix.k, [&](auto km) {
-            constexpr int V = decltype(v)::value;
             auto launch = [&](auto group) {
                 constexpr int G = decltype(group)::value;
-                sort_rows_kernel<T, V, decltype(km)::value, G>
-                    <<<dim3(move_grid(ix, token_blocks<G>(ix.T)), column_parts(ix, V)), kMoveThreads, 0, s>>>(
+                sort_rows_kernel<T, decltype(shift)::value, decltype(km)::value, G>
+                    <<<dim3(move_grid(ix, token_blocks<G>(ix.T)), column_parts<T>(ix)), kMoveThreads, 0, s>>>(
                         index_args(ix), static_cast<const T*>(x), ldx, static_cast<T*>(Xp), ldp);
             };
-            if (narrow(ix, V)) launch(One{});
+            if (narrow<T>(ix)) launch(One{});
             else launch(Block{});
         });
     });
@@ -487,20 +674,19 @@ template <typename T>
 void unsort_rows(const moe_sorted_t& ix, const void* Yp, long long ldp, const float* gates, const void* residual,
                  long long ldr, void* y, long long ldy, cudaStream_t s)
 {
-    const long long st[] = {ldp, ldy, ldr};
-    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, residual ? 3 : 2, true), [&](auto v) {
+    with_shift<T>(ix, {ldp, ldy, residual ? ldr : ldy}, [&](auto shift) {
         with_slots(ix.k, [&](auto km) {
-            constexpr int V = decltype(v)::value, KM = decltype(km)::value;
+            constexpr int KM = decltype(km)::value;
             auto launch = [&](auto whole, auto group) {
                 constexpr int G = decltype(group)::value;
-                unsort_rows_kernel<T, V, KM, decltype(whole)::value, G>
-                    <<<dim3(token_blocks<G>(ix.T), column_parts(ix, V)), kMoveThreads, 0, s>>>(
+                unsort_rows_kernel<T, decltype(shift)::value, KM, decltype(whole)::value, G>
+                    <<<dim3(token_blocks<G>(ix.T), column_parts<T>(ix)), kMoveThreads, 0, s>>>(
                         index_args(ix), static_cast<const T*>(Yp), ldp, gates, static_cast<const T*>(residual), ldr,
                         static_cast<T*>(y), ldy);
             };
             if (ix.k > KM) {
                 if constexpr (KM == kMaxSlots) launch(std::false_type{}, Block{});
-            } else if (narrow(ix, V)) {
+            } else if (narrow<T>(ix)) {
                 launch(std::true_type{}, One{});
             } else {
                 launch(std::true_type{}, Block{});
@@ -513,20 +699,19 @@ template <typename T>
 void unsort_bwd(const moe_sorted_t& ix, const void* dY, long long lddy, const void* Yp, long long ldp,
                 const float* gates, void* dYp, long long ldd, float* dgates, cudaStream_t s)
 {
-    const long long st[] = {lddy, ldd, ldp};
-    with_width<T>(access_bytes(ix.H, (int)sizeof(T), st, dgates ? 3 : 2, true), [&](auto v) {
+    with_shift<T>(ix, {lddy, ldd, dgates ? ldp : ldd}, [&](auto shift) {
         with_slots(ix.k, [&](auto km) {
-            constexpr int V = decltype(v)::value, KM = decltype(km)::value;
+            constexpr int KM = decltype(km)::value;
             auto launch = [&](auto nt, auto group, auto dg) {
                 constexpr int NT = decltype(nt)::value, G = decltype(group)::value;
-                unsort_bwd_kernel<T, V, KM, NT, G, decltype(dg)::value>
+                unsort_bwd_kernel<T, decltype(shift)::value, KM, NT, G, decltype(dg)::value>
                     <<<move_grid(ix, (ix.T + NT / G - 1) / (NT / G)), NT, 0, s>>>(
                         index_args(ix), static_cast<const T*>(dY), lddy, static_cast<const T*>(Yp), ldp, gates,
                         static_cast<T*>(dYp), ldd, dgates);
             };
             using Large = std::integral_constant<int, 512>;
             if (!dgates) launch(Block{}, Block{}, std::false_type{});
-            else if (narrow(ix, V)) launch(Block{}, One{}, std::true_type{});
+            else if (narrow<T>(ix)) launch(Block{}, One{}, std::true_type{});
             else if (ix.T < kFewTokens / 2) launch(Large{}, Large{}, std::true_type{});
             else launch(Block{}, Block{}, std::true_type{});
         });
