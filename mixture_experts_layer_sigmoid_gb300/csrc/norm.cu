@@ -6,9 +6,9 @@
 //                                  dw = sum over rows of dy n
 //
 // About ten operations per value against 2 to 16 bytes moved: every kernel
-// here is bound by HBM (large inputs), by latency (a few rows), or, where single
-// 2-byte values are worked on (rows of odd widths) or only codes are written, by
-// instruction issue. Rates below are of the measured copy rate, 6.79 TB/s.
+// here is bound by HBM (large inputs), by latency (a few rows), or, where only
+// codes are written or rows start off the 16-byte boundaries, by instruction
+// issue. Rates below are of the measured copy rate, 6.79 TB/s.
 //
 // Roundings: sums, means, rstd, the weight and its gradient are fp32; y is
 // rounded once from fp32, h once from the fp32 sum, dx once; the 8-bit codes are
@@ -69,9 +69,9 @@ template <int LEFT>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // Rows staged whole in shared memory, for rows that are too wide for registers
-// or do not start on 16-byte boundaries (WINDOW: the 16-byte windows that cover
-// the row are copied, so any alignment moves in full accesses; values are then
-// taken one at a time at the row's place inside them).
+// or start each tensor in its own way (WINDOW: the 16-byte windows that cover the
+// row are copied, so any alignment moves in full accesses; values are then taken
+// one at a time at the row's place inside them).
 template <typename T, bool WINDOW>
 struct Staged {
     static constexpr int V = WINDOW ? 1 : 16 / (int)sizeof(T);
@@ -96,6 +96,20 @@ struct Staged {
         unpack<T, V>(*reinterpret_cast<const Raw<T, V>*>(buf + at), v);
     }
 };
+
+// The cut of row `row` of tensors whose rows start alike.
+template <typename T>
+__device__ __forceinline__ Cut cut_alike(const T* row, int H)
+{
+    constexpr int V = kPiece<T>;
+    const int below = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    Cut c;
+    c.head = below ? V - below : 0;
+    if (c.head > H) c.head = H;
+    c.n = (H - c.head) / V;
+    c.edges = H - c.n * V;
+    return c;
+}
 
 template <typename T> struct FwdArgs {
     const T* x; const T* r; const float* w;
@@ -217,10 +231,14 @@ norm_fwd_loop_kernel(FwdArgs<T> a)
 // their loads cover one another's sums.
 // AHEAD fetches the weights with the row, for launches of few rows, whose time
 // is the chain of loads.
-template <typename T, int V, int N, int GROUP, int QUANT, bool AHEAD = false>
+// SHIFT: rows start alike off the 16-byte boundaries. They are cut there; the
+// weights are shifted into place and thread e < 2 V holds the e-th edge column.
+// 4308 x 5259 bf16 (odd rows): 20.5 us, 65%, with residual 30.3 us, 88%.
+template <typename T, bool SHIFT, int N, int GROUP, int QUANT, bool AHEAD = false>
 __global__ void __launch_bounds__(GROUP == 32 ? kNormThreads : GROUP)
 norm_fwd_kernel(FwdArgs<T> a)
 {
+    constexpr int V = kPiece<T>;
     constexpr int NT = GROUP == 32 ? kNormThreads : GROUP;
     __shared__ float red[NT / 32];
     const int tid = GROUP == 32 ? threadIdx.x & 31 : threadIdx.x;
@@ -233,27 +251,39 @@ norm_fwd_kernel(FwdArgs<T> a)
     }
     const T* x = a.x + row * a.ldx;
     const T* r = a.r ? a.r + row * a.ldr : nullptr;
+    Cut cut{0, a.H / V, 0};
+    if constexpr (SHIFT) cut = cut_alike(x, a.H);
+    const bool edge = SHIFT && tid < cut.edges;
+    const int ec = SHIFT ? edge_column<T>(cut, tid) : 0;
+    auto load_w = [&](int c, float (&w)[V]) {
+        if constexpr (SHIFT) load_f32_at<V>(a.w, c, a.H, w);
+        else load_f32<V>(a.w + c, w);
+    };
     Raw<T, V> qx[N], qr[N];                  // zeros past the row's end
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (tid + i * step) * V;
+        const int p = tid + i * step, c = cut.head + p * V;
         qx[i] = Raw<T, V>{};
         qr[i] = Raw<T, V>{};
-        if (c < a.H) {
+        if (p < cut.n) {
             qx[i] = load_raw<T, V>(x + c);
             if (r) qr[i] = load_raw<T, V>(r + c);
         }
     }
+    float ev[1] = {0.f}, eu[1] = {0.f};
+    if (edge) {
+        load_vec<T, 1>(x + ec, ev);
+        if (r) load_vec<T, 1>(r + ec, eu);
+        ev[0] += eu[0];
+    }
     float wa[AHEAD ? N : 1][V];
     if constexpr (AHEAD) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = (tid + i * step) * V;
-            if (c < a.H) load_f32<V>(a.w + c, wa[i]);
-        }
+        for (int i = 0; i < N; ++i)
+            if (tid + i * step < cut.n) load_w(cut.head + (tid + i * step) * V, wa[i]);
     }
     float v[N][V];
-    float s0 = 0.f, s1 = 0.f;
+    float s0 = ev[0] * ev[0], s1 = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         unpack<T, V>(qx[i], v[i]);
@@ -266,14 +296,19 @@ norm_fwd_kernel(FwdArgs<T> a)
     }
     const float rstd = rsqrtf(block_sum<GROUP>(s0 + s1, red) / (float)a.H + a.eps);
     if (tid == 0 && a.rstd) a.rstd[row] = rstd;
+    if (edge) {
+        if (a.h) store_vec<T, 1>(a.h + row * a.ldh + ec, ev);
+        ev[0] = ev[0] * rstd * a.w[ec];
+        if (a.y) store_vec<T, 1>(a.y + row * a.ldy + ec, ev);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (tid + i * step) * V;
-        const bool act = c < a.H;
+        const int p = tid + i * step, c = cut.head + p * V;
+        const bool act = p < cut.n;
         if (act) {
             float w[V];
             if (a.h) store_vec<T, V>(a.h + row * a.ldh + c, v[i]);
-            if constexpr (!AHEAD) load_f32<V>(a.w + c, w);
+            if constexpr (!AHEAD) load_w(c, w);
             scale_vec(v[i], rstd);
             mul_vec(v[i], AHEAD ? wa[AHEAD ? i : 0] : w);
             if (a.y) store_vec<T, V>(a.y + row * a.ldy + c, v[i]);
@@ -284,9 +319,9 @@ norm_fwd_kernel(FwdArgs<T> a)
 
 // One row per block at a time, the next rows' x and residual on their way into
 // a ring of S staged rows. Without WINDOW a thread reads back only what it
-// copied itself, so the row's sum is the only barrier. 4308 x 5259 bf16 (odd
-// rows): 32.7 us, 41%, bound by issue at about 35 instructions per 32 values (77
-// us held in registers one value at a time, whose loads were the wait).
+// copied itself, so the row's sum is the only barrier. With WINDOW 4308 x 5259
+// bf16 takes 32.7 us, 41%, bound by issue at about 35 instructions per 32 values
+// (77 us held in registers one value at a time, whose loads were the wait).
 constexpr int kWideThreads = 512;
 template <typename T, bool WINDOW, bool RES, int QUANT, int S>
 __global__ void __launch_bounds__(kWideThreads, 3)
@@ -441,30 +476,40 @@ norm_bwd_loop_kernel(BwdArgs<T> a)
 // GROUP threads take a row (a warp, or the block); H <= GROUP * N * V.
 // 8192 x 7168 bf16 with dh: 75.5 us with the sum of the parts, 92% (197 us when
 // each row was loaded, summed and read again); bound by HBM, 71 us of it here.
-template <typename T, int V, int N, int GROUP, int NT>
+// SHIFT: rows start alike off the 16-byte boundaries. The number of groups is a
+// multiple of eight where a group has more than one row, so all of its rows are
+// cut in the same columns; thread e < 2 V holds the e-th edge column, fetched one
+// row ahead. 4308 x 5259 bf16: 40 us, 67%.
+template <int N, int NT>
 struct Ring {
-    static constexpr int kPiece = V * (int)sizeof(T);
-    static constexpr int kTensor = NT * N * kPiece;          // one tensor's rows of one stage
+    static constexpr int kTensor = NT * N * 16;              // one tensor's rows of one stage
     static constexpr int kStage = 3 * kTensor;
     // as many stages as fit beside a second block on the SM, at most 4
     static constexpr int kStages = kStage * 4 <= 104 * 1024 ? 4 : (kStage * 3 <= 104 * 1024 ? 3 : 2);
     static constexpr int kBytes = kStages * kStage;
 };
 
-template <typename T, int V, int N, int GROUP, int NT>
+static_assert(kNormParts % 8 == 0, "see SHIFT");
+template <typename T, bool SHIFT, int N, int GROUP, int NT>
 __global__ void __launch_bounds__(NT, NT <= 256 ? 2 : 1)
 norm_bwd_kernel(BwdArgs<T> a)
 {
-    using R = Ring<T, V, N, GROUP, NT>;
+    constexpr int V = kPiece<T>;
+    using R = Ring<N, NT>;
     constexpr int S = R::kStages;
     constexpr int GROUPS = NT / GROUP;
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float red[2][NT / 32];
     __shared__ float rs[S][NT / 32];
+    __shared__ int heads[NT / 32];
     const int tid = GROUP == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long first = GROUP == 32 ? (long long)blockIdx.x * GROUPS + warp : blockIdx.x;
     const long long step = (long long)gridDim.x * GROUPS;
+    Cut cut{0, a.H / V, 0};
+    if constexpr (SHIFT) cut = cut_alike(a.h + first * a.ldh, a.H);
+    const bool edge = SHIFT && tid < cut.edges;
+    const int ec = SHIFT ? edge_column<T>(cut, tid) : 0;
 
     auto slot = [&](int stage, int tensor, int i) {
         return reinterpret_cast<Raw<T, V>*>(ring + stage * R::kStage + tensor * R::kTensor) + i * NT + threadIdx.x;
@@ -473,11 +518,11 @@ norm_bwd_kernel(BwdArgs<T> a)
         if (row < a.rows) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int c = (tid + i * GROUP) * V;
-                if (c < a.H) {
-                    copy_async<R::kPiece>(slot(stage, 0, i), a.dy + row * a.lddy + c);
-                    copy_async<R::kPiece>(slot(stage, 1, i), a.h + row * a.ldh + c);
-                    if (a.dh) copy_async<R::kPiece>(slot(stage, 2, i), a.dh + row * a.lddh + c);
+                const int c = cut.head + (tid + i * GROUP) * V;
+                if (tid + i * GROUP < cut.n) {
+                    copy_async<16>(slot(stage, 0, i), a.dy + row * a.lddy + c);
+                    copy_async<16>(slot(stage, 1, i), a.h + row * a.ldh + c);
+                    if (a.dh) copy_async<16>(slot(stage, 2, i), a.dh + row * a.lddh + c);
                 }
             }
             if (lane == 0) copy_async<4>(&rs[stage][warp], a.rstd + row);
@@ -487,24 +532,53 @@ norm_bwd_kernel(BwdArgs<T> a)
 #pragma unroll
     for (int s = 0; s < S; ++s) fetch(s, first + s * step);
 
+    // the edge column's dy, h and dh of the next row, as loaded: nothing waits for
+    // them before that row's turn
+    Raw<T, 1> ng = 0, nh = 0, nd = 0;
+    float ew = 0.f, edw = 0.f;
+    auto fetch_edge = [&](long long row) {
+        if (edge && row < a.rows) {
+            ng = load_raw<T, 1>(a.dy + row * a.lddy + ec);
+            nh = load_raw<T, 1>(a.h + row * a.ldh + ec);
+            if (a.dh) nd = load_raw<T, 1>(a.dh + row * a.lddh + ec);
+        }
+    };
+    auto value = [](Raw<T, 1> q) {
+        float v[1];
+        unpack<T, 1>(q, v);
+        return v[0];
+    };
+    if constexpr (SHIFT) {
+        fetch_edge(first);
+        if (edge) ew = a.w[ec];
+    }
     float w[N][V], dw[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = (tid + i * GROUP) * V;
+        const int p = tid + i * GROUP, c = cut.head + p * V;
 #pragma unroll
         for (int j = 0; j < V; ++j) { w[i][j] = 0.f; dw[i][j] = 0.f; }
-        if (c < a.H) load_f32<V>(a.w + c, w[i]);
+        if (p < cut.n) {
+            if constexpr (SHIFT) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) w[i][j] = a.w[c + j];      // all of them in flight together
+            } else {
+                load_f32<V>(a.w + c, w[i]);
+            }
+        }
     }
     ptx::griddep_launch_dependents();
     int stage = 0, parity = 0;
     for (long long row = first; row < a.rows; row += step) {
+        const float eg = value(ng), eh = value(nh), ed = value(nd);
+        if constexpr (SHIFT) fetch_edge(row + step);
         copy_wait<S - 1>();
         __syncwarp();
         const float rstd = rs[stage][warp];
-        float d = 0.f;
+        float d = eg * ew * eh;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if ((tid + i * GROUP) * V >= a.H) break;
+            if (tid + i * GROUP >= cut.n) break;
             float g[V], v[V];
             unpack<T, V>(*slot(stage, 0, i), g);
             unpack<T, V>(*slot(stage, 1, i), v);
@@ -524,10 +598,16 @@ norm_bwd_kernel(BwdArgs<T> a)
         }
         const float m = d * rstd / (float)a.H;
         T* dx = a.dx + row * a.lddx;
+        if (edge) {
+            const float n = eh * rstd;
+            const float o[1] = {rstd * fmaf(-n, m, eg * ew) + ed};
+            edw = fmaf(eg, n, edw);
+            store_vec<T, 1>(dx + ec, o);
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = (tid + i * GROUP) * V;
-            if (c >= a.H) break;
+            const int c = cut.head + (tid + i * GROUP) * V;
+            if (tid + i * GROUP >= cut.n) break;
             float g[V], v[V], o[V];
             unpack<T, V>(*slot(stage, 0, i), g);
             unpack<T, V>(*slot(stage, 1, i), v);
@@ -552,33 +632,68 @@ norm_bwd_kernel(BwdArgs<T> a)
     copy_wait<0>();
     if (!a.part) return;
     float* part = a.part + (size_t)blockIdx.x * a.H;
+    auto put_dw = [&](float* to) {
+        if (edge) to[ec] = edw;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = tid + i * GROUP, c = cut.head + p * V;
+            if (p >= cut.n) break;
+            if constexpr (SHIFT) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) to[c + j] = dw[i][j];
+            } else {
+                store_f32<V>(to + c, dw[i]);
+            }
+        }
+    };
     if constexpr (GROUP == 32) {
         // the warps' sums, added in warp order
-        constexpr int W = GROUP * N * V;
+        constexpr int W = GROUP * N * V;                     // at least H
         static_assert(GROUPS * W * 4 <= R::kBytes, "the sums fit the ring");
         float* sum = reinterpret_cast<float*>(ring);
         __syncthreads();
+        if constexpr (!SHIFT) {
+            put_dw(sum + warp * W);
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.H; c += NT) {
+                float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) store_f32<V>(sum + warp * W + (tid + i * GROUP) * V, dw[i]);
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.H; c += NT) {
-            float t = 0.f;
+                for (int k = 0; k < GROUPS; ++k) t += sum[k * W + c];
+                part[c] = t;
+            }
+        } else {
+            // the warps' rows are cut in different columns. Value j of a lane's pieces
+            // goes to row j of the warp's table, whose stride keeps both the lanes'
+            // stores and the columns' reads on different banks; the edges behind it
+            constexpr int L = GROUP * N + 32 / V;
+            static_assert(GROUPS * (V * L + 32) * 4 <= R::kBytes, "the tables fit the ring");
+            float* mine = sum + warp * (V * L + 32);
 #pragma unroll
-            for (int k = 0; k < GROUPS; ++k) t += sum[k * W + c];
-            part[c] = t;
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) mine[j * L + tid + i * GROUP] = dw[i][j];
+            mine[V * L + tid] = edw;
+            if (lane == 0) heads[warp] = cut.head;
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.H; c += NT) {
+                float t = 0.f;
+#pragma unroll
+                for (int k = 0; k < GROUPS; ++k) {
+                    const int head = heads[k], n = (a.H - head) / V * V, at = c - head;
+                    const float* table = sum + k * (V * L + 32);
+                    t += at < 0 ? table[V * L + c] : (at < n ? table[at % V * L + at / V] : table[V * L + c - n]);
+                }
+                part[c] = t;
+            }
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = (tid + i * GROUP) * V;
-            if (c < a.H) store_f32<V>(part + c, dw[i]);
-        }
+        put_dw(part);
     }
 }
 
-// The same for rows of any alignment, staged whole (as in the forward's ring);
-// dw is summed in shared memory, each column by one thread. 4308 x 5259 bf16:
-// 68 us, 39%, bound by issue.
+// The same for rows that start each tensor in its own way, staged whole (as in
+// the forward's ring); dw is summed in shared memory, each column by one thread.
+// 4308 x 5259 bf16 takes 68 us, 39%, bound by issue, where the ring takes 40.
 template <typename T, bool DH, int S>
 __global__ void __launch_bounds__(kWideThreads)
 norm_bwd_window_kernel(BwdArgs<T> a)
@@ -709,64 +824,60 @@ bool launch_fwd_ring(const FwdArgs<T>& a, cudaStream_t s)
 }
 
 // The held kernel with N pieces per thread and as many threads as that takes.
-template <typename T, int V, int N, int GROUP, int QUANT, bool AHEAD = false>
+template <typename T, bool SHIFT, int N, int GROUP, int QUANT, bool AHEAD = false>
 void launch_held(const FwdArgs<T>& a, int rows, cudaStream_t s)
 {
     if constexpr (GROUP == 32) {
-        norm_fwd_kernel<T, V, N, 32, QUANT><<<(rows + kNormThreads / 32 - 1) / (kNormThreads / 32), kNormThreads, 0, s>>>(a);
+        norm_fwd_kernel<T, SHIFT, N, 32, QUANT><<<(rows + kNormThreads / 32 - 1) / (kNormThreads / 32), kNormThreads, 0, s>>>(a);
     } else {
-        const int pieces = (a.H + V - 1) / V, threads = (pieces + N - 1) / N;
-        norm_fwd_kernel<T, V, N, GROUP, QUANT, AHEAD><<<rows, (threads + 31) / 32 * 32, 0, s>>>(a);
+        const int pieces = (a.H + kPiece<T> - 1) / kPiece<T>, threads = (pieces + N - 1) / N;
+        norm_fwd_kernel<T, SHIFT, N, GROUP, QUANT, AHEAD><<<rows, (threads + 31) / 32 * 32, 0, s>>>(a);
     }
 }
 
-template <typename T, int V, int QUANT>
-void launch_fwd_width(const FwdArgs<T>& a, cudaStream_t s)
+// Rows that start whole, or alike (SHIFT).
+template <typename T, bool SHIFT, int QUANT>
+void launch_fwd_cut(const FwdArgs<T>& a, cudaStream_t s)
 {
-    constexpr int P = 32 / V;                // pieces of 32 values
-    constexpr bool WHOLE = V * sizeof(T) == 16, ODD = V * sizeof(T) == 2;
+    constexpr int P = 32 / kPiece<T>;        // pieces of 32 values
     const int rows = QUANT == MOE_NORM_MXFP8 ? (a.rows + 127) / 128 * 128 : a.rows;
-    if (a.H <= 256) return launch_held<T, V, P / 4, 32, QUANT>(a, rows, s);
-    if (a.H <= 512) return launch_held<T, V, P / 2, 32, QUANT>(a, rows, s);
+    if (a.H <= 256) return launch_held<T, SHIFT, P / 4, 32, QUANT>(a, rows, s);
+    if (a.H <= 512) return launch_held<T, SHIFT, P / 2, 32, QUANT>(a, rows, s);
     // few rows: a thread per eight values shortens each row's own chain
-    if (a.H <= 8192 && a.rows <= kFewRows) return launch_held<T, V, P / 4, 1024, QUANT, true>(a, rows, s);
+    if (a.H <= 8192 && a.rows <= kFewRows) return launch_held<T, SHIFT, P / 4, 1024, QUANT, true>(a, rows, s);
     // many rows to 8-bit codes are bound by issue: more pieces per thread share what
     // a warp does once (16384 x 2048 bf16 to MXFP8 codes 24.8 us, 30.8 with a thread
     // per eight values; 300 x 4096 3.4 us, 4.3 with one per 32)
     if constexpr (QUANT != MOE_NORM_PLAIN && sizeof(T) == 2)
         if (a.rows >= 8 * kSms && a.H <= 4096) {
-            if (a.H <= 2048) return launch_held<T, V, P / 2, 256, QUANT>(a, rows, s);
-            return launch_held<T, V, P, 256, QUANT>(a, rows, s);
+            if (a.H <= 2048) return launch_held<T, SHIFT, P / 2, 256, QUANT>(a, rows, s);
+            return launch_held<T, SHIFT, P, 256, QUANT>(a, rows, s);
         }
-    if (a.H <= 1024) return launch_held<T, V, P / 4, 128, QUANT>(a, rows, s);
-    if constexpr (!ODD) {                    // single 2-byte values are staged from here on
-        if (a.H <= 2048) return launch_held<T, V, P / 4, 256, QUANT>(a, rows, s);
-        if (a.H <= 4096) return launch_held<T, V, P / 2, 256, QUANT>(a, rows, s);
-        if (a.H <= 8192) {
-            if constexpr (sizeof(T) == 2) return launch_held<T, V, P, 256, QUANT>(a, rows, s);
-            else return launch_held<T, V, P / 2, 512, QUANT>(a, rows, s);
-        }
+    if (a.H <= 1024) return launch_held<T, SHIFT, P / 4, 128, QUANT>(a, rows, s);
+    if (a.H <= 2048) return launch_held<T, SHIFT, P / 4, 256, QUANT>(a, rows, s);
+    if (a.H <= 4096) return launch_held<T, SHIFT, P / 2, 256, QUANT>(a, rows, s);
+    if (a.H <= 8192) {
+        if constexpr (sizeof(T) == 2) return launch_held<T, SHIFT, P, 256, QUANT>(a, rows, s);
+        else return launch_held<T, SHIFT, P / 2, 512, QUANT>(a, rows, s);
     }
-    if constexpr (WHOLE) {
-        // 4000 x 13568 bf16 with residual: 65.0 us, 67.2 with 512 threads, 69.5 in the ring;
-        // 4000 x 16384 to blockwise codes: 79 us with 512 threads, 108 with 1024, 106 in the ring
-        if (a.H <= 16384) {
-            if constexpr (QUANT == MOE_NORM_PLAIN) return launch_held<T, V, P / 2, 1024, QUANT>(a, rows, s);
-            else return launch_held<T, V, P, 512, QUANT>(a, rows, s);
-        }
+    // 4000 x 13568 bf16 with residual: 65.0 us, 67.2 with 512 threads, 69.5 in the ring;
+    // 4000 x 16384 to blockwise codes: 79 us with 512 threads, 108 with 1024, 106 in the ring
+    if (a.H <= 16384) {
+        if constexpr (QUANT == MOE_NORM_PLAIN) return launch_held<T, SHIFT, P / 2, 1024, QUANT>(a, rows, s);
+        else return launch_held<T, SHIFT, P, 512, QUANT>(a, rows, s);
     }
-    if (!launch_fwd_ring<T, !WHOLE, QUANT>(a, s)) norm_fwd_loop_kernel<T, V, QUANT><<<rows, kNormThreads, 0, s>>>(a);
+    if (launch_fwd_ring<T, SHIFT, QUANT>(a, s)) return;
+    norm_fwd_loop_kernel<T, SHIFT ? 1 : kPiece<T>, QUANT><<<rows, kNormThreads, 0, s>>>(a);
 }
 
 template <typename T, int QUANT>
-cudaError_t launch_fwd(const FwdArgs<T>& a, int bytes, cudaStream_t s)
+cudaError_t launch_fwd(const FwdArgs<T>& a, Rows start, cudaStream_t s)
 {
-    constexpr int V16 = 16 / (int)sizeof(T);
-    if (bytes == 16) launch_fwd_width<T, V16, QUANT>(a, s);
-    if constexpr (QUANT == MOE_NORM_PLAIN) {
-        if (bytes == 4) launch_fwd_width<T, 4 / (int)sizeof(T), QUANT>(a, s);
-        if constexpr (sizeof(T) == 2)
-            if (bytes == 2) launch_fwd_width<T, 1, QUANT>(a, s);
+    if (start == Rows::kWhole) {
+        launch_fwd_cut<T, false, QUANT>(a, s);
+    } else if constexpr (QUANT == MOE_NORM_PLAIN) {
+        if (start == Rows::kAlike) launch_fwd_cut<T, true, QUANT>(a, s);
+        else if (!launch_fwd_ring<T, true, QUANT>(a, s)) norm_fwd_loop_kernel<T, 1, QUANT><<<a.rows, kNormThreads, 0, s>>>(a);
     }
     count_launches();
     return cudaGetLastError();
@@ -778,19 +889,13 @@ moe_status_t fwd(int rows, int H, int quant, float eps, const moe_norm_fwd_args_
     FwdArgs<T> a{static_cast<const T*>(g.x), static_cast<const T*>(g.residual), g.weight,
                  static_cast<T*>(g.h), static_cast<T*>(g.y), g.rstd, g.codes, g.scales,
                  g.ldx, g.ldr, g.ldh, g.ldy, rows, H, eps};
-    long long st[4];
-    int n = 0;
-    st[n++] = g.ldx;
-    if (g.residual) st[n++] = g.ldr;
-    if (g.h) st[n++] = g.ldh;
-    if (g.y) st[n++] = g.ldy;
-    const int bytes = access_bytes(H, (int)sizeof(T), st, n);
-    if (quant != MOE_NORM_PLAIN && bytes != 16) return MOE_ERR_MISALIGNED;
+    const Rows start = rows_start<T>(H, {g.ldx, g.residual ? g.ldr : g.ldx, g.h ? g.ldh : g.ldx, g.y ? g.ldy : g.ldx});
+    if (quant != MOE_NORM_PLAIN && start != Rows::kWhole) return MOE_ERR_MISALIGNED;
     if (rows == 0) return MOE_OK;
     cudaError_t e;
-    if (quant == MOE_NORM_PLAIN) e = launch_fwd<T, MOE_NORM_PLAIN>(a, bytes, s);
-    else if (quant == MOE_NORM_FP8_BLOCK) e = launch_fwd<T, MOE_NORM_FP8_BLOCK>(a, bytes, s);
-    else e = launch_fwd<T, MOE_NORM_MXFP8>(a, bytes, s);
+    if (quant == MOE_NORM_PLAIN) e = launch_fwd<T, MOE_NORM_PLAIN>(a, start, s);
+    else if (quant == MOE_NORM_FP8_BLOCK) e = launch_fwd<T, MOE_NORM_FP8_BLOCK>(a, start, s);
+    else e = launch_fwd<T, MOE_NORM_MXFP8>(a, start, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -798,40 +903,45 @@ moe_status_t fwd(int rows, int H, int quant, float eps, const moe_norm_fwd_args_
 // us with a warp and 54 with a block per row, 400 x 512 4.3 and 4.8 us.
 constexpr int kWarpH = 1024;
 
-template <typename T, int V, int N, int GROUP, int NT>
+template <typename T, bool SHIFT, int N, int GROUP, int NT>
 void launch_ring(const BwdArgs<T>& a, int parts, cudaStream_t s)
 {
-    constexpr int bytes = Ring<T, V, N, GROUP, NT>::kBytes;
+    constexpr int bytes = Ring<N, NT>::kBytes;
     if (bytes > 40 * 1024)
-        cudaFuncSetAttribute(norm_bwd_kernel<T, V, N, GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    norm_bwd_kernel<T, V, N, GROUP, NT><<<parts, NT, bytes, s>>>(a);
+        cudaFuncSetAttribute(norm_bwd_kernel<T, SHIFT, N, GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    norm_bwd_kernel<T, SHIFT, N, GROUP, NT><<<parts, NT, bytes, s>>>(a);
 }
 
-template <typename T, int V>
-void launch_bwd_width(const BwdArgs<T>& a, int parts, cudaStream_t s)
+// Rows that start whole, or alike (SHIFT); false for wider ones than the ring takes.
+template <typename T, bool SHIFT>
+bool launch_bwd_cut(const BwdArgs<T>& a, int parts, cudaStream_t s)
 {
-    if constexpr (V * sizeof(T) >= 4) {
-        constexpr int P = 32 / V;            // pieces of 32 values
-        if (a.H <= 256) return launch_ring<T, V, P / 4, 32, 256>(a, parts, s);
-        if (a.H <= kWarpH) return launch_ring<T, V, P, 32, 256>(a, parts, s);
-        if (a.H <= 2048) return launch_ring<T, V, P / 4, 256, 256>(a, parts, s);
-        if (a.H <= 4096) return launch_ring<T, V, P / 2, 256, 256>(a, parts, s);
-        if constexpr (sizeof(T) == 2)
-            if (a.H <= 8192) return launch_ring<T, V, P, 256, 256>(a, parts, s);
-        if (a.H <= 8192 || (a.H <= 16384 && sizeof(T) == 2))
-            return launch_ring<T, V, sizeof(T) == 2 ? P : P / 2, 512, 512>(a, parts, s);
+    constexpr int P = 32 / kPiece<T>;        // pieces of 32 values
+    if (a.H <= 256) launch_ring<T, SHIFT, P / 4, 32, 256>(a, parts, s);
+    else if (a.H <= kWarpH) launch_ring<T, SHIFT, P, 32, 256>(a, parts, s);
+    else if (a.H <= 2048) launch_ring<T, SHIFT, P / 4, 256, 256>(a, parts, s);
+    else if (a.H <= 4096) launch_ring<T, SHIFT, P / 2, 256, 256>(a, parts, s);
+    else if (a.H <= 8192) {
+        if constexpr (sizeof(T) == 2) launch_ring<T, SHIFT, P, 256, 256>(a, parts, s);
+        else launch_ring<T, SHIFT, P / 2, 512, 512>(a, parts, s);
+    } else if (sizeof(T) == 2 && a.H <= 16384) {
+        if constexpr (sizeof(T) == 2) launch_ring<T, SHIFT, P, 512, 512>(a, parts, s);
+    } else {
+        return false;
     }
-    // any alignment, as far as two stages and dw fit shared memory
-    if constexpr (V * sizeof(T) < 16) {
-        const int smem = 2 * Staged<T, true>::row_bytes(a.H) * (a.dh ? 3 : 2) + a.H * (int)sizeof(float);
-        if (smem <= kSmemOne) {
-            auto kernel = a.dh ? norm_bwd_window_kernel<T, true, 2> : norm_bwd_window_kernel<T, false, 2>;
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
-            kernel<<<parts, kWideThreads, smem, s>>>(a);
-            return;
-        }
-    }
-    norm_bwd_loop_kernel<T, V><<<parts, kLoopThreads, 0, s>>>(a);
+    return true;
+}
+
+// Rows that start each in their own way, as far as two stages and dw fit shared memory.
+template <typename T>
+bool launch_bwd_window(const BwdArgs<T>& a, int parts, cudaStream_t s)
+{
+    const int smem = 2 * Staged<T, true>::row_bytes(a.H) * (a.dh ? 3 : 2) + a.H * (int)sizeof(float);
+    if (smem > kSmemOne) return false;
+    auto kernel = a.dh ? norm_bwd_window_kernel<T, true, 2> : norm_bwd_window_kernel<T, false, 2>;
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+    kernel<<<parts, kWideThreads, smem, s>>>(a);
+    return true;
 }
 
 template <typename T>
@@ -840,19 +950,16 @@ moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cud
     BwdArgs<T> a{static_cast<const T*>(g.dy), static_cast<const T*>(g.h), g.rstd, g.weight,
                  static_cast<const T*>(g.dh), static_cast<T*>(g.dx), g.dweight ? part : nullptr,
                  g.lddy, g.ldh, g.lddh, g.lddx, rows, H};
-    long long st[4];
-    int n = 0;
-    st[n++] = g.lddy;
-    st[n++] = g.ldh;
-    if (g.dh) st[n++] = g.lddh;
-    st[n++] = g.lddx;
-    const int bytes = access_bytes(H, (int)sizeof(T), st, n);
+    const Rows start = rows_start<T>(H, {g.lddy, g.ldh, g.dh ? g.lddh : g.lddy, g.lddx});
     // a block of the warp-a-row kernel takes eight rows at a time
-    const int parts = norm_parts(H <= kWarpH && bytes >= 4 ? (rows + 7) / 8 : rows);
+    const int parts = norm_parts(H <= kWarpH && start != Rows::kOwn ? (rows + 7) / 8 : rows);
     if (rows > 0) {
-        if (bytes == 16) launch_bwd_width<T, 16 / (int)sizeof(T)>(a, parts, s);
-        else if (bytes == 4) launch_bwd_width<T, 4 / (int)sizeof(T)>(a, parts, s);
-        else if constexpr (sizeof(T) == 2) launch_bwd_width<T, 1>(a, parts, s);
+        if (start == Rows::kWhole) {
+            if (!launch_bwd_cut<T, false>(a, parts, s))
+                norm_bwd_loop_kernel<T, kPiece<T>><<<parts, kLoopThreads, 0, s>>>(a);
+        } else if (!(start == Rows::kAlike && launch_bwd_cut<T, true>(a, parts, s)) && !launch_bwd_window<T>(a, parts, s)) {
+            norm_bwd_loop_kernel<T, 1><<<parts, kLoopThreads, 0, s>>>(a);
+        }
         count_launches();
     }
     if (g.dweight) {

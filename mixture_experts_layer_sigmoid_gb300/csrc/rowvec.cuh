@@ -1,11 +1,11 @@
 // rowvec.cuh -- loads and stores of row pieces for the operators around the
-// layer (norm.cu, sort.cu): V consecutive act values as one access of
-// V * sizeof(T) bytes, unpacked to fp32.
+// layer (norm.cu, sort.cu, clip.cu): the 16 bytes of a piece, or one value, as one
+// access, unpacked to fp32.
 //
-// The access width of a launch follows from its pointers and row strides:
-// 16 bytes when every row starts on a 16-byte boundary and H is a whole number
-// of such pieces; otherwise norm.cu takes 4 bytes on the same terms, or single
-// values, and sort.cu shifts 16-byte pieces into place.
+// Rows move in 16-byte pieces. Where rows do not start on 16-byte boundaries (or
+// are not a whole number of pieces) they are cut at their boundaries, with a few
+// edge columns that one lane each moves; sort.cu shifts sources that are cut
+// elsewhere, norm.cu stages them.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -34,9 +34,7 @@ __device__ __forceinline__ void unpack(const Raw<T, V>& q, float (&v)[V])
     } else if constexpr (V == 1) {
         v[0] = __uint_as_float((uint32_t)q << 16);
     } else {
-        uint32_t w[V / 2];
-        if constexpr (V == 8) { w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w; }
-        else w[0] = q;
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
             v[2 * i] = __uint_as_float(w[i] << 16);
@@ -64,8 +62,7 @@ __device__ __forceinline__ Raw<T, V> pack(const float (&v)[V])
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        if constexpr (V == 8) return make_uint4(w[0], w[1], w[2], w[3]);
-        else return w[0];
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -89,6 +86,16 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[V])
 {
     store_raw<T, V>(p, pack<T, V>(v));
 }
+
+// Values of a piece.
+template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);
+
+// How a row of H columns is cut at its own boundaries: whole pieces begin at
+// columns head, head + V, ... (n of them), `edges` columns lie around them.
+struct Cut { int head, n, edges; };
+// Column of the e-th edge.
+template <typename T>
+__device__ __forceinline__ int edge_column(const Cut& c, int e) { return e < c.head ? e : e + c.n * kPiece<T>; }
 
 // Element-wise fp32 operations on a piece, two values to an instruction.
 __device__ __forceinline__ uint64_t pair(float a, float b)
@@ -167,8 +174,7 @@ __device__ __forceinline__ float max_abs(const float (&v)[V])
     return a;
 }
 
-// V consecutive fp32 values that start on a V-value boundary of an aligned
-// array (V = 8: two 16-byte loads; V = 2: 8 bytes)
+// V consecutive fp32 values that start on a V-value boundary of an aligned array
 template <int V>
 __device__ __forceinline__ void load_f32(const float* p, float (&v)[V])
 {
@@ -178,9 +184,6 @@ __device__ __forceinline__ void load_f32(const float* p, float (&v)[V])
             const float4 q = reinterpret_cast<const float4*>(p)[i];
             v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
         }
-    } else if constexpr (V == 2) {
-        const float2 q = *reinterpret_cast<const float2*>(p);
-        v[0] = q.x; v[1] = q.y;
     } else {
         v[0] = p[0];
     }
@@ -192,24 +195,51 @@ __device__ __forceinline__ void store_f32(float* p, const float (&v)[V])
 #pragma unroll
         for (int i = 0; i < V / 4; ++i)
             reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else if constexpr (V == 2) {
-        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
     } else {
         p[0] = v[0];
     }
 }
-
-// Bytes of one access for rows of H values with the given strides (in
-// elements, every base pointer 16-byte aligned): 16, 4, or one value.
-inline int access_bytes(int H, int size, const long long* strides, int n)
+// V fp32 values from column c on of an aligned array of H, c on no boundary: the
+// aligned quads around them, shifted (by the same amount along a row).
+template <int V>
+__device__ __forceinline__ void load_f32_at(const float* p, int c, int H, float (&v)[V])
 {
-    for (int b : {16, 4}) {
-        if (b <= size) break;
-        bool ok = (long long)H * size % b == 0;
-        for (int i = 0; i < n; ++i) ok = ok && strides[i] * size % b == 0;
-        if (ok) return b;
+    const int sh = c & 3, a = c - sh;
+    float w[V + 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+        const float4 q = *reinterpret_cast<const float4*>(p + a + 4 * i);
+        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
     }
-    return size;
+#pragma unroll
+    for (int i = V; i < V + 4; ++i) w[i] = 0.f;
+    if (a + V + 4 <= H) {
+        const float4 q = *reinterpret_cast<const float4*>(p + a + V);
+        w[V] = q.x; w[V + 1] = q.y; w[V + 2] = q.z;
+    } else {
+#pragma unroll
+        for (int i = V; i < V + 3; ++i)
+            if (a + i < H) w[i] = p[a + i];
+    }
+#pragma unroll
+    for (int i = 0; i < V + 2; ++i) w[i] = sh & 1 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = sh & 2 ? w[i + 2] : w[i];
+}
+
+// How rows of H values of T with these strides (every base pointer 16-byte
+// aligned) start: all on 16-byte boundaries and whole pieces; all equally far off
+// them, row by row; or each tensor in its own way.
+enum class Rows { kWhole, kAlike, kOwn };
+template <typename T>
+Rows rows_start(int H, std::initializer_list<long long> strides)
+{
+    bool whole = H % kPiece<T> == 0, alike = true;
+    for (long long ld : strides) {
+        whole = whole && ld % kPiece<T> == 0;
+        alike = alike && (ld - *strides.begin()) % kPiece<T> == 0;
+    }
+    return whole ? Rows::kWhole : (alike ? Rows::kAlike : Rows::kOwn);
 }
 
 // Launches a kernel that begins with griddep_wait: its blocks may be set up

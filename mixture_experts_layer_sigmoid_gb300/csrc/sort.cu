@@ -246,11 +246,7 @@ struct IndexArgs {
 // in 111 us (89%; 192 in 2-byte accesses, of 4098 148 in 4-byte ones), their
 // gradient takes 273 (415, 266), 8634 x 8 rows of 3033 go out in 97 with their
 // index (145).
-template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);
-
-// How a row of H columns is cut at its own boundaries: whole pieces begin at
-// columns head, head + V, ... (n of them), `edges` columns lie around them.
-struct Cut { int head, n, edges; };
+// The pieces whose two source pieces lie in the row.
 template <typename T>
 __device__ __forceinline__ Cut cut_row(const T* row, int H)
 {
@@ -263,10 +259,6 @@ __device__ __forceinline__ Cut cut_row(const T* row, int H)
     c.edges = H - c.n * V;
     return c;
 }
-// Column of the e-th edge.
-template <typename T>
-__device__ __forceinline__ int edge_column(const Cut& c, int e) { return e < c.head ? e : e + c.n * kPiece<T>; }
-
 struct Pair { uint4 lo, hi; };
 template <typename T>
 __device__ __forceinline__ Pair load_pair(const T* row, int c)
@@ -621,9 +613,7 @@ void with_slots(int k, F&& f)
 template <typename T, typename F>
 void with_shift(const moe_sorted_t& ix, std::initializer_list<long long> strides, F&& f)
 {
-    bool whole = ix.H % kPiece<T> == 0;
-    for (long long ld : strides) whole = whole && ld % kPiece<T> == 0;
-    if (whole) f(std::false_type{});
+    if (rows_start<T>(ix.H, strides) == Rows::kWhole) f(std::false_type{});
     else f(std::true_type{});
 }
 

@@ -13,9 +13,9 @@ from opcheck import U32, UNIT, Banded, assert_within, strided
 pytestmark = pytest.mark.gpu
 
 EPS = 1e-6
-SHAPES = [(1, 1), (1, 7168), (3, 31), (5, 33), (4, 64), (130, 128), (129, 257), (7, 1001), (9, 1002), (33, 1024),
+SHAPES = [(1, 1), (1, 7), (11, 15), (350, 17), (1, 7168), (3, 31), (5, 33), (4, 64), (130, 128), (129, 257), (7, 1001), (9, 1002), (33, 1024),
           (64, 2050), (300, 4096), (17, 7168), (5, 8192), (3, 12289), (4, 16384), (2, 32768), (2, 40000),
-          (700, 96), (2000, 136)]
+          (700, 96), (2000, 136), (2500, 131), (2600, 1023), (400, 4101), (3, 20001)]
 DTYPES = [torch.float32, torch.bfloat16]
 
 
@@ -78,6 +78,22 @@ def test_row_strides(rows, H, ld, dtype):
     dx, dw = moe.add_rms_norm_backward(dy, out["h"], out["rstd"], i["w"], dh, dx=bd.t)
     check_backward(dx, dw, i["dy"], flat["h"], out["rstd"], i["w"], i["dh"])
     assert bd.intact()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,H", [(5, 97), (700, 96), (9, 1002), (400, 4099), (3, 16000), (2, 40001)])
+def test_row_strides_that_differ(rows, H, dtype):
+    """Every tensor's rows start on boundaries of their own."""
+    i = inputs(rows, H, dtype)
+    x, r, dy, dh = (strided(i[n], H + k) for n, k in (("x", 1), ("r", 2), ("dy", 3), ("dh", 6)))
+    by, bh, bd = Banded(rows, H, dtype, H + 5), Banded(rows, H, dtype, H + 8), Banded(rows, H, dtype, H)
+    out = moe.add_rms_norm(x, i["w"], r, eps=EPS, want_rstd=True, y=by.t, h=bh.t)
+    s, rstd, y = reference(i["x"], i["r"], i["w"])
+    assert_within(out["y"], y, y.abs() * (UNIT[dtype] + rel32(H)) + 1e-37, "y")
+    assert_within(out["h"], s, s.abs() * (UNIT[dtype] + U32 * (1 + UNIT[dtype])) + 1e-37, "h")
+    dx, dw = moe.add_rms_norm_backward(dy, out["h"], out["rstd"], i["w"], dh, dx=bd.t)
+    check_backward(dx, dw, i["dy"], out["h"].contiguous(), out["rstd"], i["w"], i["dh"])
+    assert by.intact() and bh.intact() and bd.intact()
 
 
 def check_backward(dx, dw, dy, h, rstd, w, dh):
