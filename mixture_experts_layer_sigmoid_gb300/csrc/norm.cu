@@ -50,6 +50,18 @@ __device__ __forceinline__ float block_sum(float v, float* red)
     return s;
 }
 
+// m^(-1/2) with one correction of the approximate root by its residual 1 - m r^2
+// (Newton's iteration, the residual formed with fused multiply-adds): rstd enters
+// every value of its row, so its last bit is worth five instructions a row.
+__device__ __forceinline__ float inv_root(float m)
+{
+    const float r = rsqrtf(m);
+    if (!(r > 0.f && r < __int_as_float(0x7F800000))) return r;      // 0, infinite or NaN
+    const float p = m * r;
+    const float e = fmaf(-fmaf(m, r, -p), r, fmaf(-p, r, 1.f));
+    return fmaf(0.5f * e, r, r);
+}
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src)
@@ -198,7 +210,7 @@ norm_fwd_loop_kernel(FwdArgs<T> a)
 #pragma unroll
         for (int i = 0; i < V; ++i) ss = fmaf(v[i], v[i], ss);
     }
-    const float rstd = rsqrtf(block_sum<kNormThreads>(ss, red) / (float)a.H + a.eps);
+    const float rstd = inv_root(block_sum<kNormThreads>(ss, red) / (float)a.H + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
     for (int c0 = 0; c0 < a.H; c0 += kNormThreads * V) {
         const int c = c0 + threadIdx.x * V;
@@ -294,7 +306,7 @@ norm_fwd_kernel(FwdArgs<T> a)
         }
         add_squares(v[i], s0, s1);
     }
-    const float rstd = rsqrtf(block_sum<GROUP>(s0 + s1, red) / (float)a.H + a.eps);
+    const float rstd = inv_root(block_sum<GROUP>(s0 + s1, red) / (float)a.H + a.eps);
     if (tid == 0 && a.rstd) a.rstd[row] = rstd;
     if (edge) {
         if (a.h) store_vec<T, 1>(a.h + row * a.ldh + ec, ev);
@@ -368,7 +380,7 @@ norm_fwd_ring_kernel(FwdArgs<T> a)
             value(i, v);
             add_squares(v, s0, s1);
         }
-        const float rstd = rsqrtf(block_sum<kWideThreads>(s0 + s1, red[parity]) / (float)a.H + a.eps);
+        const float rstd = inv_root(block_sum<kWideThreads>(s0 + s1, red[parity]) / (float)a.H + a.eps);
         parity ^= 1;
         if (tid == 0 && a.rstd) a.rstd[row] = rstd;
         const float* w = a.w + tid * V;
