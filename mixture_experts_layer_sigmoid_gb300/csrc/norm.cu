@@ -788,10 +788,16 @@ norm_dweight_kernel(const float* __restrict__ part, int nparts, int H, float* __
     __shared__ float red[kPhases][33];
     const int lane = threadIdx.x & 31, ph = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    float s = 0.f;
+    constexpr int PER = (kNormParts + kPhases - 1) / kPhases;        // parts of a phase, all read together
+    float v[PER], s = 0.f;
     ptx::griddep_wait();
-    if (c < H)
-        for (int b = ph; b < nparts; b += kPhases) s += __ldcg(part + (size_t)b * H + c);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = ph + i * kPhases;
+        v[i] = c < H && b < nparts ? __ldcg(part + (size_t)b * H + c) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s += v[i];
     red[ph][lane] = s;
     __syncthreads();
     if (ph == 0 && c < H) {

@@ -194,7 +194,9 @@ def sort_index(topk, E: int, align: int = 1) -> Dict[str, object]:
 
 
 def _sorted(index, H, dtype, like, rows, padding=True):
-    row_of, slot_of = index["row_of"], index.get("slot_of")
+    row_of, slot_of = index.get("row_of"), index.get("slot_of")
+    if row_of is None:
+        raise ValueError("index: row_of is missing")
     t = _torch
     if row_of.dim() != 2 or row_of.dtype != t.int32 or row_of.device != like.device or not row_of.is_contiguous():
         raise ValueError("row_of: a contiguous T x k int32 tensor on the rows' device is needed")
@@ -213,11 +215,14 @@ def _sorted(index, H, dtype, like, rows, padding=True):
 def sort_rows(x, index, out=None):
     """The tokens' rows in expert order (moe_sort_rows): a matrix of as many
     rows as ``slot_of`` (or ``out``), padding rows zero; rows from offsets[E]
-    on are not written."""
+    on are not written. An index without ``slot_of`` (the ``row_of`` of a
+    layer's routing) needs ``out``, and its padding rows are left alone."""
     lib = _load()
     ldx = _act(x, "x")
     T, H = x.shape
     if out is None:
+        if index.get("slot_of") is None:
+            raise ValueError("out: an index without slot_of does not say how many rows there are")
         out = _torch.empty((index["slot_of"].numel(), H), dtype=x.dtype, device=x.device)
     ldp = _act(out, "out", (out.shape[0], H), x)
     s = _sorted(index, H, x.dtype, x, out.shape[0])

@@ -66,6 +66,27 @@ def test_index_matches_the_routing_of_the_layer():
         assert torch.equal(ix[n], r[n]), n
 
 
+def test_rows_by_the_layers_own_tables():
+    """moe_forward's row_of alone moves rows; the padding stays as it was."""
+    import moe_inputs as mi
+    w = mi.scaled(mi.WORKLOADS["mixtral_8x7b"], T=130, H=256, E=8, k=2, F=256)
+    g = {n: None if v is None else v.cuda() for n, v in mi.make_inputs(w, with_grad_out=False).items()}
+    layer = moe.MoELayer(w.H, w.E, w.F, w.k, w.T, score=w.score)
+    _, r = layer.forward(g["x"], g["Wr"], g["b"], g["Wg"], g["Wu"], g["Wd"], routing=True)
+    rows = int(r["offsets"][-1])
+    out = torch.full((rows, w.H), 7.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        moe.sort_rows(g["x"], {"row_of": r["row_of"]})
+    moe.sort_rows(g["x"], {"row_of": r["row_of"]}, out=out)
+    want = torch.full_like(out, 7.0)
+    for j in range(w.k):
+        want[r["row_of"][:, j].long()] = g["x"]
+    assert torch.equal(out, want)
+    y = moe.unsort_rows(out, {"row_of": r["row_of"]}, r["gates"])
+    ref = (g["x"].double()[:, None] * r["gates"].double()[..., None]).sum(1)
+    assert_within(y, ref, ref.abs() * UNIT[torch.bfloat16] + 4 * U32 * g["x"].double().abs() + 1e-37, "y")
+
+
 def test_index_capacity_is_the_callers():
     """Buffers of more rows than needed: the rest of slot_of is -1."""
     topk = torch.from_numpy(routing(50, 2, 9, 3)).cuda()
