@@ -246,7 +246,8 @@ struct IndexArgs {
 // in 111 us (89%; 192 in 2-byte accesses, of 4098 148 in 4-byte ones), their
 // gradient takes 273 (415, 266), 8634 x 8 rows of 3033 go out in 97 with their
 // index (145).
-// The pieces whose two source pieces lie in the row.
+//
+// The cut of a destination row: its pieces whose two source pieces lie in the row.
 template <typename T>
 __device__ __forceinline__ Cut cut_row(const T* row, int H)
 {
@@ -259,6 +260,8 @@ __device__ __forceinline__ Cut cut_row(const T* row, int H)
     c.edges = H - c.n * V;
     return c;
 }
+
+// The aligned pieces that hold columns [c, c + V) of a source row.
 struct Pair { uint4 lo, hi; };
 template <typename T>
 __device__ __forceinline__ Pair load_pair(const T* row, int c)
@@ -282,6 +285,7 @@ __device__ __forceinline__ uint4 shifted(const Pair& q, const T* row, int c)
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
 // Zeros in the padding rows among [r0, r0 + kPadRows): every warp looks at all of
 // their slots at once.
 template <typename T, bool SHIFT>

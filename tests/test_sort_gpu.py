@@ -107,7 +107,8 @@ def test_index_capacity_is_the_callers():
 
 MOVES = [(1, 1, 1, 1, 1), (1, 8, 256, 1, 7168), (5, 2, 3, 16, 33), (33, 8, 64, 1, 4096), (50, 3, 11, 8, 1002),
          (77, 6, 20, 128, 1001), (40, 9, 12, 4, 520), (21, 17, 30, 1, 100), (12, 32, 33, 16, 264), (300, 4, 8, 128, 2048),
-         (200, 8, 128, 16, 96), (9, 5, 6, 1, 9000), (1300, 2, 5, 16, 1040), (1217, 9, 12, 4, 1032), (1250, 3, 7, 1, 8208)]
+         (200, 8, 128, 16, 96), (9, 5, 6, 1, 9000), (1300, 2, 5, 16, 1040), (1217, 9, 12, 4, 1032), (1250, 3, 7, 1, 8208),
+         (1300, 4, 9, 16, 200), (1500, 3, 7, 1, 77), (1400, 9, 12, 4, 129), (9, 5, 6, 1, 9001), (1300, 2, 5, 16, 2047)]
 
 
 def setup(T, k, E, align, H, dtype, drop):
