@@ -154,12 +154,11 @@ __device__ __forceinline__ void quantise(const float (&v)[V], bool act, int row,
     } else {
         const float t = __fdiv_rn(a, 448.f);
         const float s = t == 0.f ? 1.f : t;              // zero, or too small for a scale
-        if (s >= 0x1p-126f) {
-            // the quotient as a product with the rounded reciprocal: within 2^-23 of
-            // it, so a code differs from the quotient's only that near to a tie of
-            // two codes 2^-3 apart; a division per value took half of the kernel's time
-            scale_vec(q, __frcp_rn(s));
-        } else {                                         // the reciprocal could overflow
+        if (s >= 0x1p-112f && s < 0x1p100f) {
+            // a division per value took half of the kernel's time; the bare product with
+            // the reciprocal moved some codes next to ties
+            divide_vec(q, s, __frcp_rn(s));
+        } else {                                         // the remainder could underflow
 #pragma unroll
             for (int i = 0; i < V; ++i) q[i] = __fdiv_rn(v[i], s);
         }

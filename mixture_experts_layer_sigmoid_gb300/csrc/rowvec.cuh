@@ -132,6 +132,26 @@ __device__ __forceinline__ void scale_vec(float (&v)[V], float s)
     for (int i = 0; i < V; ++i) w[i] = s;
     mul_vec(v, w);
 }
+// v /= s, by the reciprocal r of s rounded to nearest and one correction of the
+// product by its remainder (P. Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990): within an
+// ulp of the quotient and nearly always equal to it. The remainder must not
+// underflow.
+template <int V>
+__device__ __forceinline__ void divide_vec(float (&v)[V], float s, float r)
+{
+    static_assert(V % 2 == 0, "pairs");
+    const uint64_t rr = pair(r, r), ns = pair(-s, -s);
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        const uint64_t x = pair(v[i], v[i + 1]);
+        uint64_t y, e;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(rr));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(ns), "l"(y), "l"(x));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(e), "l"(rr), "l"(y));
+        unpair(y, v[i], v[i + 1]);
+    }
+}
 // v += u
 template <int V>
 __device__ __forceinline__ void add_vec(float (&v)[V], const float (&u)[V])
