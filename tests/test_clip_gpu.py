@@ -134,3 +134,18 @@ def test_repeatable_side_stream_and_graph():
     gr.replay()
     torch.cuda.synchronize()
     check(other, 1.0, outs, norm)
+
+
+def test_a_tensor_of_more_than_32_bits():
+    """More than 2^31 values and 2^32 bytes in one tensor."""
+    n = (1 << 31) + 12345
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.randn(n, device="cuda", dtype=torch.bfloat16)
+    out = torch.empty_like(g)
+    norm = moe.clip_grad_norm([g], 100.0, [out])
+    ref = math.sqrt(math.fsum(float(p.double().square().sum()) for p in g.split(1 << 28)))
+    assert abs(float(norm) - ref) <= ref * (REL + U32)
+    for s in (slice(0, 70000), slice(1 << 30, (1 << 30) + 70000), slice(n - 70000, n)):
+        r = g[s].double() * (100.0 / ref)
+        assert_within(out[s], r, r.abs() * (UNIT[torch.bfloat16] + REL + 3 * U32) + 1e-37, "out")

@@ -262,3 +262,36 @@ def test_side_stream_graph_and_repeatability():
     ref = moe.add_rms_norm(i["dh"], i["w"], i["r"], want_rstd=True)
     rdx, rdw = moe.add_rms_norm_backward(i["dy"], ref["h"], ref["rstd"], i["w"])
     assert all(torch.equal(a, b) for a, b in ((out["y"], ref["y"]), (dx, rdx), (dw, rdw)))
+
+
+@pytest.mark.parametrize("H", [7168, 7167])
+def test_far_rows(H):
+    """More than 2^31 values: offsets past 32 bits, in every output."""
+    rows = (1 << 31) // H + 1000
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn((rows, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = 1 + 0.3 * torch.randn(H, generator=g, device="cuda")
+    at = [0, 1, rows // 2, rows - 2, rows - 1]
+    quants = (moe.MOE_NORM_PLAIN,) if H % 128 else (moe.MOE_NORM_FP8_BLOCK, moe.MOE_NORM_MXFP8)
+    _, rstd, y = reference(x[at], None, w)
+    for q in quants:
+        out = moe.add_rms_norm(x, w, eps=EPS, quant=q, want_rstd=True)
+        assert_within(out["y"][at], y, y.abs() * (UNIT[torch.bfloat16] + rel32(H)) + 1e-37, "y")
+        assert_within(out["rstd"][at], rstd, rstd * rel32(H), "rstd")
+        if q != moe.MOE_NORM_PLAIN:
+            few = moe.add_rms_norm(x[at], w, eps=EPS, quant=q)
+            # the few rows go through another kernel: rstd may differ in its last bits
+            assert float((out["codes"][at] != few["codes"]).float().mean()) < 1e-3
+            if q == moe.MOE_NORM_FP8_BLOCK:
+                assert_within(out["scales"][at], few["scales"].double(), few["scales"].double() * 2 * rel32(H), "scales")
+    r = out["rstd"]
+    del out
+    dx, dw = moe.add_rms_norm_backward(x, x, r, w)
+    check_backward(dx[at], None, x[at], x[at], r[at], w, None)
+    # dw = sum of x^2 rstd, every row's terms positive
+    ref = torch.zeros(H, dtype=torch.float64, device="cuda")
+    for i in range(0, rows, 20000):
+        ref += (x[i:i + 20000].double().square() * r[i:i + 20000, None].double()).sum(0)
+    assert_within(dw, ref, U32 * (rows / 152 + 64) * ref, "dweight")
