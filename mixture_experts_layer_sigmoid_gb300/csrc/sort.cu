@@ -71,6 +71,7 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
     int2* pad = hist + warps * E;
     int* tot = reinterpret_cast<int*>(pad + E);
     int* base = tot + E;
+    ptx::griddep_launch_dependents();        // sort_rows may be set up meanwhile; it waits for the end
     for (int i = tid; i < warps * E; i += nt) hist[i] = make_int2(0, 0);
     __syncthreads();
     // U groups of 32 slots are loaded together; the second part's first groups
@@ -331,16 +332,21 @@ __device__ __forceinline__ void store_wide(void* p, const Wide& q)
                  : "memory");
 }
 
+// sort_rows is launched while the kernel before it on the stream still runs and
+// waits for its end (2 us of 204 behind the index): it reads by plain loads only,
+// which see that kernel's stores, and takes no pointer as read-only.
+//
 // sort_rows for many tokens whose rows lie on 32-byte boundaries, in 32-byte
 // accesses and larger blocks: 16384 tokens x 8 rows of 4096 bf16 take 191 us, 195
 // in 16-byte ones (213 with blocks of 512 threads); 33 tokens gain nothing.
 constexpr int kWideMove = 256;
 template <typename T, int KM>
 __global__ void __launch_bounds__(kWideMove)
-sort_rows_wide_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __restrict__ Xp, long long ldp)
+sort_rows_wide_kernel(IndexArgs ix, const T* x, long long ldx, T* Xp, long long ldp)
 {
     constexpr int V = 32 / (int)sizeof(T);
     const int t = blockIdx.x;
+    ptx::griddep_wait();
     if (t >= ix.T) {
         zero_padding<T, false>(ix, Xp, ldp, (long long)(t - ix.T) * kPadRows);
         return;
@@ -369,9 +375,10 @@ __host__ __device__ constexpr int token_blocks(int T) { return (T + kMoveThreads
 // wide kernel above.
 template <typename T, bool SHIFT, int KM, int GROUP>
 __global__ void __launch_bounds__(kMoveThreads)
-sort_rows_kernel(IndexArgs ix, const T* __restrict__ x, long long ldx, T* __restrict__ Xp, long long ldp)
+sort_rows_kernel(IndexArgs ix, const T* x, long long ldx, T* Xp, long long ldp)
 {
     constexpr int V = kPiece<T>;
+    ptx::griddep_wait();
     if (blockIdx.x >= (unsigned)token_blocks<GROUP>(ix.T)) {
         zero_padding<T, SHIFT>(ix, Xp, ldp, (long long)(blockIdx.x - token_blocks<GROUP>(ix.T)) * kPadRows);
         return;
@@ -695,22 +702,24 @@ unsigned column_parts(const moe_sorted_t& s)
 }
 
 template <typename T>
-void sort_rows(const moe_sorted_t& ix, const void* x, long long ldx, void* Xp, long long ldp, cudaStream_t s)
+cudaError_t sort_rows(const moe_sorted_t& ix, const void* x, long long ldx, void* Xp, long long ldp, cudaStream_t s)
 {
+    cudaError_t e = cudaSuccess;
     with_shift<T>(ix, {ldx, ldp}, [&](auto shift) {
         with_slots(ix.k, [&](auto km) {
             auto launch = [&](auto group) {
                 constexpr int G = decltype(group)::value;
-                sort_rows_kernel<T, decltype(shift)::value, decltype(km)::value, G>
-                    <<<dim3(move_grid(ix, token_blocks<G>(ix.T)), column_parts<T>(ix)), kMoveThreads, 0, s>>>(
-                        index_args(ix), static_cast<const T*>(x), ldx, static_cast<T*>(Xp), ldp);
+                e = launch_early(sort_rows_kernel<T, decltype(shift)::value, decltype(km)::value, G>,
+                                 dim3(move_grid(ix, token_blocks<G>(ix.T)), column_parts<T>(ix)), dim3(kMoveThreads), s,
+                                 index_args(ix), static_cast<const T*>(x), ldx, static_cast<T*>(Xp), ldp);
             };
             if constexpr (!decltype(shift)::value) {
                 const uintptr_t low = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(Xp);
                 const long long off = (ix.H | ldx | ldp) * (long long)sizeof(T);
                 if (ix.T >= kFewTokens && !narrow<T>(ix) && ((low | (uintptr_t)off) & 31) == 0) {
-                    sort_rows_wide_kernel<T, decltype(km)::value><<<move_grid(ix, ix.T), kWideMove, 0, s>>>(
-                        index_args(ix), static_cast<const T*>(x), ldx, static_cast<T*>(Xp), ldp);
+                    e = launch_early(sort_rows_wide_kernel<T, decltype(km)::value>, dim3(move_grid(ix, ix.T)),
+                                     dim3(kWideMove), s, index_args(ix), static_cast<const T*>(x), ldx,
+                                     static_cast<T*>(Xp), ldp);
                     return;
                 }
             }
@@ -718,6 +727,7 @@ void sort_rows(const moe_sorted_t& ix, const void* x, long long ldx, void* Xp, l
             else launch(Block{});
         });
     });
+    return e;
 }
 
 template <typename T>
@@ -840,9 +850,10 @@ moe_status_t moe_sort_rows(const moe_sorted_t* index, const void* x, long long l
     if (!is_aligned16(x) || !is_aligned16(Xp)) return MOE_ERR_MISALIGNED;
     if (ix.rows == 0 || (ix.T == 0 && !ix.slot_of)) return MOE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (ix.dtype == MOE_FP32) sort_rows<float>(ix, x, ldx, Xp, ldp, s);
-    else sort_rows<__nv_bfloat16>(ix, x, ldx, Xp, ldp, s);
-    return launched();
+    const cudaError_t e = ix.dtype == MOE_FP32 ? sort_rows<float>(ix, x, ldx, Xp, ldp, s)
+                                               : sort_rows<__nv_bfloat16>(ix, x, ldx, Xp, ldp, s);
+    count_launches();
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status_t moe_unsort_rows(const moe_sorted_t* index, const void* Yp, long long ldp,
