@@ -130,6 +130,13 @@ template <typename T> struct FwdArgs {
     int rows, H; float eps;
 };
 
+// Scales from which divide_vec's codes are those of a division: the remainder v - s y
+// has to keep the bits down to one step of s times one of y, 2^-23 s 2^-34 where y
+// rounds to a code but zero (y >= 2^-11), and fp32 ends at 2^-149.
+// tests/e4m3_quotient_fp32_check.c finds no difference from here on; from 2^-112,
+// where bf16 values still show none, fp32 values of small blocks took wrong codes.
+constexpr float kQuotientMin = 0x1p-92f;
+
 // The 8-bit output of one piece of V values at column c of a row. All lanes
 // of a warp call it together; `act` is false past the row's end, and the
 // lanes of one block are all active or all inactive (H is a multiple of 128).
@@ -154,7 +161,7 @@ __device__ __forceinline__ void quantise(const float (&v)[V], bool act, int row,
     } else {
         const float t = __fdiv_rn(a, 448.f);
         const float s = t == 0.f ? 1.f : t;              // zero, or too small for a scale
-        if (s >= 0x1p-112f && s < 0x1p100f) {
+        if (s >= kQuotientMin && s < 0x1p100f) {
             // a division per value took half of the kernel's time; the bare product with
             // the reciprocal moved some codes next to ties
             divide_vec(q, s, __frcp_rn(s));
