@@ -429,7 +429,8 @@ moe_status_t moe_update_bias(int E, const int32_t* counts, float rate, float* b,
 /* 8-bit output of moe_add_rms_norm.
  *   MOE_NORM_FP8_BLOCK: E4M3 codes (rows x H bytes) with one fp32 scale per
  *     1x128 block (rows x H/128): amax / 448, 1 for an all-zero block; codes
- *     of value / scale, nearest even, saturated.
+ *     of the fp32 quotient value / scale, nearest even, saturated, a zero's
+ *     sign kept.
  *   MOE_NORM_MXFP8: E4M3 codes with one UE8M0 scale per 1x32 block, 2^e with
  *     e the smallest integer such that amax <= 448 2^e, in the scale atoms of
  *     moe_mx_quantize: ceil(rows/128) * H/128 atoms of 512 bytes; the scale

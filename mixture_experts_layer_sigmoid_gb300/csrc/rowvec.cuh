@@ -136,20 +136,24 @@ __device__ __forceinline__ void scale_vec(float (&v)[V], float s)
 // product by its remainder (P. Markstein, "Computation of elementary functions on
 // the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990): within an
 // ulp of the quotient and nearly always equal to it. The remainder must not
-// underflow.
+// underflow. The quotient is formed with the other sign, which keeps a zero's:
+// v = -0 gives the remainder +0, and -0 + 0 would be +0.
 template <int V>
 __device__ __forceinline__ void divide_vec(float (&v)[V], float s, float r)
 {
     static_assert(V % 2 == 0, "pairs");
-    const uint64_t rr = pair(r, r), ns = pair(-s, -s);
+    const uint64_t nr = pair(-r, -r), ss = pair(s, s);
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
         const uint64_t x = pair(v[i], v[i + 1]);
         uint64_t y, e;
-        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(rr));
-        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(ns), "l"(y), "l"(x));
-        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(e), "l"(rr), "l"(y));
-        unpair(y, v[i], v[i + 1]);
+        float a, b;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(nr));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(ss), "l"(y), "l"(x));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(e), "l"(nr), "l"(y));
+        unpair(y, a, b);
+        v[i] = -a;
+        v[i + 1] = -b;
     }
 }
 // v += u
