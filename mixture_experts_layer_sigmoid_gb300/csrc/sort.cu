@@ -180,7 +180,7 @@ sort_index_kernel(const int32_t* __restrict__ topk, int n, int per, int warps, i
     }
     // a warp per segment's padding, and the rows after the last segment
     for (int e = blockIdx.x * (nt / 32) + warp; e < E && align > 1; e += gridDim.x * (nt / 32))
-        for (int r = pad[e].x + lane; r < pad[e].y; r += 32) slot_of[r] = -1;
+        for (long long r = (long long)pad[e].x + lane; r < pad[e].y; r += 32) slot_of[r] = -1;
     for (long long r = used + (long long)blockIdx.x * nt + tid; r < rows; r += gridDim.x * nt) slot_of[r] = -1;
     if constexpr (CLUSTER) ptx::cluster_sync();          // no block leaves while another may read its totals
 }
@@ -189,7 +189,7 @@ cudaError_t launch_index(int n, int E, int align, const int32_t* topk, int32_t* 
                          int32_t* row_of, int32_t* slot_of, int rows, cudaStream_t s)
 {
     const int blocks = n <= kIndexOneBlock && rows <= kIndexOneBlockRows ? 1 : kIndexCluster;
-    const int groups = (n + 31) / 32;
+    const int groups = (int)((n + 31ll) / 32);             // n is up to 2^31 - 3: sums next to it in 64 bits
     const int most = E <= 512 ? kIndexWarps : kIndexWarps / 2;       // of (count, lanes) pairs in shared memory
     int warps = (groups + 4 * blocks - 1) / (4 * blocks);
     warps = warps < 1 ? 1 : (warps > most ? most : warps);
@@ -365,9 +365,11 @@ sort_rows_wide_kernel(IndexArgs ix, const T* x, long long ldx, T* Xp, long long 
     }
 }
 
+// Blocks of T tokens, `per` to a block (without a sum that passes 32 bits).
+__host__ __device__ constexpr int blocks_of(int T, int per) { return T / per + (T % per != 0); }
 // Blocks of the tokens with GROUP threads a token.
 template <int GROUP>
-__host__ __device__ constexpr int token_blocks(int T) { return (T + kMoveThreads / GROUP - 1) / (kMoveThreads / GROUP); }
+__host__ __device__ constexpr int token_blocks(int T) { return blocks_of(T, kMoveThreads / GROUP); }
 
 // The first blocks: a token's row to its k rows, GROUP threads a token. The
 // blocks after them: padding rows. 16384 tokens x 8 rows of 4096 bf16 with 7.7k
@@ -530,7 +532,7 @@ unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const 
 {
     constexpr int V = kPiece<T>;
     constexpr int TOKENS = NT / GROUP;       // of a block
-    const int tb = (ix.T + TOKENS - 1) / TOKENS;
+    const int tb = blocks_of(ix.T, TOKENS);
     if (blockIdx.x >= (unsigned)tb) {
         zero_padding<T, SHIFT>(ix, dYp, ldd, (long long)(blockIdx.x - tb) * kPadRows);
         return;
@@ -765,7 +767,7 @@ void unsort_bwd(const moe_sorted_t& ix, const void* dY, long long lddy, const vo
             auto launch = [&](auto nt, auto group, auto dg) {
                 constexpr int NT = decltype(nt)::value, G = decltype(group)::value;
                 unsort_bwd_kernel<T, decltype(shift)::value, KM, NT, G, decltype(dg)::value>
-                    <<<move_grid(ix, (ix.T + NT / G - 1) / (NT / G)), NT, 0, s>>>(
+                    <<<move_grid(ix, blocks_of(ix.T, NT / G)), NT, 0, s>>>(
                         index_args(ix), static_cast<const T*>(dY), lddy, static_cast<const T*>(Yp), ldp, gates,
                         static_cast<T*>(dYp), ldd, dgates);
             };
