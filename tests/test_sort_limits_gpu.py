@@ -92,3 +92,9 @@ def test_gradient_of_most_tokens(moved):
     rows, dg = moe.unsort_rows_backward(x, x, index)
     assert same(rows.view(-1), kept)
     assert same(dg.view(-1), lambda i: kept(i) ** 2)
+
+
+def test_gradient_of_most_tokens_without_the_gates(moved):
+    T, index, x, kept = moved
+    rows, none = moe.unsort_rows_backward(x, x, index, want_dgates=False)
+    assert none is None and same(rows.view(-1), kept)
