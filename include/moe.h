@@ -555,7 +555,8 @@ typedef struct {
  *   out = g min(1, max_norm / norm)   (fp32 product, rounded once).
  * max_norm > 0; infinity clips nothing. A norm that is infinite (in fp32) or
  * NaN leaves the values as they are (out = g): the caller sees it in *norm and
- * skips the step. Squares that leave fp32's range are summed in 64 bits. `list` is a
+ * skips the step. The sum carries more bits than fp32 has (and all of its range in 64
+ * bits), so the norm and max_norm / norm are the nearest fp32 values. `list` is a
  * host array, read during the call; *norm is a device float.
  * Errors: INVALID_ARG (also a norm of more than 2^46 bytes), MISALIGNED,
  * WORKSPACE_TOO_SMALL, CUDA. */

@@ -4,8 +4,8 @@
 //
 // Two passes over the values (the norm has to be known before the first
 // product): bound by HBM for large sets, by launches for small ones. 1.41 G bf16
-// values: 390 us for the norm (7.2 TB/s, reads), 857 us for the product (6.6
-// TB/s); twenty fp32 tensors of 6.3 MB together: 7.7 us. The tensors' table
+// values: 411 us for the norm (6.9 TB/s, reads), 857 us for the product (6.6
+// TB/s); twenty fp32 tensors of 6.3 MB together: 8.2 us. The tensors' table
 // travels in the kernel's parameters, so a call copies nothing to the device and
 // can be captured; blocks take chunks of any tensor, so neither one large tensor
 // nor hundreds of small ones leave SMs idle.
@@ -21,7 +21,8 @@ constexpr int kClipThreads = 256;
 // spread over the SMs and a large one keeps its pieces long.
 constexpr int kAhead = 4;               // 16-byte pieces that a thread loads together
 constexpr int kChunkMin = kClipThreads * kAhead * 16, kChunkMax = 1 << 16;
-constexpr int kClipBlocks = 1216;       // eight per SM
+constexpr int kSmCount = 152;
+constexpr int kClipBlocks = 8 * kSmCount;
 // Tensors per launch: 32 bytes each, within the 32,764 of kernel parameters (a
 // shorter table launches no faster).
 constexpr int kClipBatch = 896;
@@ -99,20 +100,20 @@ __device__ __forceinline__ Chunk<T> chunk_of(const Entry& e, int chunk, int chun
     return c;
 }
 
-// Gives each piece of V values of a whole chunk to fn(index, raw), kAhead pieces
+// Gives each piece of V values of a whole chunk to fn(index, raw), AHEAD pieces
 // of the thread loaded before the first is used.
-template <typename T, typename FN>
+template <int AHEAD, typename T, typename FN>
 __device__ __forceinline__ void whole_chunk(const Chunk<T>& c, FN&& fn)
 {
     constexpr int V = 16 / (int)sizeof(T);
     constexpr int STEP = kClipThreads * V;
 #pragma unroll 1
-    for (int at = threadIdx.x * V; at < c.hi; at += kAhead * STEP) {    // whole chunks are whole batches
-        Raw<T, V> q[kAhead];
+    for (int at = threadIdx.x * V; at < c.hi; at += AHEAD * STEP) {    // whole chunks are whole batches
+        Raw<T, V> q[AHEAD];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) q[i] = load_raw<T, V>(c.base + at + i * STEP);
+        for (int i = 0; i < AHEAD; ++i) q[i] = load_raw<T, V>(c.base + at + i * STEP);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) fn(at + i * STEP, q[i]);
+        for (int i = 0; i < AHEAD; ++i) fn(at + i * STEP, q[i]);
     }
 }
 
@@ -164,36 +165,83 @@ __device__ __noinline__ double squares_64(Chunk<T> c)
     return d;
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void add_squares(const Raw<T, V>& q, float& s, uint32_t& any)
+// A sum of squares as two fp32 values, s and what its roundings lost, e. Two such
+// sums to a register pair, those of the even and of the odd values. `any`: some bit
+// of the values is set.
+struct Squares {
+    uint64_t s = 0, e = 0;
+    uint32_t any = 0;
+};
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// s += x^2, and e += what the rounded sum t lost: with z = t - s it is x^2 - z where
+// s >= x^2 (T. J. Dekker, "A floating-point technique for extending the available
+// precision", Numer. Math. 18, 1971). Where a square is the larger one, as a thread's
+// first ones are, z is rounded too, by 2^-25 of that square at most; EXACT keeps that
+// by two more steps (D. Knuth, The Art of Computer Programming 2, 4.2.2).
+template <typename T, int V, bool EXACT>
+__device__ __forceinline__ void add_squares(const Raw<T, V>& q, Squares& a)
 {
     float v[V];
     unpack<T, V>(q, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) s = fmaf(v[i], v[i], s);
-    if constexpr (V == 1) any |= q;
-    else any |= q.x | q.y | q.z | q.w;
+    for (int i = 0; i < V; i += 2) {
+        const uint64_t x = pair(v[i], V > 1 ? v[i + 1] : 0.f);
+        const uint64_t t = fma2(x, x, a.s), nz = sub2(a.s, t);           // -z
+        uint64_t d = fma2(x, x, nz);
+        if constexpr (EXACT) d = add2(d, sub2(a.s, add2(t, nz)));
+        a.e = add2(a.e, d);
+        a.s = t;
+    }
+    if constexpr (V == 1) a.any |= q;
+    else a.any |= q.x | q.y | q.z | q.w;
 }
 
-// The squares are added in fp32; where that leaves its range (a sum that is not
-// finite, or so small that squares may have been flushed), the share is summed
-// again in 64 bits, so the norm is right from the smallest values to the
-// largest. `any`: some bit of the values is set.
+// The sum in 64 bits. At most 64 additions to a sum leave e below 2^-18 of it and
+// e's own roundings below 2^-35 of it (2^-46 in the mean); what is lost where a square
+// is the larger one comes to 2^-31 of a thread's sum in the mean and to less over the
+// 256 threads of a whole chunk. The ends of tensors, the only chunks that few values
+// have, are added exactly. Where squares or sums leave fp32's range (a sum that is not
+// finite, or so small that squares may have lost bits) the share is summed again in 64
+// bits, so the norm is right from the smallest values to the largest.
 template <typename T>
-__device__ __forceinline__ double checked(const Chunk<T>& c, float s, uint32_t any)
+__device__ __forceinline__ double checked(const Chunk<T>& c, const Squares& a)
 {
-    return !any || (s > 0x1p-60f && s < 0x1p126f) ? (double)s : squares_64(c);
+    float s0, s1, e0, e1;
+    unpair(a.s, s0, s1);
+    unpair(a.e, e0, e1);
+    const float s = s0 + s1;
+    if (a.any && !(s > 0x1p-60f && s < 0x1p126f)) return squares_64(c);
+    // s0 + s1 = s + r exactly, as above
+    const float z = s - s0, r = (s0 - (s - z)) + (s1 - z);
+    return (double)s + (double)(r + (e0 + e1));
 }
 
 template <typename T>
 __device__ __noinline__ double ragged_squares(Chunk<T> c)
 {
     constexpr int V = 16 / (int)sizeof(T);
-    float s = 0.f;
-    uint32_t any = 0;
-    ragged_chunk(c, [&](int, const Raw<T, V>& q) { add_squares<T, V>(q, s, any); },
-                 [&](int, const Raw<T, 1>& q) { add_squares<T, 1>(q, s, any); });
-    return checked(c, s, any);
+    Squares a;
+    ragged_chunk(c, [&](int, const Raw<T, V>& q) { add_squares<T, V, true>(q, a); },
+                 [&](int, const Raw<T, 1>& q) { add_squares<T, 1, true>(q, a); });
+    return checked(c, a);
 }
 
 // This thread's share of the sum of squares of one chunk.
@@ -202,13 +250,20 @@ __device__ __forceinline__ double chunk_squares(const Chunk<T>& c)
 {
     constexpr int V = 16 / (int)sizeof(T);
     if (!c.whole) return ragged_squares(c);
-    float s = 0.f;
-    uint32_t any = 0;
-    whole_chunk(c, [&](int, const Raw<T, V>& q) { add_squares<T, V>(q, s, any); });
-    return checked(c, s, any);
+    Squares a;
+    auto add = [&](int, const Raw<T, V>& q) { add_squares<T, V, false>(q, a); };
+    // eight pieces ahead of the sums' work where a chunk has them (2.8 GB bf16: 411 us,
+    // 420 with four)
+    if (c.hi % (2 * kAhead * kClipThreads * V) == 0) whole_chunk<2 * kAhead>(c, add);
+    else whole_chunk<kAhead>(c, add);
+    return checked(c, a);
 }
 
-__global__ void __launch_bounds__(kClipThreads, 4)
+// Three blocks an SM for many chunks: at four the sums spill (2.8 GB bf16: 411 us, 419
+// with four; 434 with three in two waves and a part). Four where that puts every chunk
+// in the first wave (500 tensors of 101 values: 6.3 us, 8.4 with three).
+template <int PER_SM>
+__global__ void __launch_bounds__(kClipThreads, PER_SM)
 norm_kernel(const __grid_constant__ Table t, double* __restrict__ part)
 {
     __shared__ double red[kClipThreads];
@@ -223,28 +278,47 @@ norm_kernel(const __grid_constant__ Table t, double* __restrict__ part)
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// sqrt(s) in fp32 for any s >= 0 in 64 bits: s = m 4^e with m in [1, 4), the
-// root of m taken in fp32 (64-bit roots and quotients cost microseconds here).
-__device__ __forceinline__ float root(double s)
+// sqrt(s) for any s >= 0: s = m 4^e with m in [1, 4), the root of m taken in fp32
+// and corrected once by its residual (Newton's iteration) in 64 bits, to 2^-46 of
+// it. The 64-bit root and quotient take a microsecond of a call that takes seven.
+__device__ __forceinline__ double root(double s)
 {
     const int hi = __double2hiint(s), lo = __double2loint(s);
-    if (!(s > 0.0) || hi >= 0x7FF00000) return (float)s;             // zero, infinite or NaN
-    if (hi < 0x00100000) return 0.f;                                // below 2^-1022: its root is below fp32's range
+    if (!(s > 0.0) || hi >= 0x7FF00000) return s;                    // zero, infinite or NaN
+    if (hi < 0x00100000) return 0.0;                                // below 2^-1022: its root is below fp32's range
     const int e = ((hi >> 20) - 1023) >> 1;                         // floor
     const double m = __hiloint2double(hi - (e << 21), lo);
-    return ldexpf(__fsqrt_rn((float)m), e);
+    const float r = __fsqrt_rn((float)m);
+    const double n = fma(fma(-(double)r, (double)r, m), (double)(0.5f * rsqrtf((float)m)), (double)r);
+    return __hiloint2double(__double2hiint(n) + (e << 20), __double2loint(n));
 }
 
-// The norm from the parts' sum; every block adds them in the same order.
-__device__ __forceinline__ float total_norm(const double* part, int nparts, double* red)
+// The fp32 value nearest to min(1, limit / n): the quotient in fp32 with its
+// remainder in 64 bits. A norm that is infinite in fp32 or NaN clips nothing.
+__device__ __forceinline__ float coefficient(float limit, double n)
 {
-    __shared__ float norm;
+    const float nf = (float)n;
+    if (!(n > (double)limit) || !(nf < __int_as_float(0x7F800000))) return 1.f;
+    if (!(limit > 0x1p-60f && nf < 0x1p60f)) return (float)((double)limit / n);   // fp32 parts could leave its range
+    const float inv = __fdividef(1.f, nf), q = limit * inv;
+    return (float)fma(fma(-(double)q, n, (double)limit), (double)inv, (double)q);
+}
+
+// The norm from the parts' sum, and the coefficient for the limit; every block
+// adds the parts in the same order.
+struct Total { float norm, coef; };
+__device__ __forceinline__ Total total_norm(const double* part, int nparts, float limit, double* red)
+{
+    __shared__ Total total;
     double s = 0.0;
     for (int i = threadIdx.x; i < nparts; i += kClipThreads) s += __ldcg(part + i);
     s = block_sum_double(s, red);
-    if (threadIdx.x == 0) norm = root(s);
+    if (threadIdx.x == 0) {
+        const double n = root(s);
+        total = Total{(float)n, coefficient(limit, n)};
+    }
     __syncthreads();
-    return norm;
+    return total;
 }
 
 __global__ void __launch_bounds__(kClipThreads)
@@ -252,8 +326,8 @@ norm_finish_kernel(const double* __restrict__ part, int nparts, float* __restric
 {
     __shared__ double red[kClipThreads];
     ptx::griddep_wait();
-    const float n = total_norm(part, nparts, red);
-    if (threadIdx.x == 0) *norm = n;
+    const Total t = total_norm(part, nparts, __int_as_float(0x7F800000), red);
+    if (threadIdx.x == 0) *norm = t.norm;
 }
 
 // The bits of value i of a piece.
@@ -298,7 +372,7 @@ __device__ __forceinline__ void clip_chunk(const Chunk<T>& c, bool clip, float f
 {
     constexpr int V = 16 / (int)sizeof(T);
     if (!c.whole || !c.aligned) ragged_scale(c, clip, f);
-    else whole_chunk(c, [&](int p, const Raw<T, V>& q) { store_raw<T, V>(c.out + p, clip ? scaled<T, V>(q, f) : q); });
+    else whole_chunk<kAhead>(c, [&](int p, const Raw<T, V>& q) { store_raw<T, V>(c.out + p, clip ? scaled<T, V>(q, f) : q); });
 }
 
 // out = g c with c from the norm; the last chunks first, since the norm's pass
@@ -310,10 +384,10 @@ clip_kernel(const __grid_constant__ Table t, const double* __restrict__ part, in
 {
     __shared__ double red[kClipThreads];
     ptx::griddep_wait();
-    const float n = total_norm(part, nparts, red);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = n;
-    const bool clip = n > max_norm && n - n == 0.f;
-    const float f = clip ? __fdiv_rn(max_norm, n) : 1.f;
+    const Total total = total_norm(part, nparts, max_norm, red);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = total.norm;
+    const float f = total.coef;
+    const bool clip = f < 1.f;
     for (int c = t.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
         const Entry& e = t.e[find_entry(t, c)];
         if (!e.out || (!clip && e.out == e.g)) continue;
@@ -360,13 +434,15 @@ cudaError_t run_clip(int count, const moe_grad_t* list, int chunk_bytes, bool wr
     unsigned grid = 0;
     for (int first = 0; first < count || first == 0; first += kClipBatch) {
         grid = fill(first);
+        const bool few = grid <= 4 * kSmCount;
+        const unsigned blocks = few ? grid : 3 * kSmCount;           // one wave
         double* to = part + nparts;
         void* args[] = {&t, &to};
-        const cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(norm_kernel), dim3(grid),
+        const cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(few ? norm_kernel<4> : norm_kernel<3>), dim3(blocks),
                                                dim3(kClipThreads), args, 0, s);
         if (e != cudaSuccess) return e;
         count_launches();
-        nparts += (int)grid;
+        nparts += (int)blocks;
     }
     if (!writes) {
         count_launches();
