@@ -32,10 +32,10 @@ def _load():
         import torch
         _torch = torch
         _dtypes.update({torch.float32: MOE_FP32, torch.bfloat16: MOE_BF16})
-        _lib = load_library()
         # the current stream as a number, without a Stream object (2.8 us of a call)
         _stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _lib = load_library()                # last: another thread's call takes it as the sign that the rest is there
     return _lib
 
 
