@@ -202,8 +202,11 @@ def _sorted(index, H, dtype, like, rows, padding=True):
         raise ValueError("row_of: a contiguous T x k int32 tensor on the rows' device is needed")
     s = moe_sorted_t(row_of.shape[0], row_of.shape[1], H, _dtypes[dtype], rows, row_of.data_ptr())
     if padding and slot_of is not None:
-        offsets = index["offsets"]
+        offsets, counts = index.get("offsets"), index.get("counts")
         dev = like.get_device()
+        # the rows in use stand after the last expert's offset
+        if offsets is None or offsets.numel() < 2 or (counts is not None and offsets.numel() != counts.numel() + 1):
+            raise ValueError("offsets: one value for each expert and one more are needed")
         if (slot_of.numel() < rows or slot_of.dtype != t.int32 or offsets.dtype != t.int32 or slot_of.get_device() != dev or
                 offsets.get_device() != dev or not slot_of.is_contiguous() or not offsets.is_contiguous()):
             raise ValueError(f"slot_of, offsets: contiguous int32 on the rows' device, for each of the {rows} rows")
@@ -215,8 +218,10 @@ def _sorted(index, H, dtype, like, rows, padding=True):
 def sort_rows(x, index, out=None):
     """The tokens' rows in expert order (moe_sort_rows): a matrix of as many
     rows as ``slot_of`` (or ``out``), padding rows zero; rows from offsets[E]
-    on are not written. An index without ``slot_of`` (the ``row_of`` of a
-    layer's routing) needs ``out``, and its padding rows are left alone."""
+    on are not written. With ``slot_of`` an index has ``offsets`` of exactly
+    E + 1 values (checked against ``counts`` where it has those too). An index
+    without ``slot_of`` (the ``row_of`` of a layer's routing) needs ``out``,
+    and its padding rows are left alone."""
     lib = _load()
     ldx = _act(x, "x")
     T, H = x.shape

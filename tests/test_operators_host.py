@@ -1,5 +1,5 @@
 """Host side of the operators' Python entries (CPU): the first call from several
-threads."""
+threads, and the index that the movers accept."""
 import sys
 import threading
 
@@ -41,3 +41,42 @@ def test_a_second_thread_never_sees_half_of_the_first_call(fresh):
     t.join()
     assert len(seen) > 3 and operators._lib is not None and operators._stream is not None
     assert not any(missing and not before for before, missing in seen)
+
+
+def index(E=5, offsets=None, counts=True, rows=12):
+    i32 = dict(dtype=torch.int32)
+    d = dict(row_of=torch.zeros((4, 2), **i32), slot_of=torch.zeros(rows, **i32),
+             offsets=torch.zeros(E + 1 if offsets is None else offsets, **i32))
+    if counts:
+        d["counts"] = torch.zeros(E, **i32)
+    return d
+
+
+def check(ix, rows=12):
+    operators._load()
+    return operators._sorted(ix, 64, torch.float32, torch.zeros(1), rows)
+
+
+def test_the_rows_in_use_are_read_after_the_last_expert():
+    _build.build()
+    ix = index()
+    assert check(ix).in_use == ix["offsets"].data_ptr() + 4 * 5
+    ix = index(counts=False)
+    assert check(ix).in_use == ix["offsets"].data_ptr() + 4 * 5
+    ix = index(E=1)
+    assert check(ix).in_use == ix["offsets"].data_ptr() + 4
+
+
+@pytest.mark.parametrize("bad", [dict(offsets=9), dict(offsets=5), dict(offsets=1), dict(offsets=0), dict(offsets=0, counts=False),
+                                 dict(offsets=1, counts=False)])
+def test_offsets_of_another_length_are_refused(bad):
+    """One entry after each expert's is where the rows in use stand."""
+    with pytest.raises(ValueError):
+        check(index(**bad))
+
+
+def test_missing_offsets_are_refused():
+    ix = index()
+    del ix["offsets"]
+    with pytest.raises(ValueError):
+        check(ix)
