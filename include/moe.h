@@ -268,8 +268,9 @@ moe_status_t moe_stage_times(moe_plan_t plan, moe_stage_time_t* out, int capacit
  * Computes, for T tokens, the same routing outputs as moe_forward's optional
  * outputs: topk_idx (T×k), gates (T×k), counts (E), offsets (E+1, padded
  * segment starts) and row_of (T×k), from x (T×H act), Wr (H×E fp32) and the
- * optional bias b (E fp32). All pointers are caller-owned device pointers,
- * 16-byte aligned; nothing is allocated or freed.
+ * optional bias b (E fp32). A capacity_factor of the plan changes none of
+ * them. All pointers are caller-owned device pointers, 16-byte aligned;
+ * nothing is allocated or freed.
  * Scratch: a 64 MiB array inside the library's device image, held on every GPU
  * that loads the library until the process exits. A call needs about
  * 8·T·k + 8·ceil(T/32)·E + 508·min(E, T·k) bytes of it, plus up to 32·T·E
@@ -505,7 +506,11 @@ moe_status_t moe_sort_index(int T, int k, int E, int align, const int32_t* topk,
 
 /* The index that the three calls below move rows by (moe_sort_index's, or
  * moe_route_static's row_of and offsets). Rows outside [0, rows) in row_of
- * are dropped slots. */
+ * are dropped slots. The routing tables of moe_forward and moe_route_static
+ * give every slot a row: a plan with a capacity_factor drops by the row's place
+ * in its segment and does not mark it there. To move rows as such a plan does,
+ * set row_of to -1 first wherever
+ *     row_of - offsets[expert] >= ceil(capacity_factor T k / E). */
 typedef struct {
     int T, k, H, dtype;      /* dtype MOE_FP32 or MOE_BF16                     */
     long long rows;          /* rows of the sorted buffer                      */

@@ -221,7 +221,8 @@ def sort_rows(x, index, out=None):
     on are not written. With ``slot_of`` an index has ``offsets`` of exactly
     E + 1 values (checked against ``counts`` where it has those too). An index
     without ``slot_of`` (the ``row_of`` of a layer's routing) needs ``out``,
-    and its padding rows are left alone."""
+    and its padding rows are left alone; a layer with a ``capacity_factor``
+    gives dropped slots rows there too (moe_sorted_t says which)."""
     lib = _load()
     ldx = _act(x, "x")
     T, H = x.shape
