@@ -25,8 +25,8 @@ namespace moe {
 namespace {
 
 constexpr int kNormThreads = 256;
-// Row groups of the weight gradient's partial sums (blocks of the backward):
-// two per SM, each holding 96 KB of rows in flight.
+// Row groups of the weight gradient's partial sums (blocks of the backward): two per
+// SM where a block's ring leaves room for another, else half as many (Ring::kParts).
 constexpr int kNormParts = 304;
 // Up to one row per SM the forward gives a row more threads: 8 rows of 7168 bf16
 // take 4.6 us with a thread per eight values and 8.7 with one per 28.
@@ -502,12 +502,16 @@ template <int N, int NT>
 struct Ring {
     static constexpr int kTensor = NT * N * 16;              // one tensor's rows of one stage
     static constexpr int kStage = 3 * kTensor;
-    // as many stages as fit beside a second block on the SM, at most 4
+    // as many stages as fit beside a second block on the SM, at most 4, and two at least
     static constexpr int kStages = kStage * 4 <= 104 * 1024 ? 4 : (kStage * 3 <= 104 * 1024 ? 3 : 2);
     static constexpr int kBytes = kStages * kStage;
+    // Blocks: those that are resident together, so that no ring is filled and no w read
+    // for a second wave. With 192 KB (N = 4 of 512 threads, N = 8 of 256) that is one
+    // per SM: 4000 x 16384 bf16 85.3 us, 88.2 with 304 blocks, 300 x 16384 14.4 and 18.5.
+    static constexpr int kParts = kBytes <= 104 * 1024 ? kNormParts : kNormParts / 2;
+    static_assert(kParts % 8 == 0, "see SHIFT");
 };
 
-static_assert(kNormParts % 8 == 0, "see SHIFT");
 template <typename T, bool SHIFT, int N, int GROUP, int NT>
 __global__ void __launch_bounds__(NT, NT <= 256 ? 2 : 1)
 norm_bwd_kernel(BwdArgs<T> a)
@@ -927,33 +931,35 @@ moe_status_t fwd(int rows, int H, int quant, float eps, const moe_norm_fwd_args_
 // us with a warp and 54 with a block per row, 400 x 512 4.3 and 4.8 us.
 constexpr int kWarpH = 1024;
 
+// The blocks launched, each with its part of dw.
 template <typename T, bool SHIFT, int N, int GROUP, int NT>
-void launch_ring(const BwdArgs<T>& a, int parts, cudaStream_t s)
+int launch_ring(const BwdArgs<T>& a, cudaStream_t s)
 {
-    constexpr int bytes = Ring<N, NT>::kBytes;
-    if (bytes > 40 * 1024)
-        cudaFuncSetAttribute(norm_bwd_kernel<T, SHIFT, N, GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    norm_bwd_kernel<T, SHIFT, N, GROUP, NT><<<parts, NT, bytes, s>>>(a);
+    using R = Ring<N, NT>;
+    constexpr int rows = NT / GROUP;         // of a block at a time
+    const int wanted = (a.rows + rows - 1) / rows, parts = wanted < R::kParts ? wanted : R::kParts;
+    if (R::kBytes > 40 * 1024)
+        cudaFuncSetAttribute(norm_bwd_kernel<T, SHIFT, N, GROUP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
+    norm_bwd_kernel<T, SHIFT, N, GROUP, NT><<<parts, NT, R::kBytes, s>>>(a);
+    return parts;
 }
 
-// Rows that start whole, or alike (SHIFT); false for wider ones than the ring takes.
+// Rows that start whole, or alike (SHIFT); 0 for wider ones than the ring takes.
 template <typename T, bool SHIFT>
-bool launch_bwd_cut(const BwdArgs<T>& a, int parts, cudaStream_t s)
+int launch_bwd_cut(const BwdArgs<T>& a, cudaStream_t s)
 {
     constexpr int P = 32 / kPiece<T>;        // pieces of 32 values
-    if (a.H <= 256) launch_ring<T, SHIFT, P / 4, 32, 256>(a, parts, s);
-    else if (a.H <= kWarpH) launch_ring<T, SHIFT, P, 32, 256>(a, parts, s);
-    else if (a.H <= 2048) launch_ring<T, SHIFT, P / 4, 256, 256>(a, parts, s);
-    else if (a.H <= 4096) launch_ring<T, SHIFT, P / 2, 256, 256>(a, parts, s);
-    else if (a.H <= 8192) {
-        if constexpr (sizeof(T) == 2) launch_ring<T, SHIFT, P, 256, 256>(a, parts, s);
-        else launch_ring<T, SHIFT, P / 2, 512, 512>(a, parts, s);
-    } else if (sizeof(T) == 2 && a.H <= 16384) {
-        if constexpr (sizeof(T) == 2) launch_ring<T, SHIFT, P, 512, 512>(a, parts, s);
+    if (a.H <= 256) return launch_ring<T, SHIFT, P / 4, 32, 256>(a, s);
+    if (a.H <= kWarpH) return launch_ring<T, SHIFT, P, 32, 256>(a, s);
+    if (a.H <= 2048) return launch_ring<T, SHIFT, P / 4, 256, 256>(a, s);
+    if (a.H <= 4096) return launch_ring<T, SHIFT, P / 2, 256, 256>(a, s);
+    if constexpr (sizeof(T) == 2) {
+        if (a.H <= 8192) return launch_ring<T, SHIFT, P, 256, 256>(a, s);
+        if (a.H <= 16384) return launch_ring<T, SHIFT, P, 512, 512>(a, s);
     } else {
-        return false;
+        if (a.H <= 8192) return launch_ring<T, SHIFT, P / 2, 512, 512>(a, s);
     }
-    return true;
+    return 0;
 }
 
 // Rows that start each in their own way, as far as two stages and dw fit shared memory.
@@ -975,14 +981,14 @@ moe_status_t bwd(int rows, int H, const moe_norm_bwd_args_t& g, float* part, cud
                  static_cast<const T*>(g.dh), static_cast<T*>(g.dx), g.dweight ? part : nullptr,
                  g.lddy, g.ldh, g.lddh, g.lddx, rows, H};
     const Rows start = rows_start<T>(H, {g.lddy, g.ldh, g.dh ? g.lddh : g.lddy, g.lddx});
-    // a block of the warp-a-row kernel takes eight rows at a time
-    const int parts = norm_parts(H <= kWarpH && start != Rows::kOwn ? (rows + 7) / 8 : rows);
+    int parts = 0;
     if (rows > 0) {
-        if (start == Rows::kWhole) {
-            if (!launch_bwd_cut<T, false>(a, parts, s))
-                norm_bwd_loop_kernel<T, kPiece<T>><<<parts, kLoopThreads, 0, s>>>(a);
-        } else if (!(start == Rows::kAlike && launch_bwd_cut<T, true>(a, parts, s)) && !launch_bwd_window<T>(a, parts, s)) {
-            norm_bwd_loop_kernel<T, 1><<<parts, kLoopThreads, 0, s>>>(a);
+        if (start == Rows::kWhole) parts = launch_bwd_cut<T, false>(a, s);
+        else if (start == Rows::kAlike) parts = launch_bwd_cut<T, true>(a, s);
+        if (parts == 0) {
+            parts = norm_parts(rows);
+            if (start == Rows::kWhole) norm_bwd_loop_kernel<T, kPiece<T>><<<parts, kLoopThreads, 0, s>>>(a);
+            else if (!launch_bwd_window<T>(a, parts, s)) norm_bwd_loop_kernel<T, 1><<<parts, kLoopThreads, 0, s>>>(a);
         }
         count_launches();
     }
