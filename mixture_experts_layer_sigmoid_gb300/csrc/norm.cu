@@ -29,7 +29,8 @@ constexpr int kNormThreads = 256;
 // SM where a block's ring leaves room for another, else half as many (Ring::kParts).
 constexpr int kNormParts = 304;
 // Up to one row per SM the forward gives a row more threads: 8 rows of 7168 bf16
-// take 4.6 us with a thread per eight values and 8.7 with one per 28.
+// take 2.6 us with a thread per eight values and 3.1 with one per 32 (to blockwise
+// codes 3.0 and 4.4).
 constexpr int kFewRows = 152;
 
 // Sum of v over the block's threads (at most NT; NT = 32: the warp's), the same
@@ -430,7 +431,8 @@ template <typename T> struct BwdArgs {
 
 // Block b takes rows b, b + gridDim.x, ...; each thread always holds the same
 // columns, so it adds its rows' dy n into part[b] alone. For rows wider than the
-// kernels below take: 4308 x 12000 fp32 177 us, 69% (305 us with 256 threads).
+// kernels below take: 4308 x 12000 fp32 174 us, 70% (305 us with 256 threads): each
+// row is read twice, the second time from L2, and dw read and written for every row.
 constexpr int kLoopThreads = 1024;
 template <typename T, int V>
 __global__ void __launch_bounds__(kLoopThreads)
@@ -492,12 +494,12 @@ norm_bwd_loop_kernel(BwdArgs<T> a)
 // S rows per group are in flight while one is worked on. w and the partial sums
 // of dw stay in registers over all rows of the thread.
 // GROUP threads take a row (a warp, or the block); H <= GROUP * N * V.
-// 8192 x 7168 bf16 with dh: 75.5 us with the sum of the parts, 92% (197 us when
+// 8192 x 7168 bf16 with dh: 75.4 us with the sum of the parts, 92% (197 us when
 // each row was loaded, summed and read again); bound by HBM, 71 us of it here.
 // SHIFT: rows start alike off the 16-byte boundaries. The number of groups is a
 // multiple of eight where a group has more than one row, so all of its rows are
 // cut in the same columns; thread e < 2 V holds the e-th edge column, fetched one
-// row ahead. 4308 x 5259 bf16: 40 us, 67%.
+// row ahead. 4308 x 5259 bf16: 39 us, 68%.
 template <int N, int NT>
 struct Ring {
     static constexpr int kTensor = NT * N * 16;              // one tensor's rows of one stage
@@ -874,8 +876,8 @@ void launch_fwd_cut(const FwdArgs<T>& a, cudaStream_t s)
     // few rows: a thread per eight values shortens each row's own chain
     if (a.H <= 8192 && a.rows <= kFewRows) return launch_held<T, SHIFT, P / 4, 1024, QUANT, true>(a, rows, s);
     // many rows to 8-bit codes are bound by issue: more pieces per thread share what
-    // a warp does once (16384 x 2048 bf16 to MXFP8 codes 24.8 us, 30.8 with a thread
-    // per eight values; 300 x 4096 3.4 us, 4.3 with one per 32)
+    // a warp does once (16384 x 2048 bf16 to MXFP8 codes 25.0 us, 30.8 with a thread
+    // per eight values; 300 x 4096 3.1 us, 4.3 with one per 32)
     if constexpr (QUANT != MOE_NORM_PLAIN && sizeof(T) == 2)
         if (a.rows >= 8 * kSms && a.H <= 4096) {
             if (a.H <= 2048) return launch_held<T, SHIFT, P / 2, 256, QUANT>(a, rows, s);

@@ -438,8 +438,8 @@ sort_rows_kernel(IndexArgs ix, const T* x, long long ldx, T* Xp, long long ldp)
 
 // y[t] = residual[t] + sum over the slots in order of g Yp[row]. WHOLE: k <= KM,
 // the index is read once per token. 8192 x 8 rows of 7168 bf16 with residual:
-// 165 us, 105% of the copy rate (mostly reads); the row numbers in 32 bits leave
-// 64 registers and seven blocks an SM (192 us with 88).
+// 166 us, 104% of the copy rate (mostly reads); the row numbers in 32 bits leave
+// 64 registers and eight blocks an SM (192 us with 88).
 template <typename T, bool SHIFT, int KM, bool WHOLE, int GROUP>
 __global__ void __launch_bounds__(kMoveThreads)
 unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const float* __restrict__ gates,
@@ -524,7 +524,9 @@ unsort_rows_kernel(IndexArgs ix, const T* __restrict__ Yp, long long ldp, const 
 
 // The first blocks: dYp[row_j] = g_j dY[t] and dg_j = <dY[t], Yp[row_j]>, GROUP
 // (a warp, or NT) threads a token. The blocks after them: padding rows. 16384 x
-// 8 rows of 4096 bf16: 331 us with the padding, 100%.
+// 8 rows of 4096 bf16: 335 us with the padding, 98%. Shifted rows of more than four
+// slots do not fit the 80 registers that six blocks an SM leave (up to 252 bytes
+// spilled): part of what 8192 x 8 rows of 4095 take, 271 us, 62%.
 template <typename T, bool SHIFT, int KM, int NT, int GROUP, bool DG>
 __global__ void __launch_bounds__(NT, NT == kMoveThreads ? 6 : 1)
 unsort_bwd_kernel(IndexArgs ix, const T* __restrict__ dY, long long lddy, const T* Yp, long long ldp,
