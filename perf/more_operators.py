@@ -139,14 +139,15 @@ def _weights(g, E, K, N, layout, dtype):
 
 
 def _codes_of(x):
-    """E4M3 codes (as bytes) and fp32 scales of 1x128 blocks."""
+    """E4M3 codes (as bytes) and fp32 scales of 1x128 blocks. (A tensor of 448s divides;
+    a number would be multiplied by its reciprocal on the GPU.)"""
     M, K = x.shape
     codes = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     scales = torch.empty((M, K // 128), device=x.device)
     for r in range(0, M, 16384):
         b = x[r:r + 16384].float().view(-1, K // 128, 128)
         amax = b.abs().amax(2)
-        sc = torch.where(amax == 0, torch.ones_like(amax), amax / 448.0)
+        sc = torch.where(amax == 0, torch.ones_like(amax), amax / torch.full_like(amax, 448.0))
         scales[r:r + 16384] = sc
         codes[r:r + 16384] = (b / sc[..., None]).to(torch.float8_e4m3fn).view(torch.uint8).view(-1, K)
     return codes, scales
@@ -158,7 +159,7 @@ def _tile_codes(w):
     v = torch.zeros((-(-R // 128) * 128, -(-C // 128) * 128), device=w.device)
     v[:R, :C] = w
     amax = v.abs().view(v.shape[0] // 128, 128, v.shape[1] // 128, 128).amax((1, 3))
-    sc = torch.where(amax == 0, torch.ones_like(amax), amax / 448.0)
+    sc = torch.where(amax == 0, torch.ones_like(amax), amax / torch.full_like(amax, 448.0))
     q = (v / sc.repeat_interleave(128, 0).repeat_interleave(128, 1)).to(torch.float8_e4m3fn)
     return q[:R, :C].contiguous().view(torch.uint8), sc
 
@@ -226,7 +227,7 @@ def _run_plain(s, case):
             n = max((o + -(-c // a) * a for _, o, c in s["seg"]), default=0)
         b = s["x"][:n].float().view(n, K // 128, 128)
         amax = b.abs().amax(2)
-        sc = torch.where(amax == 0, torch.ones_like(amax), amax / 448.0)
+        sc = torch.where(amax == 0, torch.ones_like(amax), amax / torch.full_like(amax, 448.0))
         s["scales"][:n] = sc
         s["codes"][:n] = (b / sc[..., None]).to(torch.float8_e4m3fn).view(torch.uint8).view(n, K)
         return {"codes": s["codes"].view(torch.float8_e4m3fn), "scales": s["scales"]}
