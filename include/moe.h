@@ -569,6 +569,93 @@ moe_status_t moe_clip_workspace_size(int count, size_t* ws_bytes);
 moe_status_t moe_clip_grad_norm(int count, const moe_grad_t* list, float max_norm, float* norm,
                                 void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Products over rows sorted by expert
+ *
+ * What stands between moe_sort_rows and moe_unsort_rows for experts of the
+ * caller's own. Conventions as above, and:
+ *   - segment e holds the rows from offsets[e] on: counts[e] of them (without
+ *     counts all up to offsets[e + 1]) belong to the expert, the others up to
+ *     offsets[e + 1] are padding. offsets and counts are moe_sort_index's or a
+ *     layer's, read on the device; what they hold is clamped to the row buffers;
+ *   - padding rows of an input are not read and those of an output are written
+ *     as zeros; rows past the last segment are neither read nor written;
+ *   - each value depends on its own row (or expert) alone: infinities and NaN
+ *     elsewhere do not reach it;
+ *   - row strides (ld*) count elements and are at least a row's values, in any
+ *     alignment for moe_grouped_*: operands whose pointer and strides are
+ *     multiples of 16 bytes are read by TMA, others by loads that cost more.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int E;                   /* experts, 1..1024                               */
+    int dtype;               /* MOE_FP32 or MOE_BF16                           */
+    long long rows;          /* rows of the row buffers, 0..2^31 - 2           */
+    const int32_t* offsets;  /* E + 1; NULL with E = 1: one segment, all rows  */
+    const int32_t* counts;   /* E, or NULL                                     */
+} moe_groups_t;
+
+/* Y[r] = X[r] W_e for the rows r of each segment e; X rows x K, Y rows x N, of
+ * type groups->dtype (products of bf16 values are exact and summed in fp32 on
+ * the tensor cores; fp32 values use fp32 FMAs), rounded once.
+ * W_e[k][n] stands at W + e sw + k ldw + n, or with w_nk at W + e sw + n ldw + k
+ * (weights stored out x in). The gradient of X is the same call on dY with the
+ * other w_nk and K and N exchanged.
+ * Errors: INVALID_ARG (null pointers, sizes out of range, K or N outside
+ * 1..2^20, a stride below a row's values, sw below an expert's), MISALIGNED (a
+ * pointer not on a 16-byte boundary; offsets and counts 4), CUDA. */
+moe_status_t moe_grouped_matmul(const moe_groups_t* groups, int K, int N, const void* X, long long ldx,
+                                const void* W, long long ldw, long long sw, int w_nk, void* Y, long long ldy,
+                                moe_stream_t stream);
+
+/* D_e[m][n] = sum over the expert's rows r of A[r][m] B[r][n], overwritten, zeros
+ * for an expert without rows; A rows x M, B rows x N, D_e[m][n] at D + e sd +
+ * m ldd + n, of type groups->dtype. With A = X and B = dY it is the gradient of
+ * W (K x N); with A = dY and B = X that of weights stored out x in.
+ * Errors: as moe_grouped_matmul. */
+moe_status_t moe_grouped_wgrad(const moe_groups_t* groups, int M, int N, const void* A, long long lda,
+                               const void* B, long long ldb, void* D, long long ldd, long long sd,
+                               moe_stream_t stream);
+
+/* The product on E4M3 codes with fp32 scales of 128 values: A is rows x K codes
+ * with one scale per 1x128 block (SA rows x K/128: moe_add_rms_norm's, moe_quantize_rows'
+ * or moe_fp8_quantize's), B_e K x N codes with one per 128x128 tile (moe_fp8_quantize
+ * with MOE_Q_TILES over the E K x N weights), K a multiple of 128, N any:
+ *   Y[r][n] = sum_kb SA[r][kb] SB_e[kb][n/128] sum_{k in block kb} A[r][k] B_e[k][n],
+ * code products and their sums of 128 in fp32 on the tensor cores, the scaled sums in
+ * fp32 FMAs in ascending kb, rounded once to groups->dtype.
+ * B_e[k][n] at B + e sb + k ldb + n with SB_e[kb][nb] at SB + e ssb + kb ldsb + nb, or
+ * with b_nk B + e sb + n ldb + k and SB + e ssb + nb ldsb + kb (the transpose's view of
+ * the same codes: the gradient of A's rows takes the codes of dY and this view).
+ * Errors: as moe_grouped_matmul, and INVALID_ARG for K not a multiple of 128,
+ * MISALIGNED for lda, ldb or sb not multiples of 16. */
+typedef struct {
+    const uint8_t* A;  long long lda;
+    const float*   SA; long long ldsa;
+    const uint8_t* B;  long long ldb, sb;
+    const float*   SB; long long ldsb, ssb;
+    int            b_nk;
+    void*          Y;  long long ldy;
+} moe_fp8_matmul_args_t;
+moe_status_t moe_fp8_matmul(const moe_groups_t* groups, int K, int N, const moe_fp8_matmul_args_t* args,
+                            moe_stream_t stream);
+
+/* E4M3 codes of activation rows, any number of them: one fp32 scale per 1x128 block,
+ * amax / 448 (1 where that is zero), codes of the fp32 quotient value / scale, nearest
+ * even, saturated. x rows x K of dtype (MOE_FP32, MOE_BF16), K a multiple of 128;
+ * codes rows x K (row stride ldc), scales rows x K/128 (row stride lds). With in_use
+ * (one device int, e.g. offsets + E) only the rows below *in_use are read and written.
+ * A NaN's code is NaN; a block that holds an infinity has an infinite scale.
+ * Errors: INVALID_ARG, MISALIGNED (a pointer, or ldx or ldc not multiples of 16
+ * bytes), CUDA. */
+moe_status_t moe_quantize_rows(long long rows, int K, int dtype, const void* x, long long ldx, uint8_t* codes,
+                               long long ldc, float* scales, long long lds, const int32_t* in_use,
+                               moe_stream_t stream);
+
+/* Synchronise `stream`, then say whether a device-side wait of the products above ran
+ * out on the current device since the last such call (MOE_ERR_DEVICE_TIMEOUT: their
+ * outputs since then cannot be used), as moe_read_status does for the layer. */
+moe_status_t moe_products_status(moe_stream_t stream);
+
 /* MOE_ABI_VERSION of the loaded library. */
 int moe_abi_version(void);
 

@@ -39,7 +39,8 @@ EXPORTS = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_size", "moe_for
            "moe_add_rms_norm", "moe_norm_workspace_size", "moe_add_rms_norm_backward",
            "moe_sort_rows_cap", "moe_sort_index", "moe_sort_rows", "moe_unsort_rows",
            "moe_unsort_rows_backward", "moe_clip_workspace_size", "moe_clip_grad_norm",
-           "moe_abi_version")
+           "moe_grouped_matmul", "moe_grouped_wgrad", "moe_fp8_matmul", "moe_quantize_rows",
+           "moe_products_status", "moe_abi_version")
 MOE_Q_ROWS, MOE_Q_TILES, MOE_Q_COLS_T, MOE_Q_TILES_T = 0, 1, 2, 3
 
 
@@ -86,6 +87,17 @@ class moe_sorted_t(ctypes.Structure):
 class moe_grad_t(ctypes.Structure):
     _fields_ = [("g", _vp), ("out", _vp), ("n", ctypes.c_longlong), ("dtype", ctypes.c_int),
                 ("reserved", ctypes.c_int)]
+
+
+class moe_groups_t(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("dtype", ctypes.c_int), ("rows", ctypes.c_longlong), ("offsets", _vp),
+                ("counts", _vp)]
+
+
+class moe_fp8_matmul_args_t(ctypes.Structure):
+    _fields_ = [("A", _vp), ("lda", ctypes.c_longlong), ("SA", _vp), ("ldsa", ctypes.c_longlong), ("B", _vp),
+                ("ldb", ctypes.c_longlong), ("sb", ctypes.c_longlong), ("SB", _vp), ("ldsb", ctypes.c_longlong),
+                ("ssb", ctypes.c_longlong), ("b_nk", ctypes.c_int), ("Y", _vp), ("ldy", ctypes.c_longlong)]
 
 
 class MoEError(RuntimeError):
@@ -137,6 +149,11 @@ def load_library() -> ctypes.CDLL:
         lib.moe_unsort_rows_backward.argtypes = [P(moe_sorted_t), _vp, ll, _vp, ll, _vp, _vp, ll, _vp, _vp]
         lib.moe_clip_workspace_size.argtypes = [i, P(ctypes.c_size_t)]
         lib.moe_clip_grad_norm.argtypes = [i, _vp, ctypes.c_float, _vp, _vp, ctypes.c_size_t, _vp]
+        lib.moe_grouped_matmul.argtypes = [P(moe_groups_t), i, i, _vp, ll, _vp, ll, ll, i, _vp, ll, _vp]
+        lib.moe_grouped_wgrad.argtypes = [P(moe_groups_t), i, i, _vp, ll, _vp, ll, _vp, ll, ll, _vp]
+        lib.moe_fp8_matmul.argtypes = [P(moe_groups_t), i, i, P(moe_fp8_matmul_args_t), _vp]
+        lib.moe_quantize_rows.argtypes = [ll, i, i, _vp, ll, _vp, ll, _vp, ll, _vp, _vp]
+        lib.moe_products_status.argtypes = [_vp]
         lib.moe_abi_version.argtypes = []
         for n in EXPORTS:
             if n not in ("moe_status_string", "moe_abi_version"):
@@ -395,5 +412,6 @@ class MoELayer:
 
 # the operators around the layer, on torch tensors
 from .operators import (MOE_NORM_FP8_BLOCK, MOE_NORM_MXFP8, MOE_NORM_PLAIN, add_rms_norm,  # noqa: E402
-                        add_rms_norm_backward, clip_grad_norm, sort_index, sort_rows, unsort_rows,
-                        unsort_rows_backward)
+                        add_rms_norm_backward, clip_grad_norm, fp8_matmul, grouped_matmul,
+                        grouped_matmul_backward, products_status, quantize_rows, quantize_tiles, sort_index,
+                        sort_rows, unsort_rows, unsort_rows_backward)

@@ -2,8 +2,8 @@
 
 Torch allocates outputs and scratch and supplies the current stream of the
 tensors' device; every value is computed by the kernels behind include/moe.h
-(``moe_add_rms_norm``, ``moe_sort_*``, ``moe_unsort_*``, ``moe_clip_grad_norm``),
-whose entries describe the mathematics, the limits and the errors. Activations
+(``moe_add_rms_norm``, ``moe_sort_*``, ``moe_unsort_*``, ``moe_clip_grad_norm``,
+``moe_grouped_*``, ``moe_fp8_matmul``, ``moe_quantize_rows``), whose entries describe the mathematics, the limits and the errors. Activations
 are fp32 or bf16 matrices whose last dimension is contiguous (any row stride).
 Wrong devices, types and shapes raise ValueError here; what the library
 refuses raises MoEError.
@@ -14,9 +14,9 @@ import array
 import ctypes
 from typing import Dict, Optional, Sequence
 
-from . import (MOE_BF16, MOE_FP32, MOE_OK, MoEError, load_library, moe_clip_workspace_size,
-               moe_norm_bwd_args_t, moe_norm_fwd_args_t, moe_norm_workspace_size, moe_sort_rows_cap,
-               moe_sorted_t)
+from . import (MOE_BF16, MOE_FP32, MOE_OK, MOE_Q_TILES, MoEError, load_library, moe_clip_workspace_size,
+               moe_fp8_matmul_args_t, moe_groups_t, moe_norm_bwd_args_t, moe_norm_fwd_args_t,
+               moe_norm_workspace_size, moe_sort_rows_cap, moe_sorted_t)
 
 MOE_NORM_PLAIN, MOE_NORM_FP8_BLOCK, MOE_NORM_MXFP8 = 0, 1, 2
 
@@ -311,3 +311,230 @@ def clip_grad_norm(grads: Sequence, max_norm: float, outs: Optional[Sequence] = 
     _call("moe_clip_grad_norm", dev, lib.moe_clip_grad_norm, len(grads), table.buffer_info()[0], max_norm,
           norm.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return norm
+
+
+def _groups(index, rows, E, dtype, dev):
+    """The segments of an index (or, None, of one expert that has all rows)."""
+    if index is None:
+        if E != 1:
+            raise ValueError("index: without one there is one expert")
+        return moe_groups_t(1, _dtypes[dtype], rows, None, None)
+    offsets, counts = index.get("offsets"), index.get("counts")
+    i32 = _torch.int32
+    if (offsets is None or offsets.dtype != i32 or offsets.get_device() != dev or not offsets.is_contiguous() or
+            offsets.numel() != E + 1):
+        raise ValueError(f"offsets: {E + 1} contiguous int32 values on the rows' device are needed")
+    if counts is None:
+        return moe_groups_t(E, _dtypes[dtype], rows, offsets.data_ptr(), None)
+    if counts.dtype != i32 or counts.get_device() != dev or not counts.is_contiguous() or counts.numel() != E:
+        raise ValueError(f"counts: {E} contiguous int32 values on the rows' device are needed")
+    return moe_groups_t(E, _dtypes[dtype], rows, offsets.data_ptr(), counts.data_ptr())
+
+
+def _experts(w, name, dtype, dev, shape=None):
+    """Checks E x K x N weights; returns (row stride, stride of an expert, whether
+    they are stored N x K). Either of the last two dimensions is contiguous."""
+    if w.get_device() != dev or dev < 0 or w.dtype != dtype or len(w.shape) != 3 or (shape is not None and w.shape != shape):
+        raise ValueError(f"{name}: an {'E x K x N' if shape is None else tuple(shape)} {dtype} tensor on the rows' device is "
+                         f"needed, got {tuple(w.shape)} {w.dtype} on {w.device}")
+    E, K, N = w.shape
+    se, sk, sn = w.stride()
+    if N == 1 and sk == 1:
+        ld, nk, least = K, 1, K
+    elif sn == 1 or N == 1:
+        ld, nk, least = (sk if K > 1 else N), 0, (K - 1) * sk + N
+    elif sk == 1 or K == 1:
+        ld, nk, least = sn, 1, (N - 1) * sn + K
+    else:
+        raise ValueError(f"{name}: one of the last two dimensions has to be contiguous")
+    return ld, se if E > 1 else least, nk
+
+
+def _rows_out(out, name, rows, H, like, dtype):
+    """The output rows (new ones if None) and their stride."""
+    if out is None:
+        return _torch.empty((rows, H), dtype=dtype, device=like.device), H
+    if out.shape != (rows, H) or out.get_device() != like.get_device() or out.dtype != dtype:
+        raise ValueError(f"{name}: {tuple(out.shape)} {out.dtype} on {out.device}, expected ({rows}, {H}) {dtype} on {like.device}")
+    ld, one = out.stride()
+    if one != 1 and H > 1:
+        raise ValueError(f"{name}: the last dimension has to be contiguous")
+    return out, ld if rows > 1 else H
+
+
+def grouped_matmul(rows, w, index, out=None):
+    """``out[r] = rows[r] @ w[e]`` for the rows of each expert's segment
+    (moe_grouped_matmul): ``rows`` (R x K) as sort_rows gives them, ``w`` (E x K
+    x N) contiguous in either of its last two dimensions (weights stored out x
+    in are passed as their transposed view), ``index`` the sort's or a layer's
+    ``offsets`` and, where there is padding, ``counts``. Padding rows come out as
+    zeros; rows behind the last segment are neither read nor written."""
+    lib = _load()
+    ldx = _act(rows, "rows")
+    R, K = rows.shape
+    dev = rows.get_device()
+    ldw, sw, nk = _experts(w, "w", rows.dtype, dev)
+    E, Kw, N = w.shape
+    if Kw != K:
+        raise ValueError(f"w: {Kw} x {N} for rows of {K}")
+    g = _groups(index, R, E, rows.dtype, dev)
+    out, ldy = _rows_out(out, "out", R, N, rows, rows.dtype)
+    _call("moe_grouped_matmul", dev, lib.moe_grouped_matmul, ctypes.byref(g), K, N, rows.data_ptr(), ldx, w.data_ptr(), ldw,
+          sw, nk, out.data_ptr(), ldy)
+    return out
+
+
+def grouped_matmul_backward(dY, rows, w, index, *, want_drows: bool = True, want_dw: bool = True, drows=None, dw=None):
+    """Gradients of grouped_matmul (moe_grouped_matmul, moe_grouped_wgrad):
+    ``(drows, dw)``, ``drows[r] = dY[r] @ w[e].T`` with rows outside the segments
+    as there, and ``dw[e]`` the sum of its rows' ``rows[r].T @ dY[r]``, zeros for
+    an expert without rows, laid out as ``w``. ``drows`` and ``dw`` may be given.
+    ``rows`` is only read for dw, ``w`` only for drows (then its shape and strides
+    still say dw's)."""
+    lib = _load()
+    t = _torch
+    lddy = _act(dY, "dY")
+    R, N = dY.shape
+    dev = dY.get_device()
+    ldw, sw, nk = _experts(w, "w", dY.dtype, dev)
+    E, K, Nw = w.shape
+    if Nw != N:
+        raise ValueError(f"w: {K} x {Nw} for gradients of {N}")
+    ldx = _act(rows, "rows", (R, K), dY)
+    g = _groups(index, R, E, dY.dtype, dev)
+    if want_drows:
+        drows, ldd = _rows_out(drows, "drows", R, K, dY, dY.dtype)
+        _call("moe_grouped_matmul", dev, lib.moe_grouped_matmul, ctypes.byref(g), N, K, dY.data_ptr(), lddy, w.data_ptr(),
+              ldw, sw, 1 - nk, drows.data_ptr(), ldd)
+    if want_dw:
+        if dw is None:
+            dw = t.empty((E, N, K), dtype=w.dtype, device=w.device).transpose(1, 2) if nk else t.empty(
+                (E, K, N), dtype=w.dtype, device=w.device)
+        ldg, sg, gnk = _experts(dw, "dw", dY.dtype, dev, w.shape)
+        if gnk:
+            _call("moe_grouped_wgrad", dev, lib.moe_grouped_wgrad, ctypes.byref(g), N, K, dY.data_ptr(), lddy,
+                  rows.data_ptr(), ldx, dw.data_ptr(), ldg, sg)
+        else:
+            _call("moe_grouped_wgrad", dev, lib.moe_grouped_wgrad, ctypes.byref(g), K, N, rows.data_ptr(), ldx,
+                  dY.data_ptr(), lddy, dw.data_ptr(), ldg, sg)
+    return (drows if want_drows else None), (dw if want_dw else None)
+
+
+def _bytes(t, name, dtype, dev, shape):
+    if t.dtype != dtype or t.get_device() != dev or dev < 0 or t.shape != shape:
+        raise ValueError(f"{name}: {tuple(shape)} {dtype} on the codes' device is needed, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the last dimension has to be contiguous")
+    return ld if shape[0] > 1 else shape[1]
+
+
+def fp8_matmul(codes, scales, w_codes, w_scales, index=None, *, dtype=None, out=None):
+    """The product on E4M3 codes with a scale for each block of 128
+    (moe_fp8_matmul): ``codes`` (R x K uint8) with ``scales`` (R x K/128 fp32), as
+    add_rms_norm and quantize_rows give them, times ``w_codes`` (E x K x N uint8,
+    or K x N without an index) with ``w_scales`` (E x K/128 x ceil(N/128)), as
+    quantize_tiles gives them. Either of the weights' last two dimensions may be
+    the contiguous one, the same in both tensors: the transposed views of codes
+    and scales give the product with the transposed weights. ``dtype`` (default
+    bf16) or ``out`` says fp32 or bf16; padding rows and rows behind the last
+    segment as in grouped_matmul."""
+    lib = _load()
+    t = _torch
+    if codes.dim() != 2 or codes.dtype != t.uint8 or not codes.is_cuda:
+        raise ValueError("codes: a 2-D uint8 CUDA tensor is needed")
+    dev = codes.get_device()
+    R, K = codes.shape
+    if w_codes.dim() == 2:
+        if index is not None:
+            raise ValueError("w_codes: E x K x N codes are needed with an index")
+        w_codes, w_scales = w_codes[None], w_scales[None]
+    if K % 128:
+        raise ValueError(f"codes: {K} columns are not a multiple of 128")
+    ldb, sb, nk = _experts(w_codes, "w_codes", t.uint8, dev)
+    E, Kw, N = w_codes.shape
+    if Kw != K:
+        raise ValueError(f"w_codes: {Kw} x {N} for codes of {K}")
+    nb = -(-N // 128)
+    _experts(w_scales, "w_scales", t.float32, dev, (E, K // 128, nb))
+    se, sk, sn = w_scales.stride()
+    if nk:                               # the scales' rows run along n
+        if sk != 1 and K > 128:
+            raise ValueError("w_scales: contiguous in the dimension in which w_codes is")
+        ldsb = sn if nb > 1 else K // 128
+    else:
+        if sn != 1 and nb > 1:
+            raise ValueError("w_scales: contiguous in the dimension in which w_codes is")
+        ldsb = sk if K > 128 else nb
+    if out is not None:
+        dtype = out.dtype if dtype is None else dtype
+    elif dtype is None:
+        dtype = t.bfloat16
+    if dtype not in _dtypes:
+        raise ValueError(f"dtype: fp32 or bf16, got {dtype}")
+    a = moe_fp8_matmul_args_t(codes.data_ptr(), _bytes(codes, "codes", t.uint8, dev, codes.shape))
+    a.ldsa = _bytes(scales, "scales", t.float32, dev, (R, K // 128))
+    a.SA, a.B, a.ldb, a.sb, a.b_nk = scales.data_ptr(), w_codes.data_ptr(), ldb, sb, nk
+    a.SB, a.ldsb, a.ssb = w_scales.data_ptr(), ldsb, se if E > 1 else nb * (K // 128)
+    g = _groups(index, R, E, dtype, dev)
+    out, a.ldy = _rows_out(out, "out", R, N, codes, dtype)
+    a.Y = out.data_ptr()
+    _call("moe_fp8_matmul", dev, lib.moe_fp8_matmul, ctypes.byref(g), K, N, ctypes.byref(a))
+    return out
+
+
+def quantize_rows(x, index=None, *, codes=None, scales=None):
+    """E4M3 codes (uint8) and fp32 scales of 1x128 blocks of activation rows
+    (moe_quantize_rows), any number of rows, columns a multiple of 128. With an
+    ``index`` only the rows in use are read and written."""
+    lib = _load()
+    t = _torch
+    ldx = _act(x, "x")
+    R, K = x.shape
+    dev = x.get_device()
+    if K % 128:
+        raise ValueError(f"x: {K} columns are not a multiple of 128")
+    if codes is None:
+        codes = t.empty((R, K), dtype=t.uint8, device=x.device)
+    if scales is None:
+        scales = t.empty((R, K // 128), dtype=t.float32, device=x.device)
+    ldc, lds = _bytes(codes, "codes", t.uint8, dev, (R, K)), _bytes(scales, "scales", t.float32, dev, (R, K // 128))
+    in_use = None
+    if index is not None:
+        offsets = index.get("offsets")
+        if (offsets is None or offsets.dtype != t.int32 or offsets.get_device() != dev or not offsets.is_contiguous() or
+                offsets.numel() < 2):
+            raise ValueError("offsets: contiguous int32, one value for each expert and one more, on the rows' device")
+        in_use = offsets.data_ptr() + 4 * (offsets.numel() - 1)
+    _call("moe_quantize_rows", dev, lib.moe_quantize_rows, R, K, _dtypes[x.dtype], x.data_ptr(), ldx, codes.data_ptr(), ldc,
+          scales.data_ptr(), lds, in_use)
+    return codes, scales
+
+
+def quantize_tiles(w):
+    """E4M3 codes and fp32 scales of 128x128 tiles of bf16 weights (moe_fp8_quantize
+    with MOE_Q_TILES): E x K x N or K x N, contiguous, K and N multiples of 128.
+    Their transposed views are the codes and scales of the transposed weights."""
+    lib = _load()
+    t = _torch
+    if not w.is_cuda or w.dtype != t.bfloat16 or w.dim() not in (2, 3) or not w.is_contiguous():
+        raise ValueError("w: a contiguous 2-D or 3-D bf16 CUDA tensor is needed")
+    K, N = w.shape[-2:]
+    if K % 128 or N % 128 or w.numel() == 0 or w.numel() // N >= 2 ** 31:
+        raise ValueError(f"w: {K} x {N} is not a multiple of 128 x 128, or there are too many rows")
+    codes = t.empty(w.shape, dtype=t.uint8, device=w.device)
+    scales = t.empty((*w.shape[:-2], K // 128, N // 128), dtype=t.float32, device=w.device)
+    _call("moe_fp8_quantize", w.get_device(), lib.moe_fp8_quantize, w.numel() // N, N, MOE_Q_TILES, w.data_ptr(),
+          codes.data_ptr(), scales.data_ptr(), None, None)
+    return codes, scales
+
+
+def products_status(device: Optional[int] = None) -> int:
+    """Waits for the current stream of a device (default: the current one) and
+    returns moe_products_status: MOE_OK, or MOE_ERR_DEVICE_TIMEOUT if a product's
+    device-side wait ran out there since the last call."""
+    lib = _load()
+    cuda = _torch.cuda
+    dev = cuda.current_device() if device is None else device
+    with cuda.device(dev):
+        return lib.moe_products_status(_stream(dev))
