@@ -103,8 +103,12 @@ struct Fp8Rows {
     moe_fp8_matmul_args_t a;
 };
 
-cudaError_t launch_grouped_rows_simt(const GroupedRows& p, int dtype, int num_sms, cudaStream_t s);
-cudaError_t launch_grouped_wgrad_simt(const GroupedWgrad& p, int dtype, int num_sms, cudaStream_t s);
+// fp32
+cudaError_t launch_grouped_rows_simt(const GroupedRows& p, int num_sms, cudaStream_t s);
+cudaError_t launch_grouped_wgrad_simt(const GroupedWgrad& p, int num_sms, cudaStream_t s);
+// bf16
+cudaError_t launch_grouped_rows_tc(const GroupedRows& p, int num_sms, cudaStream_t s);
+cudaError_t launch_grouped_wgrad_tc(const GroupedWgrad& p, int num_sms, cudaStream_t s);
 cudaError_t launch_fp8_rows(const Fp8Rows& p, int num_sms, cudaStream_t s);
 
 }  // namespace moe

@@ -191,13 +191,13 @@ cudaError_t wgrad_simt(const GroupedWgrad& p, int num_sms, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_grouped_rows_simt(const GroupedRows& p, int dtype, int num_sms, cudaStream_t s)
+cudaError_t launch_grouped_rows_simt(const GroupedRows& p, int num_sms, cudaStream_t s)
 {
-    return dtype == MOE_FP32 ? rows_simt<float, 64, 64>(p, num_sms, s) : rows_simt<__nv_bfloat16, 64, 64>(p, num_sms, s);
+    return rows_simt<float, 64, 64>(p, num_sms, s);
 }
-cudaError_t launch_grouped_wgrad_simt(const GroupedWgrad& p, int dtype, int num_sms, cudaStream_t s)
+cudaError_t launch_grouped_wgrad_simt(const GroupedWgrad& p, int num_sms, cudaStream_t s)
 {
-    return dtype == MOE_FP32 ? wgrad_simt<float, 64, 64>(p, num_sms, s) : wgrad_simt<__nv_bfloat16, 64, 64>(p, num_sms, s);
+    return wgrad_simt<float, 64, 64>(p, num_sms, s);
 }
 
 }  // namespace moe

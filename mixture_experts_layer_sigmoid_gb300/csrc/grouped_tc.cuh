@@ -1,0 +1,604 @@
+// grouped_tc.cuh -- products grouped by expert on the sm_103a tensor cores (bf16
+// operands, fp32 accumulation in tensor memory): one kernel template, instantiated for
+// rows (grouped_tc_rows.cu) and weight gradients (grouped_tc_wgrad.cu).
+//
+//   rows            Y[r][n] = sum_k X[r][k] W[e(r)][k][n], tiles of 128 rows of one segment
+//                   (256 in a CTA pair) by up to 256 columns
+//   weight gradient D[e][m][n] = sum over the expert's rows r of A[r][m] B[r][n]
+//
+// Persistent blocks, one to an SM. Warp 0 loads 64-deep blocks of both operands into a
+// ring of shared-memory stages by TMA (128-byte swizzle); warp 1 issues tcgen05.mma from
+// one elected thread into one of two 256-column accumulators; warps 2-5 read the other
+// one (tcgen05.ld, a row to a thread) and store it through a swizzled staging buffer in
+// whole lines. Segments start at any row: a tile's A box simply runs into the next
+// expert's rows, whose products are not stored.
+//   - The issuing loops run in an elected thread (elect.sync): from a branch on the lane
+//     number the compiler cannot use the uniform datapath, and a block of four MMAs, its
+//     commit and its wait took 536 cycles instead of 293 (512 is the time of the MMAs).
+//   - CTA pairs (cta_group::2, M = 256) halve what a block loads and reads of B: 64 bytes a
+//     cycle of shared memory for operands and 64 for loads, where a single CTA needs 96 and 96.
+//   - The columns of the last tile need no padding: the MMA's N is the tile's own.
+//   - A weight gradient's contraction ends inside a 64-row block that also holds rows of
+//     others (perhaps NaN). That block's loads complete on a barrier of their own; a fixing
+//     warp zeroes the rows up to the next multiple of 16 in both operands and then signals
+//     the block; the MMAs stop at that multiple.
+//   - GUARD: operands that TMA cannot take (strides off the 16-byte boundaries) are loaded by
+//     four warps, as pairs of aligned 16-byte windows that are shifted, into the same layout.
+#pragma once
+#include "grouped.cuh"
+#include "ptx.cuh"
+
+#include <atomic>
+#include <cudaTypedefs.h>
+#include <mutex>
+
+namespace moe {
+namespace gtc {
+
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int STRIPE = 64 * 128;               // 64 columns of a 64-deep block, MN-major
+constexpr int kSmemMax = 232448;               // 227 KB
+constexpr int kStaging = 4 * 4096;             // per epilogue warp 32 rows of 128 bytes
+constexpr int kPre = (kMaxGroups + 4) * 4;     // row-tile prefix
+constexpr int kBars = 512;
+constexpr int kGroupSpan = 16;                 // as the layer's engine: a weight tile's units run at
+                                               // most this many tiles apart
+
+struct Args {
+    Groups g;
+    int K;                    // rows: contraction; unused by weight gradients
+    int M, N;                 // outputs of a weight gradient (M); columns (N)
+    void* out;
+    long long ldo, so;
+    int vec;                  // outputs in 16-byte pieces
+    const __nv_bfloat16 *A, *B;   // GUARD
+    long long lda, ldb, sb;
+};
+
+template <bool PAIR>
+struct Cfg {
+    static constexpr int A_BYTES = BM * BK * 2;
+    static constexpr int B_COLS = PAIR ? BN / 2 : BN;
+    static constexpr int STAGE = A_BYTES + B_COLS * BK * 2;
+    static constexpr int STAGES = (kSmemMax - 1024 - kStaging - kPre - kBars) / STAGE;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + kStaging + kPre + kBars;
+};
+
+// Set by a wait that ran out (one word per translation unit and device).
+static __device__ DeviceStatus wait_status;
+
+template <bool WGRAD, bool GUARD>
+constexpr int threads() { return GUARD ? 320 : (WGRAD ? 224 : 192); }
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p != 0;
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z)
+{
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar),
+                     "r"(x), "r"(y), "r"(z) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar),
+                     "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+// A tile of outputs, as every role of a block sees it.
+struct Tile {
+    int e;
+    int row;                  // first row: of the output rows, or of the contraction
+    int m0, n0, nt;           // first column (and output row of a weight gradient); the MMA's N
+    int kblocks, tail;        // 64-deep blocks; values in the last one
+    int end, valid;           // rows: stored rows of this CTA's 128; those that are not padding
+};
+
+template <bool WGRAD, bool PAIR>
+struct Work {
+    int num_n, num_m;
+    long long total;
+    __device__ __forceinline__ void init(const Args& a, const int* pre)
+    {
+        num_n = (a.N + BN - 1) / BN;
+        num_m = WGRAD ? (a.M + (PAIR ? 2 * BM : BM) - 1) / (PAIR ? 2 * BM : BM) : pre[a.g.E];
+        total = WGRAD ? (long long)a.g.E * num_m * num_n : (long long)num_m * num_n;
+    }
+    __device__ __forceinline__ Tile at(const Args& a, const int* pre, long long w, int rank) const
+    {
+        Tile t;
+        if constexpr (WGRAD) {
+            // the smaller of the two tile counts runs fastest, so that the blocks at work
+            // cover all of that dimension and read each slice of the other once
+            const int per = num_m * num_n;
+            t.e = (int)(w / per);
+            const int r = (int)(w - (long long)t.e * per);
+            const int mu = num_n < num_m ? r / num_n : r % num_m;
+            t.n0 = (num_n < num_m ? r % num_n : r / num_m) * BN;
+            t.m0 = (PAIR ? 2 * mu + rank : mu) * BM;
+            const Segment s = segment_of(a.g, t.e);
+            t.row = s.begin;
+            t.kblocks = (s.valid + BK - 1) / BK;
+            t.tail = s.valid - (t.kblocks - 1) * BK;
+            t.end = t.valid = a.M - t.m0;
+        } else {
+            // expert by expert; within one, groups of G column tiles walk its row units, so
+            // that its rows and weights stay in L2 while they are used
+            const int q = (int)(w / num_n);
+            t.e = segment_at(pre, a.g.E, q);
+            const int u0 = pre[t.e], nu = max(pre[t.e + 1] - u0, 1);
+            const int r0 = (int)(w - (long long)u0 * num_n);
+            const int G = nu <= kGroupSpan / 2 ? max(1, kGroupSpan / nu) : kGroupSpan;
+            const int group = r0 / (nu * G), r = r0 - group * nu * G;
+            const int gsz = min(G, num_n - group * G);
+            const int mu = r / gsz;
+            t.n0 = (group * G + r % gsz) * BN;
+            const Segment s = segment_of(a.g, t.e);
+            const int first = mu * (PAIR ? 2 * BM : BM);       // row of the unit in its segment
+            const int mine = first + (PAIR ? rank * BM : 0);
+            t.row = s.begin + mine;
+            t.m0 = 0;
+            t.kblocks = first < s.valid ? (a.K + BK - 1) / BK : 0;
+            t.tail = BK;
+            t.end = s.end - t.row;
+            t.valid = s.valid - mine;
+        }
+        // the MMA's N: a multiple of 16, of 32 in a pair
+        constexpr int step = PAIR ? 32 : 16;
+        t.nt = min(BN, (a.N - t.n0 + step - 1) / step * step);
+        return t;
+    }
+};
+
+// Eight bf16 values from any 2-byte aligned address; of them `n` exist (n <= 0: zeros).
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int n)
+{
+    if (n <= 0) return make_uint4(0, 0, 0, 0);
+    if (n < 8) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < n) w[i / 2] |= (uint32_t)u[i] << (16 * (i & 1));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const unsigned off = (unsigned)(at & 15u);
+    const uint4* base = reinterpret_cast<const uint4*>(at - off);
+    const uint4 a = base[0];
+    if (off == 0) return a;
+    const uint4 b = base[1];                   // holds the last of the eight values
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8u) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const unsigned sh = (off & 2u) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                      __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+}
+// A box of `rows` rows of 64 values into shared memory, 128 bytes a row, swizzled;
+// n_rows and n_cols of them exist.
+__device__ __forceinline__ void load_box(uint32_t dst, const __nv_bfloat16* p, long long ld, int rows, int n_rows,
+                                         int n_cols, int tid)
+{
+    for (int c0 = tid; c0 < rows * 8; c0 += 4 * 128) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * 128, r = c >> 3, ch = c & 7;
+            v[i] = load8(p + r * ld + ch * 8, c < rows * 8 && r < n_rows ? n_cols - ch * 8 : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * 128, r = c >> 3, ch = c & 7;
+            if (c < rows * 8)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 + ((ch ^ (r & 7)) << 4)),
+                             "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w) : "memory");
+        }
+    }
+}
+
+template <bool WGRAD, bool B_MN, bool PAIR, bool GUARD>
+__global__ void __launch_bounds__(threads<WGRAD, GUARD>(), 1)
+kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const Args a)
+{
+    using C = Cfg<PAIR>;
+    DeviceStatus* const status = &wait_status;
+    constexpr int S = C::STAGES;
+    constexpr uint32_t IDESC = ptx::idesc_bf16<0, WGRAD, B_MN, PAIR ? 2 * BM : BM>();
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t ring = ptx::smem_u32(smem);
+    const uint32_t staging = ring + S * C::STAGE;
+    int* pre = reinterpret_cast<int*>(smem + S * C::STAGE + kStaging);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE + kStaging + kPre);
+    static_assert((3 * S + 5) * 8 + 8 + 16 <= kBars && C::SMEM % 16 == 0, "barriers");
+    const uint32_t bar0 = (ptx::smem_u32(bars) + 7u) & ~7u;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+    auto land_bar = [&](int s) { return bar0 + 8u * (2 * S + s); };
+    auto accf_bar = [&](int i) { return bar0 + 8u * (3 * S + i); };
+    auto acce_bar = [&](int i) { return bar0 + 8u * (3 * S + 2 + i); };
+    const uint32_t final_bar = bar0 + 8u * (3 * S + 4);
+    uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem + C::SMEM - 1024 - 16);
+    volatile int& abort_flag = *reinterpret_cast<volatile int*>(smem + C::SMEM - 1024 - 8);
+
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)ptx::cluster_ctarank() : 0;
+    const int unit0 = PAIR ? (int)ptx::cluster_id_x() : (int)blockIdx.x;
+    const int nunits = PAIR ? (int)ptx::nclusters_x() : (int)gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            // a weight gradient's block is signalled once by each CTA (its producer or, for
+            // the last block, its fixing warp); other blocks by the even CTA's producer
+            ptx::mbar_init(full_bar(s), GUARD ? 128 : (WGRAD && PAIR ? 2 : 1));
+            ptx::mbar_init(empty_bar(s), 1);
+            ptx::mbar_init(land_bar(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(accf_bar(i), 1);
+            ptx::mbar_init(acce_bar(i), PAIR ? 8 : 4);
+        }
+        ptx::mbar_init(final_bar, 1);
+        abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (!GUARD && warp == 0 && elect_one()) {
+        ptx::prefetch_tmap(&mA);
+        ptx::prefetch_tmap(&mB);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            ptx::tmem_alloc_pair(ptx::smem_u32(&tmem_slot), 2 * BN);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), 2 * BN);
+            ptx::tmem_relinquish();
+        }
+    }
+    if (!WGRAD) count_row_tiles<PAIR ? 2 * BM : BM>(a.g, pre);
+    ptx::tc_fence_before();
+    if (PAIR) ptx::cluster_sync();             // the peer's barriers exist before any remote signal
+    else __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    Work<WGRAD, PAIR> work;
+    work.init(a, pre);
+    auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+        return ptx::wait_bounded(bar, parity, &abort_flag, status, where);
+    };
+
+    if (warp == 0 && !GUARD) {
+        // ------------------------------------------------------- TMA loads
+        if (elect_one()) {
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (long long w = unit0; ok && w < work.total; w += nunits) {
+                const Tile t = work.at(a, pre, w, rank);
+                const int bcols = PAIR ? t.nt / 2 : t.nt, b0 = t.n0 + (PAIR ? rank * bcols : 0);
+                const int stripes = (bcols + 63) / 64;
+                const uint32_t bytes = C::A_BYTES + (B_MN ? stripes * STRIPE : C::B_COLS * BK * 2);
+                for (int kb = 0; kb < t.kblocks; ++kb) {
+                    if (!wait(empty_bar(s), ph ^ 1u, 1)) { ok = false; break; }
+                    const uint32_t dst_a = ring + s * C::STAGE, dst_b = dst_a + C::A_BYTES;
+                    const bool fix = WGRAD && kb == t.kblocks - 1 && t.tail < BK;
+                    uint32_t bar;
+                    if (fix) {
+                        bar = land_bar(s);
+                        ptx::mbar_arrive_expect_tx(bar, bytes);
+                    } else {
+                        bar = PAIR ? ptx::mapa_shared(full_bar(s), 0) : full_bar(s);
+                        if (rank == 0) {
+                            ptx::mbar_arrive_expect_tx(full_bar(s), (PAIR ? 2 : 1) * bytes);
+                            if (WGRAD && PAIR) ptx::mbar_arrive(full_bar(s));
+                        }
+                    }
+                    if constexpr (WGRAD) {
+                        const int y = t.row + kb * BK;
+#pragma unroll
+                        for (int i = 0; i < BM / 64; ++i) load_3d<PAIR>(dst_a + i * STRIPE, &mA, bar, t.m0 + 64 * i, y, 0);
+                        for (int i = 0; i < stripes; ++i) load_3d<PAIR>(dst_b + i * STRIPE, &mB, bar, b0 + 64 * i, y, 0);
+                    } else {
+                        load_3d<PAIR>(dst_a, &mA, bar, kb * BK, t.row, 0);
+                        if constexpr (B_MN) {
+                            for (int i = 0; i < stripes; ++i)
+                                load_3d<PAIR>(dst_b + i * STRIPE, &mB, bar, b0 + 64 * i, kb * BK, t.e);
+                        } else {
+                            load_3d<PAIR>(dst_b, &mB, bar, kb * BK, b0, t.e);
+                        }
+                    }
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && elect_one()) {
+            // ------------------------------------------------------- MMAs
+            int s = 0, acc = 0;
+            uint32_t ph = 0, aph = 0;
+            bool ok = true;
+            for (long long w = unit0; ok && w < work.total; w += nunits) {
+                const Tile t = work.at(a, pre, w, rank);
+                if (!wait(acce_bar(acc), aph ^ 1u, 2)) break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * BN);
+                const uint32_t id = IDESC | ((uint32_t)(t.nt >> 3) << 17);
+                for (int kb = 0; kb < t.kblocks; ++kb) {
+                    if (!wait(full_bar(s), ph, 3)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    const uint32_t pa = ring + s * C::STAGE, pb = pa + C::A_BYTES;
+                    const int steps = WGRAD && kb == t.kblocks - 1 ? (t.tail + 15) / 16 : BK / 16;
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k) {
+                        if (WGRAD && k >= steps) break;
+                        const uint64_t da = WGRAD ? ptx::smem_desc_sw128(pa + k * 2048, STRIPE, 1024)
+                                                  : ptx::smem_desc_sw128(pa + k * 32, 16, 1024);
+                        const uint64_t db = B_MN ? ptx::smem_desc_sw128(pb + k * 2048, STRIPE, 1024)
+                                                 : ptx::smem_desc_sw128(pb + k * 32, 16, 1024);
+                        const uint32_t more = (kb > 0 || k > 0) ? 1u : 0u;
+                        if (PAIR) ptx::tc_mma_f16_pair(d, da, db, id, more);
+                        else ptx::tc_mma_f16(d, da, db, id, more);
+                    }
+                    if (PAIR) ptx::tc_commit_pair(empty_bar(s), 3);
+                    else ptx::tc_commit(empty_bar(s));
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                }
+                if (!ok) break;
+                if (PAIR) ptx::tc_commit_pair(accf_bar(acc), 3);
+                else ptx::tc_commit(accf_bar(acc));
+                acc ^= 1;
+                if (acc == 0) aph ^= 1u;
+            }
+            if (PAIR) ptx::tc_commit_pair(final_bar, 3);
+            else ptx::tc_commit(final_bar);
+        }
+        __syncwarp();
+        // every MMA has completed before tensor memory is freed (the odd CTA's is written
+        // by its peer's MMAs)
+        if (lane == 0) {
+            volatile int never = 0;
+            ptx::wait_bounded(final_bar, 0, &never, status, 4);
+        }
+        __syncwarp();
+    } else if (warp < 6) {
+        // ----------------------------------------------------------- outputs
+        const int q = warp & 3;                 // this warp's quarter of the TMEM lanes
+        const uint32_t stg = staging + (uint32_t)q * 4096u;
+        int acc = 0;
+        uint32_t aph = 0;
+        for (long long w = unit0; w < work.total; w += nunits) {
+            const Tile t = work.at(a, pre, w, rank);
+            if (!__all_sync(0xffffffffu, wait(accf_bar(acc), aph, 5))) break;
+            ptx::tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+            const int rows = t.end - q * 32;    // of this warp's 32 rows those that are stored
+            const bool mine = lane + q * 32 < t.valid;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + t.n0 +
+                               (WGRAD ? t.e * a.so + (long long)(t.m0 + q * 32) * a.ldo
+                                      : (long long)(t.row + q * 32) * a.ldo);
+            const int cols = min(a.N - t.n0, BN);
+#pragma unroll 1
+            for (int u = 0; u * 64 < cols && rows > 0; ++u) {
+                uint32_t v0[32], v1[32];
+                if (t.kblocks > 0) {
+                    ptx::tmem_ld32(taddr + u * 64, v0);
+                    ptx::tmem_ld32(taddr + u * 64 + 32, v1);
+                    ptx::tmem_ld_wait();
+                }
+                if (t.kblocks == 0 || !mine) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v0[i] = v1[i] = 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t* src = j < 4 ? v0 + 8 * j : v1 + 8 * (j - 4);
+                    uint32_t p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(src[2 * i]), __uint_as_float(src[2 * i + 1]));
+                        p[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                                 "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]) : "memory");
+                }
+                __syncwarp();
+                const int left = cols - u * 64;
+                if (a.vec) {
+                    // eight lanes to a row of 128 bytes, four rows an instruction
+                    const int ch = lane & 7;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3);
+                        const uint32_t at = stg + r * 128 + ((ch ^ (r & 7)) << 4);
+                        if (r < rows) {
+                            __nv_bfloat16* dst = o + r * a.ldo + u * 64 + ch * 8;
+                            if (ch * 8 + 8 <= left) {
+                                uint4 x;
+                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+                                *reinterpret_cast<uint4*>(dst) = x;
+                            } else {
+                                for (int c = 0; ch * 8 + c < left; ++c) {
+                                    unsigned short x;
+                                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + 2 * c));
+                                    reinterpret_cast<unsigned short*>(dst)[c] = x;
+                                }
+                            }
+                        }
+                    }
+                } else {
+                    for (int r = 0; r < min(rows, 32); ++r) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = lane + 32 * h;
+                            if (c < left) {
+                                unsigned short x;
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(stg + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2));
+                                reinterpret_cast<unsigned short*>(o + r * a.ldo + u * 64)[c] = x;
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            // relaxed: nothing in memory is published, and a release would wait for the stores
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(acce_bar(acc), 0));
+                else ptx::mbar_arrive_relaxed(acce_bar(acc));
+            }
+            acc ^= 1;
+            if (acc == 0) aph ^= 1u;
+        }
+    } else if (GUARD) {
+        // ------------------------------------------- loads off the boundaries
+        const int tid = (int)threadIdx.x - 192;
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (long long w = unit0; ok && w < work.total; w += nunits) {
+            const Tile t = work.at(a, pre, w, rank);
+            const int n_cols = a.N - t.n0;
+            for (int kb = 0; kb < t.kblocks; ++kb) {
+                if (!__all_sync(0xffffffffu, wait(empty_bar(s), ph ^ 1u, 6))) { ok = false; break; }
+                const uint32_t dst_a = ring + s * C::STAGE, dst_b = dst_a + C::A_BYTES;
+                if constexpr (WGRAD) {
+                    const int n_k = kb == t.kblocks - 1 ? t.tail : BK;
+                    const long long r = t.row + kb * BK;
+                    for (int i = 0; i < BM / 64; ++i)
+                        load_box(dst_a + i * STRIPE, a.A + r * a.lda + t.m0 + 64 * i, a.lda, BK, n_k, a.M - t.m0 - 64 * i, tid);
+                    for (int i = 0; i * 64 < t.nt; ++i)
+                        load_box(dst_b + i * STRIPE, a.B + r * a.ldb + t.n0 + 64 * i, a.ldb, BK, n_k, n_cols - 64 * i, tid);
+                } else {
+                    const int k = kb * BK;
+                    load_box(dst_a, a.A + t.row * a.lda + k, a.lda, BM, t.valid, a.K - k, tid);
+                    const __nv_bfloat16* b = a.B + t.e * a.sb;
+                    if constexpr (B_MN) {
+                        for (int i = 0; i * 64 < t.nt; ++i)
+                            load_box(dst_b + i * STRIPE, b + k * a.ldb + t.n0 + 64 * i, a.ldb, BK, a.K - k, n_cols - 64 * i, tid);
+                    } else {
+                        load_box(dst_b, b + t.n0 * a.ldb + k, a.ldb, t.nt, n_cols, a.K - k, tid);
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(full_bar(s));
+                if (++s == S) { s = 0; ph ^= 1u; }
+            }
+        }
+    } else if (WGRAD) {
+        // ------------------------------- the contraction's last, partial block
+        int s0 = 0;
+        uint32_t phases = 0;
+        for (long long w = unit0; w < work.total; w += nunits) {
+            const Tile t = work.at(a, pre, w, rank);
+            if (t.kblocks == 0) continue;
+            const int s = (s0 + t.kblocks - 1) % S;
+            s0 = (s0 + t.kblocks) % S;
+            if (t.tail == BK) continue;
+            if (!__all_sync(0xffffffffu, wait(land_bar(s), (phases >> s) & 1u, 7))) break;
+            phases ^= 1u << s;
+            const int up = min((t.tail + 15) / 16 * 16, BK), n = (up - t.tail) * 8;   // 16-byte pieces of a stripe
+            const int bcols = PAIR ? t.nt / 2 : t.nt, stripes = BM / 64 + (bcols + 63) / 64;
+            const uint32_t at = ring + s * C::STAGE + t.tail * 128;
+            for (int i = lane; i < n * stripes; i += 32)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i / n * STRIPE + i % n * 16), "r"(0) : "memory");
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(full_bar(s), 0));
+                else ptx::mbar_arrive(full_bar(s));
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    if (PAIR) ptx::cluster_sync();             // both CTAs are done with tensor memory and signals
+    else __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        if (PAIR) ptx::tmem_dealloc_pair(tmem, 2 * BN);
+        else ptx::tmem_dealloc(tmem, 2 * BN);
+    }
+}
+
+// ------------------------------------------------------------------ host
+// 3-D bf16 tensor map: inner x rows x mats, boxes of 64 x box_rows x 1, 128-byte
+// swizzle, zeros outside. False where the strides are none that TMA takes.
+bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, long long mats, long long ld,
+              long long stride, int box_rows);
+// Waits for the stream and takes the word.
+inline cudaError_t take_status(int* code, cudaStream_t s)
+{
+    DeviceStatus h{};
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&h, wait_status, sizeof(h), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && h.code != 0) {
+        *code = h.code;
+        const DeviceStatus zero{};
+        e = cudaMemcpyToSymbolAsync(wait_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e;
+}
+
+template <bool WGRAD, bool B_MN, bool PAIR, bool GUARD>
+cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const Args& a, long long units, int num_sms, cudaStream_t s)
+{
+    using C = Cfg<PAIR>;
+    auto k = kernel<WGRAD, B_MN, PAIR, GUARD>;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    cfg.blockDim = dim3(threads<WGRAD, GUARD>());
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    if (PAIR) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    // per device, once: 0 = not set up, else the units that run at once
+    static std::atomic<int> slots[64];
+    int n = dev < 64 ? slots[dev].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        n = num_sms;
+        if (PAIR) {
+            cfg.gridDim = dim3(2);
+            int most = 0;
+            e = cudaOccupancyMaxActiveClusters(&most, k, &cfg);
+            if (e != cudaSuccess) return e;
+            n = most > 0 ? most : 1;
+        }
+        if (dev < 64) slots[dev].store(n, std::memory_order_release);
+    }
+    const long long grid = units < n ? (units > 0 ? units : 1) : n;
+    cfg.gridDim = dim3((unsigned)(PAIR ? 2 * grid : grid));
+    return cudaLaunchKernelEx(&cfg, k, mA, mB, a);
+}
+
+}  // namespace gtc
+
+// The code of a wait that ran out on the current device, if one did, cleared.
+cudaError_t take_rows_status(int* code, cudaStream_t s);
+cudaError_t take_wgrad_status(int* code, cudaStream_t s);
+
+}  // namespace moe

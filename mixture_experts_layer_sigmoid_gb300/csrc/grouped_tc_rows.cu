@@ -1,0 +1,71 @@
+// grouped_tc_rows.cu -- Y[r] = X[r] W_e on the tensor cores (grouped_tc.cuh has the
+// kernel): the forward product, and with the weights' other orientation the gradient of X.
+#include "grouped_tc.cuh"
+
+namespace moe {
+namespace gtc {
+
+bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, long long mats, long long ld,
+              long long stride, int box_rows)
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (!encode || (reinterpret_cast<uintptr_t>(p) & 15u) || ld % 8 || (mats > 1 && stride % 8)) return false;
+    if (mats == 1) stride = ld * rows;
+    if (stride * 2 >= (1ll << 40) || ld * 2 >= (1ll << 40)) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)mats};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u}, es[3] = {1u, 1u, 1u};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace gtc
+
+using namespace gtc;
+
+namespace {
+
+// Rows an expert has on average from which tiles go to CTA pairs.
+constexpr long long kPairRows = 512;
+
+template <bool B_MN>
+cudaError_t rows_tc(const GroupedRows& p, int num_sms, cudaStream_t s)
+{
+    Args a{};
+    a.g = p.g;
+    a.K = p.K; a.N = p.N;
+    a.out = p.Y; a.ldo = p.ldy;
+    a.vec = p.ldy % 8 == 0;
+    const bool pair = p.g.rows / p.g.E >= kPairRows;
+    const long long num_n = (p.N + BN - 1) / BN;
+    const long long units = row_tiles_bound(p.g.rows, p.g.E, pair ? 2 * BM : BM) * num_n;
+    CUtensorMap mA, mB;
+    const int bcols = pair ? BN / 2 : BN;
+    if (make_map(&mA, p.X, p.K, p.g.rows, 1, p.ldx, 0, BM) &&
+        (B_MN ? make_map(&mB, p.W, p.N, p.K, p.g.E, p.ldw, p.sw, BK) : make_map(&mB, p.W, p.K, p.N, p.g.E, p.ldw, p.sw, bcols)))
+        return pair ? launch<false, B_MN, true, false>(mA, mB, a, units, num_sms, s)
+                    : launch<false, B_MN, false, false>(mA, mB, a, units, num_sms, s);
+    a.A = static_cast<const __nv_bfloat16*>(p.X); a.lda = p.ldx;
+    a.B = static_cast<const __nv_bfloat16*>(p.W); a.ldb = p.ldw; a.sb = p.sw;
+    return launch<false, B_MN, false, true>(CUtensorMap{}, CUtensorMap{}, a,
+                                            row_tiles_bound(p.g.rows, p.g.E, BM) * num_n, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_rows_tc(const GroupedRows& p, int num_sms, cudaStream_t s)
+{
+    return p.w_nk ? rows_tc<false>(p, num_sms, s) : rows_tc<true>(p, num_sms, s);
+}
+cudaError_t take_rows_status(int* code, cudaStream_t s) { return take_status(code, s); }
+
+}  // namespace moe

@@ -4,7 +4,7 @@
 // Row codes: one thread holds eight consecutive values, sixteen neighbours share a
 // block of 128 and its largest magnitude. The kernel moves 16 or 32 bytes in and 8 out
 // per thread and is bound by HBM; kPieces loads per thread are in flight.
-#include "grouped.cuh"
+#include "grouped_tc.cuh"
 #include "mx.cuh"
 #include "rowvec.cuh"
 
@@ -145,7 +145,8 @@ moe_status_t moe_grouped_matmul(const moe_groups_t* groups, int K, int N, const 
     int sms = 0;
     if (!current_sms(&sms)) return MOE_ERR_CUDA;
     count_launches();
-    return done(launch_grouped_rows_simt(p, groups->dtype, sms, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return done(groups->dtype == MOE_FP32 ? launch_grouped_rows_simt(p, sms, s) : launch_grouped_rows_tc(p, sms, s));
 }
 
 moe_status_t moe_grouped_wgrad(const moe_groups_t* groups, int M, int N, const void* A, long long lda, const void* B,
@@ -165,7 +166,8 @@ moe_status_t moe_grouped_wgrad(const moe_groups_t* groups, int M, int N, const v
     int sms = 0;
     if (!current_sms(&sms)) return MOE_ERR_CUDA;
     count_launches();
-    return done(launch_grouped_wgrad_simt(p, groups->dtype, sms, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return done(groups->dtype == MOE_FP32 ? launch_grouped_wgrad_simt(p, sms, s) : launch_grouped_wgrad_tc(p, sms, s));
 }
 
 moe_status_t moe_fp8_matmul(const moe_groups_t* groups, int K, int N, const moe_fp8_matmul_args_t* args,
@@ -215,5 +217,9 @@ moe_status_t moe_quantize_rows(long long rows, int K, int dtype, const void* x, 
 
 moe_status_t moe_products_status(moe_stream_t stream)
 {
-    return done(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int code = 0;
+    for (auto take : {take_rows_status, take_wgrad_status})
+        if (take(&code, s) != cudaSuccess) return MOE_ERR_CUDA;
+    return code ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
