@@ -76,6 +76,21 @@ __device__ __forceinline__ bool elect_one()
     asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
     return p != 0;
 }
+// Waits for the phase with this parity, up to a number of tries, each of which the hardware
+// lets sleep a while (all of them are more than a tenth of a second). Nothing else stands in
+// the loop: with a look at the abort flag or the clock in it, the compiler's code around the
+// waits of matmul_fp8.cu's fold took 961 cycles a block instead of 711.
+__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity)
+{
+    for (int i = 0; i < (1 << 22); ++i)
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+// Records a wait that ran out.
+__device__ __forceinline__ void report_timeout(DeviceStatus* st, int where)
+{
+    if (atomicCAS(&st->code, 0, (int)MOE_ERR_DEVICE_TIMEOUT) == 0) st->where = where;
+}
 template <bool PAIR>
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z)
 {
@@ -94,11 +109,11 @@ struct Tile {
     int e;
     int row;                  // first row: of the output rows, or of the contraction
     int m0, n0, nt;           // first column (and output row of a weight gradient); the MMA's N
-    int kblocks, tail;        // 64-deep blocks; values in the last one
+    int kblocks, tail;        // blocks of the contraction; values in the last one
     int end, valid;           // rows: stored rows of this CTA's 128; those that are not padding
 };
 
-template <bool WGRAD, bool PAIR>
+template <bool WGRAD, bool PAIR, int DEPTH = BK>
 struct Work {
     int num_n, num_m;
     long long total;
@@ -122,8 +137,8 @@ struct Work {
             t.m0 = (PAIR ? 2 * mu + rank : mu) * BM;
             const Segment s = segment_of(a.g, t.e);
             t.row = s.begin;
-            t.kblocks = (s.valid + BK - 1) / BK;
-            t.tail = s.valid - (t.kblocks - 1) * BK;
+            t.kblocks = (s.valid + DEPTH - 1) / DEPTH;
+            t.tail = s.valid - (t.kblocks - 1) * DEPTH;
             t.end = t.valid = a.M - t.m0;
         } else {
             // expert by expert; within one, groups of G column tiles walk its row units, so
@@ -142,8 +157,8 @@ struct Work {
             const int mine = first + (PAIR ? rank * BM : 0);
             t.row = s.begin + mine;
             t.m0 = 0;
-            t.kblocks = first < s.valid ? (a.K + BK - 1) / BK : 0;
-            t.tail = BK;
+            t.kblocks = first < s.valid ? (a.K + DEPTH - 1) / DEPTH : 0;
+            t.tail = DEPTH;
             t.end = s.end - t.row;
             t.valid = s.valid - mine;
         }
@@ -535,10 +550,46 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
 }
 
 // ------------------------------------------------------------------ host
-// 3-D bf16 tensor map: inner x rows x mats, boxes of 64 x box_rows x 1, 128-byte
-// swizzle, zeros outside. False where the strides are none that TMA takes.
+// 3-D tensor map of bf16 values (or bytes): inner x rows x mats, boxes of 128 bytes x
+// box_rows x 1, 128-byte swizzle, zeros outside. False where the strides are none that TMA
+// takes.
 bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, long long mats, long long ld,
-              long long stride, int box_rows);
+              long long stride, int box_rows, int bytes = 2);
+
+// The units that run at once of a kernel with this much shared memory, set up on the first
+// call of each device (slots: one per kernel, zeros).
+inline cudaError_t units_at_once(const void* k, int threads, int smem, bool pair, int num_sms, std::atomic<int> (&slots)[64],
+                                 int* out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int n = dev < 64 ? slots[dev].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        n = num_sms;
+        if (pair) {
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = 2;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(2);
+            cfg.blockDim = dim3((unsigned)threads);
+            cfg.dynamicSmemBytes = (size_t)smem;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            int most = 0;
+            e = cudaOccupancyMaxActiveClusters(&most, k, &cfg);
+            if (e != cudaSuccess) return e;
+            n = most > 0 ? most : 1;
+        }
+        if (dev < 64) slots[dev].store(n, std::memory_order_release);
+    }
+    *out = n;
+    return cudaSuccess;
+}
 // Waits for the stream and takes the word.
 inline cudaError_t take_status(int* code, cudaStream_t s)
 {
@@ -571,25 +622,10 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const Args& a, 
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    // per device, once: 0 = not set up, else the units that run at once
     static std::atomic<int> slots[64];
-    int n = dev < 64 ? slots[dev].load(std::memory_order_acquire) : 0;
-    if (n == 0) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (e != cudaSuccess) return e;
-        n = num_sms;
-        if (PAIR) {
-            cfg.gridDim = dim3(2);
-            int most = 0;
-            e = cudaOccupancyMaxActiveClusters(&most, k, &cfg);
-            if (e != cudaSuccess) return e;
-            n = most > 0 ? most : 1;
-        }
-        if (dev < 64) slots[dev].store(n, std::memory_order_release);
-    }
+    int n = 0;
+    const cudaError_t e = units_at_once(reinterpret_cast<const void*>(k), threads<WGRAD, GUARD>(), C::SMEM, PAIR, num_sms, slots, &n);
+    if (e != cudaSuccess) return e;
     const long long grid = units < n ? (units > 0 ? units : 1) : n;
     cfg.gridDim = dim3((unsigned)(PAIR ? 2 * grid : grid));
     return cudaLaunchKernelEx(&cfg, k, mA, mB, a);
@@ -600,5 +636,6 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const Args& a, 
 // The code of a wait that ran out on the current device, if one did, cleared.
 cudaError_t take_rows_status(int* code, cudaStream_t s);
 cudaError_t take_wgrad_status(int* code, cudaStream_t s);
+cudaError_t take_fp8_status(int* code, cudaStream_t s);
 
 }  // namespace moe

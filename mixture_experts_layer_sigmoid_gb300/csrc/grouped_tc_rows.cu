@@ -6,7 +6,7 @@ namespace moe {
 namespace gtc {
 
 bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, long long mats, long long ld,
-              long long stride, int box_rows)
+              long long stride, int box_rows, int bytes)
 {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
@@ -17,13 +17,13 @@ bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, lo
             q == cudaDriverEntryPointSuccess)
             encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
-    if (!encode || (reinterpret_cast<uintptr_t>(p) & 15u) || ld % 8 || (mats > 1 && stride % 8)) return false;
+    if (!encode || (reinterpret_cast<uintptr_t>(p) & 15u) || ld * bytes % 16 || (mats > 1 && stride * bytes % 16)) return false;
     if (mats == 1) stride = ld * rows;
-    if (stride * 2 >= (1ll << 40) || ld * 2 >= (1ll << 40)) return false;
+    if (stride * bytes >= (1ll << 40) || ld * bytes >= (1ll << 40)) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)mats};
-    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u}, es[3] = {1u, 1u, 1u};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
+    const cuuint64_t strides[2] = {(cuuint64_t)(ld * bytes), (cuuint64_t)(stride * bytes)};
+    const cuuint32_t box[3] = {128u / (unsigned)bytes, (cuuint32_t)box_rows, 1u}, es[3] = {1u, 1u, 1u};
+    return encode(m, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -219,7 +219,7 @@ moe_status_t moe_products_status(moe_stream_t stream)
 {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int code = 0;
-    for (auto take : {take_rows_status, take_wgrad_status})
+    for (auto take : {take_rows_status, take_wgrad_status, take_fp8_status})
         if (take(&code, s) != cudaSuccess) return MOE_ERR_CUDA;
     return code ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
