@@ -32,13 +32,25 @@ __device__ __forceinline__ Segment segment_of(const Groups& g, int e)
     return s;
 }
 
-// pre[e] = row tiles of TM rows in the segments before e; pre[E] = all of them. Called by
-// every thread of the block; pre is shared memory of E + 1 ints.
+// The segments in shared memory (a tile's place is looked up by every role of a block, and a
+// look at the index in L2 costs more than a short tile's products).
+struct SegmentTable {
+    int pre[kMaxGroups + 4];           // row tiles before each segment
+    int begin[kMaxGroups], end[kMaxGroups], valid[kMaxGroups];
+    __device__ __forceinline__ Segment at(int e) const { return Segment{begin[e], end[e], valid[e]}; }
+};
+
+// Fills the table: pre[e] = row tiles of TM rows in the segments before e; pre[E] = all of
+// them. Called by every thread of the block.
 template <int TM>
-__device__ __forceinline__ void count_row_tiles(const Groups& g, int* pre)
+__device__ __forceinline__ void read_segments(const Groups& g, SegmentTable* table)
 {
+    int* pre = table->pre;
     for (int e = threadIdx.x; e < g.E; e += blockDim.x) {
         const Segment s = segment_of(g, e);
+        table->begin[e] = s.begin;
+        table->end[e] = s.end;
+        table->valid[e] = s.valid;
         pre[e + 1] = (s.end - s.begin + TM - 1) / TM;
     }
     if (threadIdx.x == 0) pre[0] = 0;

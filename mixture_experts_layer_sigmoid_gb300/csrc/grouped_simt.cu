@@ -126,14 +126,15 @@ grouped_rows_kernel(const GroupedRows p)
 {
     __shared__ __align__(16) float As[2][BK][TM + 4];
     __shared__ __align__(16) float Bs[2][BK][TN + 4];
-    __shared__ int pre[kMaxGroups + 1];
-    count_row_tiles<TM>(p.g, pre);
+    __shared__ SegmentTable table;
+    read_segments<TM>(p.g, &table);
+    const int* pre = table.pre;
     const int num_n = (p.N + TN - 1) / TN;
     const long long total = (long long)pre[p.g.E] * num_n;
     for (long long w = blockIdx.x; w < total; w += gridDim.x) {
         const int q = (int)(w / num_n), n0 = (int)(w % num_n) * TN;
         const int e = segment_at(pre, p.g.E, q);
-        const Segment s = segment_of(p.g, e);
+        const Segment s = table.at(e);
         const int at = (q - pre[e]) * TM, row = s.begin + at, valid = s.valid - at;
         uint64_t acc[TM / 16][TN / 32] = {};
         if (valid > 0) {

@@ -17,7 +17,8 @@
 //     commit and its wait took 536 cycles instead of 293 (512 is the time of the MMAs).
 //   - CTA pairs (cta_group::2, M = 256) halve what a block loads and reads of B: 64 bytes a
 //     cycle of shared memory for operands and 64 for loads, where a single CTA needs 96 and 96.
-//   - The columns of the last tile need no padding: the MMA's N is the tile's own.
+//   - The columns of the last tile need no padding: the MMA's N is the tile's own. The last
+//     unit of a segment in a pair that has at most 128 rows takes M = 128, 64 rows to a CTA.
 //   - A weight gradient's contraction ends inside a 64-row block that also holds rows of
 //     others (perhaps NaN). That block's loads complete on a barrier of their own; a fixing
 //     warp zeroes the rows up to the next multiple of 16 in both operands and then signals
@@ -39,7 +40,7 @@ constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int STRIPE = 64 * 128;               // 64 columns of a 64-deep block, MN-major
 constexpr int kSmemMax = 232448;               // 227 KB
 constexpr int kStaging = 4 * 4096;             // per epilogue warp 32 rows of 128 bytes
-constexpr int kPre = (kMaxGroups + 4) * 4;     // row-tile prefix
+constexpr int kTable = (int)sizeof(SegmentTable);
 constexpr int kBars = 512;
 constexpr int kGroupSpan = 16;                 // as the layer's engine: a weight tile's units run at
                                                // most this many tiles apart
@@ -60,8 +61,8 @@ struct Cfg {
     static constexpr int A_BYTES = BM * BK * 2;
     static constexpr int B_COLS = PAIR ? BN / 2 : BN;
     static constexpr int STAGE = A_BYTES + B_COLS * BK * 2;
-    static constexpr int STAGES = (kSmemMax - 1024 - kStaging - kPre - kBars) / STAGE;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + kStaging + kPre + kBars;
+    static constexpr int STAGES = (kSmemMax - 1024 - kStaging - kTable - kBars) / STAGE;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + kStaging + kTable + kBars;
 };
 
 // Set by a wait that ran out (one word per translation unit and device).
@@ -111,6 +112,7 @@ struct Tile {
     int m0, n0, nt;           // first column (and output row of a weight gradient); the MMA's N
     int kblocks, tail;        // blocks of the contraction; values in the last one
     int end, valid;           // rows: stored rows of this CTA's 128; those that are not padding
+    bool half;                // a pair's unit of 128 rows (M = 128), 64 to a CTA
 };
 
 template <bool WGRAD, bool PAIR, int DEPTH = BK>
@@ -123,8 +125,9 @@ struct Work {
         num_m = WGRAD ? (a.M + (PAIR ? 2 * BM : BM) - 1) / (PAIR ? 2 * BM : BM) : pre[a.g.E];
         total = WGRAD ? (long long)a.g.E * num_m * num_n : (long long)num_m * num_n;
     }
-    __device__ __forceinline__ Tile at(const Args& a, const int* pre, long long w, int rank) const
+    __device__ __forceinline__ Tile at(const Args& a, const SegmentTable& table, long long w, int rank) const
     {
+        const int* pre = table.pre;
         Tile t;
         if constexpr (WGRAD) {
             // the smaller of the two tile counts runs fastest, so that the blocks at work
@@ -135,11 +138,12 @@ struct Work {
             const int mu = num_n < num_m ? r / num_n : r % num_m;
             t.n0 = (num_n < num_m ? r % num_n : r / num_m) * BN;
             t.m0 = (PAIR ? 2 * mu + rank : mu) * BM;
-            const Segment s = segment_of(a.g, t.e);
+            const Segment s = table.at(t.e);
             t.row = s.begin;
             t.kblocks = (s.valid + DEPTH - 1) / DEPTH;
             t.tail = s.valid - (t.kblocks - 1) * DEPTH;
             t.end = t.valid = a.M - t.m0;
+            t.half = false;
         } else {
             // expert by expert; within one, groups of G column tiles walk its row units, so
             // that its rows and weights stay in L2 while they are used
@@ -152,9 +156,10 @@ struct Work {
             const int gsz = min(G, num_n - group * G);
             const int mu = r / gsz;
             t.n0 = (group * G + r % gsz) * BN;
-            const Segment s = segment_of(a.g, t.e);
+            const Segment s = table.at(t.e);
             const int first = mu * (PAIR ? 2 * BM : BM);       // row of the unit in its segment
-            const int mine = first + (PAIR ? rank * BM : 0);
+            t.half = PAIR && s.end - s.begin - first <= BM;
+            const int mine = first + (PAIR ? rank * (t.half ? BM / 2 : BM) : 0);
             t.row = s.begin + mine;
             t.m0 = 0;
             t.kblocks = first < s.valid ? (a.K + DEPTH - 1) / DEPTH : 0;
@@ -224,7 +229,8 @@ __device__ __forceinline__ void load_box(uint32_t dst, const __nv_bfloat16* p, l
 
 template <bool WGRAD, bool B_MN, bool PAIR, bool GUARD>
 __global__ void __launch_bounds__(threads<WGRAD, GUARD>(), 1)
-kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const Args a)
+kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
+       const __grid_constant__ CUtensorMap mH, const Args a)
 {
     using C = Cfg<PAIR>;
     DeviceStatus* const status = &wait_status;
@@ -234,8 +240,8 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t ring = ptx::smem_u32(smem);
     const uint32_t staging = ring + S * C::STAGE;
-    int* pre = reinterpret_cast<int*>(smem + S * C::STAGE + kStaging);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE + kStaging + kPre);
+    SegmentTable& table = *reinterpret_cast<SegmentTable*>(smem + S * C::STAGE + kStaging);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE + kStaging + kTable);
     static_assert((3 * S + 5) * 8 + 8 + 16 <= kBars && C::SMEM % 16 == 0, "barriers");
     const uint32_t bar0 = (ptx::smem_u32(bars) + 7u) & ~7u;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -281,15 +287,16 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             ptx::tmem_relinquish();
         }
     }
-    if (!WGRAD) count_row_tiles<PAIR ? 2 * BM : BM>(a.g, pre);
+    read_segments<PAIR ? 2 * BM : BM>(a.g, &table);
     ptx::tc_fence_before();
     if (PAIR) ptx::cluster_sync();             // the peer's barriers exist before any remote signal
     else __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
     Work<WGRAD, PAIR> work;
-    work.init(a, pre);
+    work.init(a, table.pre);
+    work.total = __shfl_sync(0xffffffffu, work.total, 0);
     auto wait = [&](uint32_t bar, uint32_t parity, int where) {
         return ptx::wait_bounded(bar, parity, &abort_flag, status, where);
     };
@@ -301,10 +308,10 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             uint32_t ph = 0;
             bool ok = true;
             for (long long w = unit0; ok && w < work.total; w += nunits) {
-                const Tile t = work.at(a, pre, w, rank);
+                const Tile t = work.at(a, table, w, rank);
                 const int bcols = PAIR ? t.nt / 2 : t.nt, b0 = t.n0 + (PAIR ? rank * bcols : 0);
                 const int stripes = (bcols + 63) / 64;
-                const uint32_t bytes = C::A_BYTES + (B_MN ? stripes * STRIPE : C::B_COLS * BK * 2);
+                const uint32_t bytes = (t.half ? C::A_BYTES / 2 : C::A_BYTES) + (B_MN ? stripes * STRIPE : C::B_COLS * BK * 2);
                 for (int kb = 0; kb < t.kblocks; ++kb) {
                     if (!wait(empty_bar(s), ph ^ 1u, 1)) { ok = false; break; }
                     const uint32_t dst_a = ring + s * C::STAGE, dst_b = dst_a + C::A_BYTES;
@@ -326,7 +333,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                         for (int i = 0; i < BM / 64; ++i) load_3d<PAIR>(dst_a + i * STRIPE, &mA, bar, t.m0 + 64 * i, y, 0);
                         for (int i = 0; i < stripes; ++i) load_3d<PAIR>(dst_b + i * STRIPE, &mB, bar, b0 + 64 * i, y, 0);
                     } else {
-                        load_3d<PAIR>(dst_a, &mA, bar, kb * BK, t.row, 0);
+                        load_3d<PAIR>(dst_a, t.half ? &mH : &mA, bar, kb * BK, t.row, 0);
                         if constexpr (B_MN) {
                             for (int i = 0; i < stripes; ++i)
                                 load_3d<PAIR>(dst_b + i * STRIPE, &mB, bar, b0 + 64 * i, kb * BK, t.e);
@@ -346,13 +353,14 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             uint32_t ph = 0, aph = 0;
             bool ok = true;
             for (long long w = unit0; ok && w < work.total; w += nunits) {
-                const Tile t = work.at(a, pre, w, rank);
-                if (!wait(acce_bar(acc), aph ^ 1u, 2)) break;
+                const Tile t = work.at(a, table, w, rank);
+                if (!spin(acce_bar(acc), aph ^ 1u)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * BN);
-                const uint32_t id = IDESC | ((uint32_t)(t.nt >> 3) << 17);
+                // (256 rows less 128 in the M / 16 field)
+                const uint32_t id = (IDESC | ((uint32_t)(t.nt >> 3) << 17)) - (t.half ? 8u << 24 : 0u);
                 for (int kb = 0; kb < t.kblocks; ++kb) {
-                    if (!wait(full_bar(s), ph, 3)) { ok = false; break; }
+                    if (!spin(full_bar(s), ph)) { ok = false; break; }
                     ptx::tc_fence_after();
                     const uint32_t pa = ring + s * C::STAGE, pb = pa + C::A_BYTES;
                     const int steps = WGRAD && kb == t.kblocks - 1 ? (t.tail + 15) / 16 : BK / 16;
@@ -379,6 +387,10 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             }
             if (PAIR) ptx::tc_commit_pair(final_bar, 3);
             else ptx::tc_commit(final_bar);
+            if (!ok) {
+                abort_flag = 1;
+                report_timeout(status, 2);
+            }
         }
         __syncwarp();
         // every MMA has completed before tensor memory is freed (the odd CTA's is written
@@ -395,16 +407,21 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         int acc = 0;
         uint32_t aph = 0;
         for (long long w = unit0; w < work.total; w += nunits) {
-            const Tile t = work.at(a, pre, w, rank);
+            Tile t = work.at(a, table, w, rank);
+            t.kblocks = __shfl_sync(0xffffffffu, t.kblocks, 0);
             if (!__all_sync(0xffffffffu, wait(accf_bar(acc), aph, 5))) break;
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-            const int rows = t.end - q * 32;    // of this warp's 32 rows those that are stored
-            const bool mine = lane + q * 32 < t.valid;
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + t.n0 +
-                               (WGRAD ? t.e * a.so + (long long)(t.m0 + q * 32) * a.ldo
-                                      : (long long)(t.row + q * 32) * a.ldo);
-            const int cols = min(a.N - t.n0, BN);
+            // this warp's rows and columns of the tile: with M = 256 (or 128 in one CTA) a lane is a
+            // row; with M = 128 in a pair, lanes 64-127 hold the second half of the columns
+            // of the rows in lanes 0-63
+            const int r0 = (t.half ? q & 1 : q) * 32, c0 = t.half ? (q >> 1) * (t.nt / 2) : 0;
+            const int rows = t.end - r0;        // of this warp's 32 rows those that are stored
+            const bool mine = lane + r0 < t.valid;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + t.n0 + c0 +
+                               (WGRAD ? t.e * a.so + (long long)(t.m0 + r0) * a.ldo
+                                      : (long long)(t.row + r0) * a.ldo);
+            const int cols = min(a.N - t.n0 - c0, t.half ? t.nt / 2 : t.nt);
 #pragma unroll 1
             for (int u = 0; u * 64 < cols && rows > 0; ++u) {
                 uint32_t v0[32], v1[32];
@@ -485,7 +502,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         uint32_t ph = 0;
         bool ok = true;
         for (long long w = unit0; ok && w < work.total; w += nunits) {
-            const Tile t = work.at(a, pre, w, rank);
+            const Tile t = work.at(a, table, w, rank);
             const int n_cols = a.N - t.n0;
             for (int kb = 0; kb < t.kblocks; ++kb) {
                 if (!__all_sync(0xffffffffu, wait(empty_bar(s), ph ^ 1u, 6))) { ok = false; break; }
@@ -518,7 +535,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         int s0 = 0;
         uint32_t phases = 0;
         for (long long w = unit0; w < work.total; w += nunits) {
-            const Tile t = work.at(a, pre, w, rank);
+            const Tile t = work.at(a, table, w, rank);
             if (t.kblocks == 0) continue;
             const int s = (s0 + t.kblocks - 1) % S;
             s0 = (s0 + t.kblocks) % S;
@@ -606,7 +623,7 @@ inline cudaError_t take_status(int* code, cudaStream_t s)
 }
 
 template <bool WGRAD, bool B_MN, bool PAIR, bool GUARD>
-cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const Args& a, long long units, int num_sms, cudaStream_t s)
+cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mH, const Args& a, long long units, int num_sms, cudaStream_t s)
 {
     using C = Cfg<PAIR>;
     auto k = kernel<WGRAD, B_MN, PAIR, GUARD>;
@@ -628,7 +645,7 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const Args& a, 
     if (e != cudaSuccess) return e;
     const long long grid = units < n ? (units > 0 ? units : 1) : n;
     cfg.gridDim = dim3((unsigned)(PAIR ? 2 * grid : grid));
-    return cudaLaunchKernelEx(&cfg, k, mA, mB, a);
+    return cudaLaunchKernelEx(&cfg, k, mA, mB, mH, a);
 }
 
 }  // namespace gtc

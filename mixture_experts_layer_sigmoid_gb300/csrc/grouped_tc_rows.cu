@@ -34,8 +34,9 @@ using namespace gtc;
 
 namespace {
 
-// Rows an expert has on average from which tiles go to CTA pairs.
-constexpr long long kPairRows = 512;
+// Rows an expert has on average from which tiles go to CTA pairs (64 experts of 256 rows,
+// 7168 x 2048, the gradient of the rows: 451 us as single CTAs, 414 as pairs).
+constexpr long long kPairRows = 128;
 
 template <bool B_MN>
 cudaError_t rows_tc(const GroupedRows& p, int num_sms, cudaStream_t s)
@@ -48,15 +49,15 @@ cudaError_t rows_tc(const GroupedRows& p, int num_sms, cudaStream_t s)
     const bool pair = p.g.rows / p.g.E >= kPairRows;
     const long long num_n = (p.N + BN - 1) / BN;
     const long long units = row_tiles_bound(p.g.rows, p.g.E, pair ? 2 * BM : BM) * num_n;
-    CUtensorMap mA, mB;
+    CUtensorMap mA, mB, mH;
     const int bcols = pair ? BN / 2 : BN;
-    if (make_map(&mA, p.X, p.K, p.g.rows, 1, p.ldx, 0, BM) &&
+    if (make_map(&mA, p.X, p.K, p.g.rows, 1, p.ldx, 0, BM) && make_map(&mH, p.X, p.K, p.g.rows, 1, p.ldx, 0, BM / 2) &&
         (B_MN ? make_map(&mB, p.W, p.N, p.K, p.g.E, p.ldw, p.sw, BK) : make_map(&mB, p.W, p.K, p.N, p.g.E, p.ldw, p.sw, bcols)))
-        return pair ? launch<false, B_MN, true, false>(mA, mB, a, units, num_sms, s)
-                    : launch<false, B_MN, false, false>(mA, mB, a, units, num_sms, s);
+        return pair ? launch<false, B_MN, true, false>(mA, mB, mH, a, units, num_sms, s)
+                    : launch<false, B_MN, false, false>(mA, mB, mH, a, units, num_sms, s);
     a.A = static_cast<const __nv_bfloat16*>(p.X); a.lda = p.ldx;
     a.B = static_cast<const __nv_bfloat16*>(p.W); a.ldb = p.ldw; a.sb = p.sw;
-    return launch<false, B_MN, false, true>(CUtensorMap{}, CUtensorMap{}, a,
+    return launch<false, B_MN, false, true>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, a,
                                             row_tiles_bound(p.g.rows, p.g.E, BM) * num_n, num_sms, s);
 }
 

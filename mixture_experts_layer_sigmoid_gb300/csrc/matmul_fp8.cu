@@ -38,8 +38,8 @@ struct Args8 {
 };
 
 constexpr int A8 = BM * QK, STAGE8 = A8 + BN * QK;
-constexpr int S8 = (kSmemMax - 1024 - kSlots * kSlot - kPre - kBars) / STAGE8;
-constexpr int SMEM8 = 1024 + S8 * STAGE8 + kSlots * kSlot + kPre + kBars;
+constexpr int S8 = (kSmemMax - 1024 - kSlots * kSlot - kTable - kBars) / STAGE8;
+constexpr int SMEM8 = 1024 + S8 * STAGE8 + kSlots * kSlot + kTable + kBars;
 static_assert(S8 + 2 <= kSlots && kSlot % 16 == 0, "a slot's last readers are done when its next group's first stage is free");
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more)
@@ -83,8 +83,8 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t ring = ptx::smem_u32(smem);
     const uint32_t slots = ring + S * STAGE8;
-    int* pre = reinterpret_cast<int*>(smem + S * STAGE8 + kSlots * kSlot);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * STAGE8 + kSlots * kSlot + kPre);
+    SegmentTable& table = *reinterpret_cast<SegmentTable*>(smem + S * STAGE8 + kSlots * kSlot);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * STAGE8 + kSlots * kSlot + kTable);
     static_assert((2 * S + 5 + kSlots) * 8 + 8 + 16 <= kBars && SMEM8 % 16 == 0, "barriers");
     const uint32_t bar0 = (ptx::smem_u32(bars) + 7u) & ~7u;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -119,14 +119,14 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
         ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), 512);
         ptx::tmem_relinquish();
     }
-    count_row_tiles<BM>(a.g, pre);
+    read_segments<BM>(a.g, &table);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
     Work<false, false, QK> work;
-    work.init(a, pre);
+    work.init(a, table.pre);
     work.total = __shfl_sync(0xffffffffu, work.total, 0);
     auto wait = [&](uint32_t bar, uint32_t parity, int where) {
         return ptx::wait_bounded(bar, parity, &abort_flag, status, where);
@@ -142,7 +142,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
                 uint32_t ph = 0;
                 bool ok = true;
                 for (long long w = blockIdx.x; ok && w < work.total; w += gridDim.x) {
-                    const Tile t = work.at(a, pre, w, 0);
+                    const Tile t = work.at(a, table, w, 0);
                     const int stripes = (t.nt + 127) / 128;        // MN-major: 128 columns each
                     const uint32_t bytes = A8 + (B_MN ? stripes * 128 : BN) * QK;
                     for (int kb = 0; kb < t.kblocks; ++kb) {
@@ -168,7 +168,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
                 uint32_t ph = 0, used = 0;
                 bool ok = true;
                 for (long long w = blockIdx.x; ok && w < work.total; w += gridDim.x) {
-                    const Tile t = work.at(a, pre, w, 0);
+                    const Tile t = work.at(a, table, w, 0);
                     const uint32_t id = IDESC | ((uint32_t)(t.nt >> 3) << 17);
                     for (int kb = 0; kb < t.kblocks; ++kb, ++used) {
                         const int b = (int)(used & 1u);
@@ -211,7 +211,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
             uint32_t ph = 0;
             bool ok = true;
             for (long long w = blockIdx.x; ok && w < work.total; w += gridDim.x) {
-                const Tile t = work.at(a, pre, w, 0);
+                const Tile t = work.at(a, table, w, 0);
                 // four of the tile's 128 rows to a lane; the first two lanes also have the
                 // scales of its one or two column blocks
                 const float* src = p.SA + (long long)t.row * p.ldsa;
@@ -255,7 +255,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
         uint32_t it = 0, slot = 0, sph = 0;                    // blocks; groups of scales
         bool ok = true;
         for (long long w = blockIdx.x; ok && w < work.total; w += gridDim.x) {
-            Tile t = work.at(a, pre, w, 0);
+            Tile t = work.at(a, table, w, 0);
             t.kblocks = __shfl_sync(0xffffffffu, t.kblocks, 0);
             uint64_t acc[64];
 #pragma unroll
