@@ -400,7 +400,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             ptx::wait_bounded(final_bar, 0, &never, status, 4);
         }
         __syncwarp();
-    } else if (warp < 6) {
+    } else if (warp >= 2 && warp < 6) {
         // ----------------------------------------------------------- outputs
         const int q = warp & 3;                 // this warp's quarter of the TMEM lanes
         const uint32_t stg = staging + (uint32_t)q * 4096u;
@@ -416,12 +416,17 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             // row; with M = 128 in a pair, lanes 64-127 hold the second half of the columns
             // of the rows in lanes 0-63
             const int r0 = (t.half ? q & 1 : q) * 32, c0 = t.half ? (q >> 1) * (t.nt / 2) : 0;
-            const int rows = t.end - r0;        // of this warp's 32 rows those that are stored
+            const int rows = __shfl_sync(0xffffffffu, t.end - r0, 0);   // of this warp's 32 rows those stored
             const bool mine = lane + r0 < t.valid;
             __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + t.n0 + c0 +
                                (WGRAD ? t.e * a.so + (long long)(t.m0 + r0) * a.ldo
                                       : (long long)(t.row + r0) * a.ldo);
-            const int cols = min(a.N - t.n0 - c0, t.half ? t.nt / 2 : t.nt);
+            const int cols = __shfl_sync(0xffffffffu, min(a.N - t.n0 - c0, t.half ? t.nt / 2 : t.nt), 0);
+            // eight lanes to a row of 128 bytes, four rows an instruction
+            const int ch = lane & 7;
+            __nv_bfloat16* p0 = o + (lane >> 3) * a.ldo + ch * 8;
+            const long long step = 4 * a.ldo;
+            const uint32_t s0 = stg + (lane >> 3) * 128, x0 = (uint32_t)((ch ^ (lane >> 3)) << 4);
 #pragma unroll 1
             for (int u = 0; u * 64 < cols && rows > 0; ++u) {
                 uint32_t v0[32], v1[32];
@@ -448,28 +453,15 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                 }
                 __syncwarp();
                 const int left = cols - u * 64;
-                if (a.vec) {
-                    // eight lanes to a row of 128 bytes, four rows an instruction
-                    const int ch = lane & 7;
+                if (a.vec && rows >= 32 && left >= 64) {
+                    uint4 x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3);
-                        const uint32_t at = stg + r * 128 + ((ch ^ (r & 7)) << 4);
-                        if (r < rows) {
-                            __nv_bfloat16* dst = o + r * a.ldo + u * 64 + ch * 8;
-                            if (ch * 8 + 8 <= left) {
-                                uint4 x;
-                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
-                                *reinterpret_cast<uint4*>(dst) = x;
-                            } else {
-                                for (int c = 0; ch * 8 + c < left; ++c) {
-                                    unsigned short x;
-                                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + 2 * c));
-                                    reinterpret_cast<unsigned short*>(dst)[c] = x;
-                                }
-                            }
-                        }
-                    }
+                    for (int i = 0; i < 8; ++i)     // row 4 i + lane / 8: its swizzle is that of 4 (i % 2) + lane / 8
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                                     : "r"(s0 + i * 512 + (i & 1 ? x0 ^ 64u : x0)) : "memory");
+                    __nv_bfloat16* dst = p0 + u * 64;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i, dst += step) *reinterpret_cast<uint4*>(dst) = x[i];
                 } else {
                     for (int r = 0; r < min(rows, 32); ++r) {
 #pragma unroll
@@ -477,7 +469,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                             const int c = lane + 32 * h;
                             if (c < left) {
                                 unsigned short x;
-                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(stg + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2));
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(stg + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2) : "memory");
                                 reinterpret_cast<unsigned short*>(o + r * a.ldo + u * 64)[c] = x;
                             }
                         }
@@ -495,7 +487,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
-    } else if (GUARD) {
+    } else if (GUARD && warp >= 6) {
         // ------------------------------------------- loads off the boundaries
         const int tid = (int)threadIdx.x - 192;
         int s = 0;
@@ -530,7 +522,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                 if (++s == S) { s = 0; ph ^= 1u; }
             }
         }
-    } else if (WGRAD) {
+    } else if (WGRAD && !GUARD) {
         // ------------------------------- the contraction's last, partial block
         int s0 = 0;
         uint32_t phases = 0;
