@@ -24,7 +24,7 @@
 //     warp zeroes the rows up to the next multiple of 16 in both operands and then signals
 //     the block; the MMAs stop at that multiple.
 //   - GUARD: operands that TMA cannot take (strides off the 16-byte boundaries) are loaded by
-//     four warps, as pairs of aligned 16-byte windows that are shifted, into the same layout.
+//     ten warps, as pairs of aligned 16-byte windows that are shifted, into the same layout.
 #pragma once
 #include "grouped.cuh"
 #include "ptx.cuh"
@@ -68,8 +68,10 @@ struct Cfg {
 // Set by a wait that ran out (one word per translation unit and device).
 static __device__ DeviceStatus wait_status;
 
+constexpr int kLoaders = 320;                  // GUARD: loading threads
+
 template <bool WGRAD, bool GUARD>
-constexpr int threads() { return GUARD ? 320 : (WGRAD ? 224 : 192); }
+constexpr int threads() { return GUARD ? 192 + kLoaders : (WGRAD ? 224 : 192); }
 
 __device__ __forceinline__ bool elect_one()
 {
@@ -174,25 +176,22 @@ struct Work {
     }
 };
 
-// Eight bf16 values from any 2-byte aligned address; of them `n` exist (n <= 0: zeros).
-__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int n)
+// Eight bf16 values from any 2-byte aligned address, of which `n` exist, in two steps: the
+// aligned 16-byte windows that hold them, and the shift.
+struct Windows { uint4 a, b; };
+__device__ __forceinline__ Windows load_windows(const __nv_bfloat16* p, int n)
 {
-    if (n <= 0) return make_uint4(0, 0, 0, 0);
-    if (n < 8) {
-        uint32_t w[4] = {0, 0, 0, 0};
-        const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < n) w[i / 2] |= (uint32_t)u[i] << (16 * (i & 1));
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const unsigned off = (unsigned)(at & 15u);
-    const uint4* base = reinterpret_cast<const uint4*>(at - off);
-    const uint4 a = base[0];
-    if (off == 0) return a;
-    const uint4 b = base[1];                   // holds the last of the eight values
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    Windows w{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
+    const uint4* base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+    if (n > 0) w.a = base[0];                           // holds the first value
+    if (n > 0 && off + 2 * min(n, 8) > 16) w.b = base[1];   // holds the last one
+    return w;
+}
+__device__ __forceinline__ uint4 shift_windows(const Windows& q, const __nv_bfloat16* p, int n)
+{
+    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
+    uint32_t w[8] = {q.a.x, q.a.y, q.a.z, q.a.w, q.b.x, q.b.y, q.b.z, q.b.w};
     if (off & 8u) {
 #pragma unroll
         for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
@@ -202,29 +201,13 @@ __device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int n)
         for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
     }
     const unsigned sh = (off & 2u) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
-                      __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
-}
-// A box of `rows` rows of 64 values into shared memory, 128 bytes a row, swizzled;
-// n_rows and n_cols of them exist.
-__device__ __forceinline__ void load_box(uint32_t dst, const __nv_bfloat16* p, long long ld, int rows, int n_rows,
-                                         int n_cols, int tid)
-{
-    for (int c0 = tid; c0 < rows * 8; c0 += 4 * 128) {
-        uint4 v[4];
+    uint32_t r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + i * 128, r = c >> 3, ch = c & 7;
-            v[i] = load8(p + r * ld + ch * 8, c < rows * 8 && r < n_rows ? n_cols - ch * 8 : 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + i * 128, r = c >> 3, ch = c & 7;
-            if (c < rows * 8)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 + ((ch ^ (r & 7)) << 4)),
-                             "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w) : "memory");
-        }
+    for (int i = 0; i < 4; ++i) {
+        r[i] = __funnelshift_r(w[i], w[i + 1], sh);
+        if (2 * i + 2 > n) r[i] = 2 * i + 1 > n ? 0u : r[i] & 0xFFFFu;
     }
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <bool WGRAD, bool B_MN, bool PAIR, bool GUARD>
@@ -262,7 +245,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         for (int s = 0; s < S; ++s) {
             // a weight gradient's block is signalled once by each CTA (its producer or, for
             // the last block, its fixing warp); other blocks by the even CTA's producer
-            ptx::mbar_init(full_bar(s), GUARD ? 128 : (WGRAD && PAIR ? 2 : 1));
+            ptx::mbar_init(full_bar(s), GUARD ? kLoaders : (WGRAD && PAIR ? 2 : 1));
             ptx::mbar_init(empty_bar(s), 1);
             ptx::mbar_init(land_bar(s), 1);
         }
@@ -489,7 +472,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         }
     } else if (GUARD && warp >= 6) {
         // ------------------------------------------- loads off the boundaries
-        const int tid = (int)threadIdx.x - 192;
+        const int tid = (int)threadIdx.x - 192, ch = tid & 7;
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -498,23 +481,54 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             const int n_cols = a.N - t.n0;
             for (int kb = 0; kb < t.kblocks; ++kb) {
                 if (!__all_sync(0xffffffffu, wait(empty_bar(s), ph ^ 1u, 6))) { ok = false; break; }
-                const uint32_t dst_a = ring + s * C::STAGE, dst_b = dst_a + C::A_BYTES;
-                if constexpr (WGRAD) {
-                    const int n_k = kb == t.kblocks - 1 ? t.tail : BK;
-                    const long long r = t.row + kb * BK;
-                    for (int i = 0; i < BM / 64; ++i)
-                        load_box(dst_a + i * STRIPE, a.A + r * a.lda + t.m0 + 64 * i, a.lda, BK, n_k, a.M - t.m0 - 64 * i, tid);
-                    for (int i = 0; i * 64 < t.nt; ++i)
-                        load_box(dst_b + i * STRIPE, a.B + r * a.ldb + t.n0 + 64 * i, a.ldb, BK, n_k, n_cols - 64 * i, tid);
-                } else {
-                    const int k = kb * BK;
-                    load_box(dst_a, a.A + t.row * a.lda + k, a.lda, BM, t.valid, a.K - k, tid);
-                    const __nv_bfloat16* b = a.B + t.e * a.sb;
-                    if constexpr (B_MN) {
-                        for (int i = 0; i * 64 < t.nt; ++i)
-                            load_box(dst_b + i * STRIPE, b + k * a.ldb + t.n0 + 64 * i, a.ldb, BK, a.K - k, n_cols - 64 * i, tid);
+                const uint32_t dst = ring + s * C::STAGE;
+                // The stage as rows of 128 bytes: 128 of A (rows, or two stripes of 64), then B's
+                // (columns, or stripes of 64); eight threads to a row, five rows of a thread in
+                // flight.
+                const int k = kb * BK, total = BM + (B_MN ? (t.nt + 63) / 64 * 64 : t.nt);
+                const int n_k = WGRAD ? (kb == t.kblocks - 1 ? t.tail : BK) : a.K - k;
+                auto source = [&](int v, int& n) -> const __nv_bfloat16* {
+                    const bool is_a = v < BM;
+                    const int i = is_a ? v : v - BM;
+                    if constexpr (WGRAD) {
+                        const int col = (i & ~63) + ch * 8, r = i & 63;
+                        n = r < n_k ? (is_a ? a.M - t.m0 : n_cols) - col : 0;
+                        return is_a ? a.A + (long long)(t.row + k + r) * a.lda + t.m0 + col
+                                    : a.B + (long long)(t.row + k + r) * a.ldb + t.n0 + col;
                     } else {
-                        load_box(dst_b, b + t.n0 * a.ldb + k, a.ldb, t.nt, n_cols, a.K - k, tid);
+                        const __nv_bfloat16* w = a.B + t.e * a.sb;
+                        if (is_a) {
+                            n = i < t.valid ? n_k - ch * 8 : 0;
+                            return a.A + (long long)(t.row + i) * a.lda + k + ch * 8;
+                        }
+                        if constexpr (B_MN) {
+                            const int col = (i & ~63) + ch * 8, r = i & 63;
+                            n = r < n_k ? n_cols - col : 0;
+                            return w + (long long)(k + r) * a.ldb + t.n0 + col;
+                        } else {
+                            n = i < n_cols ? n_k - ch * 8 : 0;
+                            return w + (long long)(t.n0 + i) * a.ldb + k + ch * 8;
+                        }
+                    }
+                };
+                for (int v0 = tid >> 3; v0 < total; v0 += 5 * (kLoaders / 8)) {
+                    Windows q[5];
+#pragma unroll
+                    for (int j = 0; j < 5; ++j) {
+                        const int v = v0 + j * (kLoaders / 8);
+                        int n = 0;
+                        const __nv_bfloat16* p = source(v, n);
+                        q[j] = load_windows(p, v < total ? n : 0);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 5; ++j) {
+                        const int v = v0 + j * (kLoaders / 8);
+                        int n = 0;
+                        const __nv_bfloat16* p = source(v, n);
+                        const uint4 x = shift_windows(q[j], p, n);
+                        if (v < total)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + v * 128 + ((ch ^ (v & 7)) << 4)),
+                                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
                     }
                 }
                 ptx::fence_proxy_async_smem();

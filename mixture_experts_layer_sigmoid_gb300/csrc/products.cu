@@ -1,9 +1,10 @@
 // products.cu -- C ABI of the products over rows sorted by expert (moe.h): the
 // checks of their arguments, and the codes of activation rows.
 //
-// Row codes: one thread holds eight consecutive values, sixteen neighbours share a
-// block of 128 and its largest magnitude. The kernel moves 16 or 32 bytes in and 8 out
-// per thread and is bound by HBM; kPieces loads per thread are in flight.
+// Row codes: a thread holds sixteen consecutive values (32 or 64 bytes in, 16 out), eight
+// neighbours share a block of 128 and its largest magnitude. Bound by HBM, with the
+// instructions close behind: with eight values a thread, the block's division and shuffles
+// came twice as often (139264 rows of 4096 bf16 349 us).
 #include "grouped_tc.cuh"
 #include "mx.cuh"
 #include "rowvec.cuh"
@@ -11,62 +12,82 @@
 namespace moe {
 namespace {
 
-constexpr int kQThreads = 256, kPieces = 4;
+constexpr int kQThreads = 256, kPieces = 2, kPer = 16;
 // Scales from which the corrected product's codes are those of a division (norm.cu has
 // the reason, and the test that walks the pairs).
 constexpr float kRowQuotientMin = 0x1p-92f;
 
+// n / d for n below 2^31, as a product: floor(n m / 2^(32 + s)), m = ceil(2^(32 + s) / d),
+// 2^s >= d / 2 (T. Granlund and P. L. Montgomery, "Division by invariant integers using
+// multiplication", PLDI 1994).
+struct Divider {
+    unsigned m, s, d;
+    explicit Divider(unsigned d_) : s(0), d(d_)
+    {
+        while ((1ull << (s + 1)) < d) ++s;
+        m = (unsigned)(((1ull << (32 + s)) + d - 1) / d);
+    }
+    __device__ __forceinline__ unsigned operator()(unsigned n) const { return d == 1 ? n : __umulhi(n, m) >> s; }
+};
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&v)[kPer])
+{
+    constexpr int V = kPiece<T>;
+#pragma unroll
+    for (int i = 0; i < kPer / V; ++i) {
+        float u[V];
+        load_vec<T, V>(p + i * V, u);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i * V + j] = u[j];
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
 quantize_rows_kernel(const T* __restrict__ x, long long ldx, uint8_t* codes, long long ldc, float* scales, long long lds,
-                     unsigned rows, unsigned per_row, long long row0, const int* in_use)
+                     unsigned rows, Divider per_row, long long row0, const int* in_use)
 {
     if (in_use) {
         const long long n = (long long)*in_use - row0;
         rows = n < 0 ? 0u : (unsigned)(n < (long long)rows ? n : (long long)rows);
     }
-    const unsigned total = rows * per_row;                 // below 2^31: the host cuts the rows
+    const unsigned total = rows * per_row.d;               // below 2^31: the host cuts the rows
     for (unsigned base = blockIdx.x * (kQThreads * kPieces) + threadIdx.x; base - threadIdx.x < total;
          base += gridDim.x * (kQThreads * kPieces)) {
-        float v[kPieces][8];
+        float v[kPieces][kPer];
         unsigned r[kPieces], c[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const unsigned at = base + i * kQThreads;
-            r[i] = at / per_row;
-            c[i] = (at - r[i] * per_row) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+            r[i] = per_row(at);
+            c[i] = (at - r[i] * per_row.d) * kPer;
             if (at < total) {
-                const T* p = x + (long long)r[i] * ldx + c[i];
-                if constexpr (sizeof(T) == 2) {
-                    load_vec<T, 8>(p, v[i]);
-                } else {
-                    float lo[4], hi[4];
-                    load_vec<T, 4>(p, lo);
-                    load_vec<T, 4>(p + 4, hi);
+                load16(x + (long long)r[i] * ldx + c[i], v[i]);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) { v[i][j] = lo[j]; v[i][4 + j] = hi[j]; }
-                }
+                for (int j = 0; j < kPer; ++j) v[i][j] = 0.f;
             }
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             float a = max_abs(v[i]);
 #pragma unroll
-            for (int off = 8; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-            if (base + i * kQThreads >= total) continue;   // the sixteen lanes of a block alike
+            for (int off = 4; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+            if (base + i * kQThreads >= total) continue;   // the eight lanes of a block alike
             const float t = __fdiv_rn(a, 448.f);
             const float s = t == 0.f ? 1.f : t;
             if (s >= kRowQuotientMin && s < 0x1p100f) {
                 divide_vec(v[i], s, __frcp_rn(s));
             } else {                                       // the remainder could underflow
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = __fdiv_rn(v[i][j], s);
+                for (int j = 0; j < kPer; ++j) v[i][j] = __fdiv_rn(v[i][j], s);
             }
             if (c[i] % 128 == 0) scales[(long long)r[i] * lds + c[i] / 128] = s;
-            *reinterpret_cast<uint2*>(codes + (long long)r[i] * ldc + c[i]) =
-                make_uint2(e4m3x4(v[i][0], v[i][1], v[i][2], v[i][3]), e4m3x4(v[i][4], v[i][5], v[i][6], v[i][7]));
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = e4m3x4(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3]);
+            *reinterpret_cast<uint4*>(codes + (long long)r[i] * ldc + c[i]) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
@@ -75,12 +96,12 @@ template <typename T>
 cudaError_t quantize_rows(long long rows, int K, const void* x, long long ldx, uint8_t* codes, long long ldc,
                           float* scales, long long lds, const int* in_use, int num_sms, cudaStream_t s)
 {
-    const unsigned per_row = (unsigned)K / 8;
-    const long long slab = (1ll << 30) / per_row;          // rows whose pieces 32 bits count
+    const Divider per_row((unsigned)K / kPer);
+    const long long slab = (1ll << 30) / per_row.d;        // rows whose pieces 32 bits count
     for (long long r = 0; r < rows; r += slab) {
         const long long n = rows - r < slab ? rows - r : slab;
-        const long long blocks = (n * per_row + kQThreads * kPieces - 1) / (kQThreads * kPieces);
-        const unsigned grid = (unsigned)(blocks < num_sms * 8ll ? blocks : num_sms * 8ll);
+        const long long blocks = (n * per_row.d + kQThreads * kPieces - 1) / (kQThreads * kPieces);
+        const unsigned grid = (unsigned)(blocks < num_sms * 16ll ? blocks : num_sms * 16ll);
         quantize_rows_kernel<T><<<grid, kQThreads, 0, s>>>(static_cast<const T*>(x) + r * ldx, ldx, codes + r * ldc, ldc,
                                                            scales + r * lds, lds, (unsigned)n, per_row, r, in_use);
         count_launches();
