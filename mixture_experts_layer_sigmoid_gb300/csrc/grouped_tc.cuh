@@ -23,6 +23,9 @@
 //     others (perhaps NaN). That block's loads complete on a barrier of their own; a fixing
 //     warp zeroes the rows up to the next multiple of 16 in both operands and then signals
 //     the block; the MMAs stop at that multiple.
+//   - FEW: tiles of 32 rows by 64 columns for experts of few rows, whose weights are all there is
+//     to read: 16 stages of 8 KB of them in flight, and enough tiles for every SM. (The MMAs
+//     still take 128 rows, 250 cycles a block, less than HBM takes to bring it.)
 //   - GUARD: operands that TMA cannot take (strides off the 16-byte boundaries) are loaded by
 //     ten warps, as pairs of aligned 16-byte windows that are shifted, into the same layout.
 #pragma once
@@ -56,13 +59,22 @@ struct Args {
     long long lda, ldb, sb;
 };
 
-template <bool PAIR>
+// Single CTAs, pairs, or single CTAs on tiles of few rows.
+enum Mode { SINGLE, PAIRS, FEW };
+constexpr int FM = 32, FN = 64;                // a FEW tile
+
+template <Mode MODE>
 struct Cfg {
-    static constexpr int A_BYTES = BM * BK * 2;
-    static constexpr int B_COLS = PAIR ? BN / 2 : BN;
+    static constexpr bool PAIR = MODE == PAIRS;
+    static constexpr int ROWS = MODE == FEW ? FM : (PAIR ? 2 * BM : BM);        // of a unit
+    static constexpr int COLS = MODE == FEW ? FN : BN;
+    static constexpr int A_BYTES = (MODE == FEW ? FM : BM) * BK * 2;
+    static constexpr int B_COLS = PAIR ? BN / 2 : COLS;
     static constexpr int STAGE = A_BYTES + B_COLS * BK * 2;
     static constexpr int STAGES = (kSmemMax - 1024 - kStaging - kTable - kBars) / STAGE;
     static constexpr int SMEM = 1024 + STAGES * STAGE + kStaging + kTable + kBars;
+    // the MMAs of a FEW tile read 128 rows of A: what lies behind its 32, whose products are not stored
+    static_assert(BM * BK * 2 - STAGE <= kStaging, "inside the block's shared memory");
 };
 
 // Set by a wait that ran out (one word per translation unit and device).
@@ -117,13 +129,15 @@ struct Tile {
     bool half;                // a pair's unit of 128 rows (M = 128), 64 to a CTA
 };
 
-template <bool WGRAD, bool PAIR, int DEPTH = BK>
+template <bool WGRAD, Mode MODE, int DEPTH = BK>
 struct Work {
+    static constexpr bool PAIR = MODE == PAIRS;
+    static constexpr int TN = Cfg<MODE>::COLS;
     int num_n, num_m;
     long long total;
     __device__ __forceinline__ void init(const Args& a, const int* pre)
     {
-        num_n = (a.N + BN - 1) / BN;
+        num_n = (a.N + TN - 1) / TN;
         num_m = WGRAD ? (a.M + (PAIR ? 2 * BM : BM) - 1) / (PAIR ? 2 * BM : BM) : pre[a.g.E];
         total = WGRAD ? (long long)a.g.E * num_m * num_n : (long long)num_m * num_n;
     }
@@ -138,7 +152,7 @@ struct Work {
             t.e = (int)(w / per);
             const int r = (int)(w - (long long)t.e * per);
             const int mu = num_n < num_m ? r / num_n : r % num_m;
-            t.n0 = (num_n < num_m ? r % num_n : r / num_m) * BN;
+            t.n0 = (num_n < num_m ? r % num_n : r / num_m) * TN;
             t.m0 = (PAIR ? 2 * mu + rank : mu) * BM;
             const Segment s = table.at(t.e);
             t.row = s.begin;
@@ -157,9 +171,9 @@ struct Work {
             const int group = r0 / (nu * G), r = r0 - group * nu * G;
             const int gsz = min(G, num_n - group * G);
             const int mu = r / gsz;
-            t.n0 = (group * G + r % gsz) * BN;
+            t.n0 = (group * G + r % gsz) * TN;
             const Segment s = table.at(t.e);
-            const int first = mu * (PAIR ? 2 * BM : BM);       // row of the unit in its segment
+            const int first = mu * Cfg<MODE>::ROWS;       // row of the unit in its segment
             t.half = PAIR && s.end - s.begin - first <= BM;
             const int mine = first + (PAIR ? rank * (t.half ? BM / 2 : BM) : 0);
             t.row = s.begin + mine;
@@ -167,11 +181,12 @@ struct Work {
             t.kblocks = first < s.valid ? (a.K + DEPTH - 1) / DEPTH : 0;
             t.tail = DEPTH;
             t.end = s.end - t.row;
+            if (MODE == FEW) t.end = min(t.end, FM);
             t.valid = s.valid - mine;
         }
         // the MMA's N: a multiple of 16, of 32 in a pair
         constexpr int step = PAIR ? 32 : 16;
-        t.nt = min(BN, (a.N - t.n0 + step - 1) / step * step);
+        t.nt = min(TN, (a.N - t.n0 + step - 1) / step * step);
         return t;
     }
 };
@@ -210,12 +225,13 @@ __device__ __forceinline__ uint4 shift_windows(const Windows& q, const __nv_bflo
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <bool WGRAD, bool B_MN, bool PAIR, bool GUARD>
+template <bool WGRAD, bool B_MN, Mode MODE, bool GUARD>
 __global__ void __launch_bounds__(threads<WGRAD, GUARD>(), 1)
 kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
        const __grid_constant__ CUtensorMap mH, const Args a)
 {
-    using C = Cfg<PAIR>;
+    using C = Cfg<MODE>;
+    constexpr bool PAIR = MODE == PAIRS;
     DeviceStatus* const status = &wait_status;
     constexpr int S = C::STAGES;
     constexpr uint32_t IDESC = ptx::idesc_bf16<0, WGRAD, B_MN, PAIR ? 2 * BM : BM>();
@@ -270,14 +286,14 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             ptx::tmem_relinquish();
         }
     }
-    read_segments<PAIR ? 2 * BM : BM>(a.g, &table);
+    read_segments<C::ROWS>(a.g, &table);
     ptx::tc_fence_before();
     if (PAIR) ptx::cluster_sync();             // the peer's barriers exist before any remote signal
     else __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
-    Work<WGRAD, PAIR> work;
+    Work<WGRAD, MODE> work;
     work.init(a, table.pre);
     work.total = __shfl_sync(0xffffffffu, work.total, 0);
     auto wait = [&](uint32_t bar, uint32_t parity, int where) {
@@ -445,6 +461,14 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                     __nv_bfloat16* dst = p0 + u * 64;
 #pragma unroll
                     for (int i = 0; i < 8; ++i, dst += step) *reinterpret_cast<uint4*>(dst) = x[i];
+                } else if (a.vec && left >= 64) {
+                    __nv_bfloat16* dst = p0 + u * 64;
+                    for (int i = 0; 4 * i < rows; ++i, dst += step) {
+                        uint4 x;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                     : "r"(s0 + i * 512 + (i & 1 ? x0 ^ 64u : x0)) : "memory");
+                        if (4 * i + (lane >> 3) < rows) *reinterpret_cast<uint4*>(dst) = x;
+                    }
                 } else {
                     for (int r = 0; r < min(rows, 32); ++r) {
 #pragma unroll
@@ -628,11 +652,12 @@ inline cudaError_t take_status(int* code, cudaStream_t s)
     return e;
 }
 
-template <bool WGRAD, bool B_MN, bool PAIR, bool GUARD>
+template <bool WGRAD, bool B_MN, Mode MODE, bool GUARD>
 cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mH, const Args& a, long long units, int num_sms, cudaStream_t s)
 {
-    using C = Cfg<PAIR>;
-    auto k = kernel<WGRAD, B_MN, PAIR, GUARD>;
+    using C = Cfg<MODE>;
+    constexpr bool PAIR = MODE == PAIRS;
+    auto k = kernel<WGRAD, B_MN, MODE, GUARD>;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
     cfg.blockDim = dim3(threads<WGRAD, GUARD>());

@@ -38,6 +38,24 @@ namespace {
 // 7168 x 2048, the gradient of the rows: 451 us as single CTAs, 414 as pairs).
 constexpr long long kPairRows = 128;
 
+// ... and below which they are tiles of few rows.
+constexpr long long kFewRows = 32;
+
+template <bool B_MN, Mode MODE>
+bool rows_mode(const GroupedRows& p, const Args& a, int num_sms, cudaStream_t s, cudaError_t* e)
+{
+    using C = Cfg<MODE>;
+    CUtensorMap mA, mB, mH{};
+    if (!make_map(&mA, p.X, p.K, p.g.rows, 1, p.ldx, 0, MODE == FEW ? FM : BM) ||
+        (MODE == PAIRS && !make_map(&mH, p.X, p.K, p.g.rows, 1, p.ldx, 0, BM / 2)) ||
+        !(B_MN ? make_map(&mB, p.W, p.N, p.K, p.g.E, p.ldw, p.sw, BK)
+               : make_map(&mB, p.W, p.K, p.N, p.g.E, p.ldw, p.sw, C::B_COLS)))
+        return false;
+    const long long units = row_tiles_bound(p.g.rows, p.g.E, C::ROWS) * ((p.N + C::COLS - 1) / C::COLS);
+    *e = launch<false, B_MN, MODE, false>(mA, mB, mH, a, units, num_sms, s);
+    return true;
+}
+
 template <bool B_MN>
 cudaError_t rows_tc(const GroupedRows& p, int num_sms, cudaStream_t s)
 {
@@ -46,19 +64,16 @@ cudaError_t rows_tc(const GroupedRows& p, int num_sms, cudaStream_t s)
     a.K = p.K; a.N = p.N;
     a.out = p.Y; a.ldo = p.ldy;
     a.vec = p.ldy % 8 == 0;
-    const bool pair = p.g.rows / p.g.E >= kPairRows;
-    const long long num_n = (p.N + BN - 1) / BN;
-    const long long units = row_tiles_bound(p.g.rows, p.g.E, pair ? 2 * BM : BM) * num_n;
-    CUtensorMap mA, mB, mH;
-    const int bcols = pair ? BN / 2 : BN;
-    if (make_map(&mA, p.X, p.K, p.g.rows, 1, p.ldx, 0, BM) && make_map(&mH, p.X, p.K, p.g.rows, 1, p.ldx, 0, BM / 2) &&
-        (B_MN ? make_map(&mB, p.W, p.N, p.K, p.g.E, p.ldw, p.sw, BK) : make_map(&mB, p.W, p.K, p.N, p.g.E, p.ldw, p.sw, bcols)))
-        return pair ? launch<false, B_MN, true, false>(mA, mB, mH, a, units, num_sms, s)
-                    : launch<false, B_MN, false, false>(mA, mB, mH, a, units, num_sms, s);
+    const long long each = p.g.rows / p.g.E;
+    cudaError_t e = cudaSuccess;
+    if (each < kFewRows ? rows_mode<B_MN, FEW>(p, a, num_sms, s, &e)
+                        : (each >= kPairRows ? rows_mode<B_MN, PAIRS>(p, a, num_sms, s, &e)
+                                             : rows_mode<B_MN, SINGLE>(p, a, num_sms, s, &e)))
+        return e;
     a.A = static_cast<const __nv_bfloat16*>(p.X); a.lda = p.ldx;
     a.B = static_cast<const __nv_bfloat16*>(p.W); a.ldb = p.ldw; a.sb = p.sw;
-    return launch<false, B_MN, false, true>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, a,
-                                            row_tiles_bound(p.g.rows, p.g.E, BM) * num_n, num_sms, s);
+    const long long units = row_tiles_bound(p.g.rows, p.g.E, BM) * ((p.N + BN - 1) / BN);
+    return launch<false, B_MN, SINGLE, true>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, a, units, num_sms, s);
 }
 
 }  // namespace

@@ -125,7 +125,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
-    Work<false, false, QK> work;
+    Work<false, SINGLE, QK> work;
     work.init(a, table.pre);
     work.total = __shfl_sync(0xffffffffu, work.total, 0);
     auto wait = [&](uint32_t bar, uint32_t parity, int where) {
