@@ -9,8 +9,8 @@
 // Persistent blocks, one to an SM. Warp 0 loads 64-deep blocks of both operands into a
 // ring of shared-memory stages by TMA (128-byte swizzle); warp 1 issues tcgen05.mma from
 // one elected thread into one of two 256-column accumulators; warps 2-5 read the other
-// one (tcgen05.ld, a row to a thread) and store it through a swizzled staging buffer in
-// whole lines. Segments start at any row: a tile's A box simply runs into the next
+// one (tcgen05.ld, a row to a thread) and store it by TMA from swizzled staging buffers (a
+// segment's last rows by the warp). Segments start at any row: a tile's A box simply runs into the next
 // expert's rows, whose products are not stored.
 //   - The issuing loops run in an elected thread (elect.sync): from a branch on the lane
 //     number the compiler cannot use the uniform datapath, and a block of four MMAs, its
@@ -54,7 +54,7 @@ struct Args {
     int M, N;                 // outputs of a weight gradient (M); columns (N)
     void* out;
     long long ldo, so;
-    int vec;                  // outputs in 16-byte pieces
+    int vec;                  // outputs in 16-byte pieces (and by TMA)
     const __nv_bfloat16 *A, *B;   // GUARD
     long long lda, ldb, sb;
 };
@@ -117,6 +117,12 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint
         asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
                      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar),
                      "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+__device__ __forceinline__ void store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
 // A tile of outputs, as every role of a block sees it.
@@ -228,7 +234,7 @@ __device__ __forceinline__ uint4 shift_windows(const Windows& q, const __nv_bflo
 template <bool WGRAD, bool B_MN, Mode MODE, bool GUARD>
 __global__ void __launch_bounds__(threads<WGRAD, GUARD>(), 1)
 kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
-       const __grid_constant__ CUtensorMap mH, const Args a)
+       const __grid_constant__ CUtensorMap mH, const __grid_constant__ CUtensorMap mO, const Args a)
 {
     using C = Cfg<MODE>;
     constexpr bool PAIR = MODE == PAIRS;
@@ -403,7 +409,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         // ----------------------------------------------------------- outputs
         const int q = warp & 3;                 // this warp's quarter of the TMEM lanes
         const uint32_t stg = staging + (uint32_t)q * 4096u;
-        int acc = 0;
+        int acc = 0, stores = 0;
         uint32_t aph = 0;
         for (long long w = unit0; w < work.total; w += nunits) {
             Tile t = work.at(a, table, w, rank);
@@ -421,65 +427,64 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                                (WGRAD ? t.e * a.so + (long long)(t.m0 + r0) * a.ldo
                                       : (long long)(t.row + r0) * a.ldo);
             const int cols = __shfl_sync(0xffffffffu, min(a.N - t.n0 - c0, t.half ? t.nt / 2 : t.nt), 0);
-            // eight lanes to a row of 128 bytes, four rows an instruction
-            const int ch = lane & 7;
-            __nv_bfloat16* p0 = o + (lane >> 3) * a.ldo + ch * 8;
-            const long long step = 4 * a.ldo;
-            const uint32_t s0 = stg + (lane >> 3) * 128, x0 = (uint32_t)((ch ^ (lane >> 3)) << 4);
+            const bool whole = a.vec && (WGRAD || rows >= 32), last = t.n0 + c0 + cols == a.N;
 #pragma unroll 1
-            for (int u = 0; u * 64 < cols && rows > 0; ++u) {
-                uint32_t v0[32], v1[32];
+            for (int u = 0; u * 32 < cols && rows > 0; ++u) {
+                uint32_t v[32];
                 if (t.kblocks > 0) {
-                    ptx::tmem_ld32(taddr + u * 64, v0);
-                    ptx::tmem_ld32(taddr + u * 64 + 32, v1);
+                    ptx::tmem_ld32(taddr + u * 32, v);
                     ptx::tmem_ld_wait();
                 }
                 if (t.kblocks == 0 || !mine) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v0[i] = v1[i] = 0u;
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
+                // 32 rows of 64 bytes, swizzled over them, in turns with the other half's store; TMA
+                // leaves out what lies past the tensor (not past this warp's columns)
+                const int left = cols - u * 32;
+                const bool by_tma = __shfl_sync(0xffffffffu, (int)(whole && (left >= 32 || last)), 0) != 0;
+                const uint32_t buf = stg + (uint32_t)(stores & 1) * 2048u;
+                if (lane == 0) {                // what still reads this half
+                    if (by_tma) ptx::bulk_wait_read<1>();
+                    else ptx::bulk_wait_read<0>();
+                }
+                __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t* src = j < 4 ? v0 + 8 * j : v1 + 8 * (j - 4);
+                for (int j = 0; j < 4; ++j) {
                     uint32_t p[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(src[2 * i]), __uint_as_float(src[2 * i + 1]));
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
                         p[i] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
                                  "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]) : "memory");
                 }
+                if (by_tma) {
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        store_3d(&mO, buf, t.n0 + c0 + u * 32, WGRAD ? t.m0 + r0 : t.row + r0, WGRAD ? t.e : 0);
+                        ptx::bulk_commit();
+                    }
+                    ++stores;
+                    continue;
+                }
+                // the last rows of a segment, or outputs off the 16-byte boundaries
                 __syncwarp();
-                const int left = cols - u * 64;
-                if (a.vec && rows >= 32 && left >= 64) {
-                    uint4 x[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)     // row 4 i + lane / 8: its swizzle is that of 4 (i % 2) + lane / 8
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
-                                     : "r"(s0 + i * 512 + (i & 1 ? x0 ^ 64u : x0)) : "memory");
-                    __nv_bfloat16* dst = p0 + u * 64;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i, dst += step) *reinterpret_cast<uint4*>(dst) = x[i];
-                } else if (a.vec && left >= 64) {
-                    __nv_bfloat16* dst = p0 + u * 64;
-                    for (int i = 0; 4 * i < rows; ++i, dst += step) {
+                if (a.vec && left >= 32) {
+                    // four lanes to a row of 64 bytes, eight rows an instruction
+                    for (int r = lane >> 2; r < min(rows, 32); r += 8) {
                         uint4 x;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                                     : "r"(s0 + i * 512 + (i & 1 ? x0 ^ 64u : x0)) : "memory");
-                        if (4 * i + (lane >> 3) < rows) *reinterpret_cast<uint4*>(dst) = x;
+                                     : "r"(buf + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)) : "memory");
+                        *reinterpret_cast<uint4*>(o + r * a.ldo + u * 32 + (lane & 3) * 8) = x;
                     }
-                } else {
+                } else if (lane < left) {
                     for (int r = 0; r < min(rows, 32); ++r) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int c = lane + 32 * h;
-                            if (c < left) {
-                                unsigned short x;
-                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(stg + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2) : "memory");
-                                reinterpret_cast<unsigned short*>(o + r * a.ldo + u * 64)[c] = x;
-                            }
-                        }
+                        unsigned short x;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(buf + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2) : "memory");
+                        reinterpret_cast<unsigned short*>(o + r * a.ldo + u * 32)[lane] = x;
                     }
                 }
                 __syncwarp();
@@ -494,6 +499,8 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
+        if (lane == 0) ptx::bulk_wait_all();   // the stores are done before the block ends
+        __syncwarp();
     } else if (GUARD && warp >= 6) {
         // ------------------------------------------- loads off the boundaries
         const int tid = (int)threadIdx.x - 192, ch = tid & 7;
@@ -572,11 +579,13 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             if (t.tail == BK) continue;
             if (!__all_sync(0xffffffffu, wait(land_bar(s), (phases >> s) & 1u, 7))) break;
             phases ^= 1u << s;
-            const int up = min((t.tail + 15) / 16 * 16, BK), n = (up - t.tail) * 8;   // 16-byte pieces of a stripe
+            // the rows up to the next multiple of 16, in A's two stripes and in B's
+            const int n = ((t.tail + 15) / 16 * 16 - t.tail) * 8;
             const int bcols = PAIR ? t.nt / 2 : t.nt, stripes = BM / 64 + (bcols + 63) / 64;
             const uint32_t at = ring + s * C::STAGE + t.tail * 128;
-            for (int i = lane; i < n * stripes; i += 32)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + i / n * STRIPE + i % n * 16), "r"(0) : "memory");
+            for (int st = 0; st < stripes; ++st)
+                for (int i = lane; i < n; i += 32)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + st * STRIPE + i * 16), "r"(0) : "memory");
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -597,11 +606,11 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
 }
 
 // ------------------------------------------------------------------ host
-// 3-D tensor map of bf16 values (or bytes): inner x rows x mats, boxes of 128 bytes x
-// box_rows x 1, 128-byte swizzle, zeros outside. False where the strides are none that TMA
-// takes.
+// 3-D tensor map of bf16 values (or bytes): inner x rows x mats, boxes of `width` bytes x
+// box_rows x 1, swizzled over that width, zeros outside. False where the strides are none
+// that TMA takes.
 bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, long long mats, long long ld,
-              long long stride, int box_rows, int bytes = 2);
+              long long stride, int box_rows, int bytes = 2, int width = 128);
 
 // The units that run at once of a kernel with this much shared memory, set up on the first
 // call of each device (slots: one per kernel, zeros).
@@ -653,7 +662,7 @@ inline cudaError_t take_status(int* code, cudaStream_t s)
 }
 
 template <bool WGRAD, bool B_MN, Mode MODE, bool GUARD>
-cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mH, const Args& a, long long units, int num_sms, cudaStream_t s)
+cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mH, const CUtensorMap& mO, const Args& a, long long units, int num_sms, cudaStream_t s)
 {
     using C = Cfg<MODE>;
     constexpr bool PAIR = MODE == PAIRS;
@@ -676,7 +685,7 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
     if (e != cudaSuccess) return e;
     const long long grid = units < n ? (units > 0 ? units : 1) : n;
     cfg.gridDim = dim3((unsigned)(PAIR ? 2 * grid : grid));
-    return cudaLaunchKernelEx(&cfg, k, mA, mB, mH, a);
+    return cudaLaunchKernelEx(&cfg, k, mA, mB, mH, mO, a);
 }
 
 }  // namespace gtc

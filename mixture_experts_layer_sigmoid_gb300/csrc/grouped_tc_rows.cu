@@ -6,7 +6,7 @@ namespace moe {
 namespace gtc {
 
 bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, long long mats, long long ld,
-              long long stride, int box_rows, int bytes)
+              long long stride, int box_rows, int bytes, int width)
 {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
@@ -22,9 +22,9 @@ bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, lo
     if (stride * bytes >= (1ll << 40) || ld * bytes >= (1ll << 40)) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)mats};
     const cuuint64_t strides[2] = {(cuuint64_t)(ld * bytes), (cuuint64_t)(stride * bytes)};
-    const cuuint32_t box[3] = {128u / (unsigned)bytes, (cuuint32_t)box_rows, 1u}, es[3] = {1u, 1u, 1u};
+    const cuuint32_t box[3] = {(unsigned)(width / bytes), (cuuint32_t)box_rows, 1u}, es[3] = {1u, 1u, 1u};
     return encode(m, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -42,7 +42,7 @@ constexpr long long kPairRows = 128;
 constexpr long long kFewRows = 32;
 
 template <bool B_MN, Mode MODE>
-bool rows_mode(const GroupedRows& p, const Args& a, int num_sms, cudaStream_t s, cudaError_t* e)
+bool rows_mode(const GroupedRows& p, const Args& a, const CUtensorMap& mO, int num_sms, cudaStream_t s, cudaError_t* e)
 {
     using C = Cfg<MODE>;
     CUtensorMap mA, mB, mH{};
@@ -52,7 +52,7 @@ bool rows_mode(const GroupedRows& p, const Args& a, int num_sms, cudaStream_t s,
                : make_map(&mB, p.W, p.K, p.N, p.g.E, p.ldw, p.sw, C::B_COLS)))
         return false;
     const long long units = row_tiles_bound(p.g.rows, p.g.E, C::ROWS) * ((p.N + C::COLS - 1) / C::COLS);
-    *e = launch<false, B_MN, MODE, false>(mA, mB, mH, a, units, num_sms, s);
+    *e = launch<false, B_MN, MODE, false>(mA, mB, mH, mO, a, units, num_sms, s);
     return true;
 }
 
@@ -63,17 +63,18 @@ cudaError_t rows_tc(const GroupedRows& p, int num_sms, cudaStream_t s)
     a.g = p.g;
     a.K = p.K; a.N = p.N;
     a.out = p.Y; a.ldo = p.ldy;
-    a.vec = p.ldy % 8 == 0;
+    CUtensorMap mO{};
+    a.vec = make_map(&mO, p.Y, p.N, p.g.rows, 1, p.ldy, 0, 32, 2, 64);
     const long long each = p.g.rows / p.g.E;
     cudaError_t e = cudaSuccess;
-    if (each < kFewRows ? rows_mode<B_MN, FEW>(p, a, num_sms, s, &e)
-                        : (each >= kPairRows ? rows_mode<B_MN, PAIRS>(p, a, num_sms, s, &e)
-                                             : rows_mode<B_MN, SINGLE>(p, a, num_sms, s, &e)))
+    if (each < kFewRows ? rows_mode<B_MN, FEW>(p, a, mO, num_sms, s, &e)
+                        : (each >= kPairRows ? rows_mode<B_MN, PAIRS>(p, a, mO, num_sms, s, &e)
+                                             : rows_mode<B_MN, SINGLE>(p, a, mO, num_sms, s, &e)))
         return e;
     a.A = static_cast<const __nv_bfloat16*>(p.X); a.lda = p.ldx;
     a.B = static_cast<const __nv_bfloat16*>(p.W); a.ldb = p.ldw; a.sb = p.sw;
     const long long units = row_tiles_bound(p.g.rows, p.g.E, BM) * ((p.N + BN - 1) / BN);
-    return launch<false, B_MN, SINGLE, true>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, a, units, num_sms, s);
+    return launch<false, B_MN, SINGLE, true>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, mO, a, units, num_sms, s);
 }
 
 }  // namespace

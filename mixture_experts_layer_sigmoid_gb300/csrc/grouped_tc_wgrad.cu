@@ -12,18 +12,19 @@ cudaError_t launch_grouped_wgrad_tc(const GroupedWgrad& p, int num_sms, cudaStre
     a.g = p.g;
     a.M = p.M; a.N = p.N;
     a.out = p.D; a.ldo = p.ldd; a.so = p.sd;
-    a.vec = p.ldd % 8 == 0 && p.sd % 8 == 0;
+    CUtensorMap mO{};
+    a.vec = make_map(&mO, p.D, p.N, p.M, p.g.E, p.ldd, p.sd, 32, 2, 64);
     // one CTA's 128 rows hold a narrow M; wider ones go to pairs
     const bool pair = p.M > BM;
     const long long num_n = (p.N + BN - 1) / BN;
     auto units = [&](int tm) { return (long long)p.g.E * ((p.M + tm - 1) / tm) * num_n; };
     CUtensorMap mA, mB;
     if (p.g.rows > 0 && make_map(&mA, p.A, p.M, p.g.rows, 1, p.lda, 0, BK) && make_map(&mB, p.B, p.N, p.g.rows, 1, p.ldb, 0, BK))
-        return pair ? launch<true, true, PAIRS, false>(mA, mB, mA, a, units(2 * BM), num_sms, s)
-                    : launch<true, true, SINGLE, false>(mA, mB, mA, a, units(BM), num_sms, s);
+        return pair ? launch<true, true, PAIRS, false>(mA, mB, mA, mO, a, units(2 * BM), num_sms, s)
+                    : launch<true, true, SINGLE, false>(mA, mB, mA, mO, a, units(BM), num_sms, s);
     a.A = static_cast<const __nv_bfloat16*>(p.A); a.lda = p.lda;
     a.B = static_cast<const __nv_bfloat16*>(p.B); a.ldb = p.ldb;
-    return launch<true, true, SINGLE, true>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, a, units(BM), num_sms, s);
+    return launch<true, true, SINGLE, true>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, mO, a, units(BM), num_sms, s);
 }
 cudaError_t take_wgrad_status(int* code, cudaStream_t s) { return take_status(code, s); }
 
