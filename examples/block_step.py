@@ -1,8 +1,8 @@
 """Two pre-norm expert blocks, trained for a few steps, then one token decoded.
 
 Block 1 has this library's expert layer (MoELayer); block 2 has experts of its
-own (here squared-ReLU FFNs in torch), which the library's routing and token
-sort serve:
+own (here squared-ReLU FFNs), which the library's routing, token sort and grouped
+products serve:
 
     h1, y1 = add_rms_norm(x)            m1  = MoELayer(y1)
     h2, y2 = add_rms_norm(m1, h1)       out = h2 + sum_j g_j expert_j(y2)
@@ -53,10 +53,6 @@ class Blocks:
             raise moe.MoEError(st, "moe_route_static")
         return topk, gates
 
-    def segments(self, index):
-        o = index["offsets"].tolist()
-        return [(e, slice(o[e], o[e + 1])) for e in range(self.E) if o[e + 1] > o[e]]
-
     def forward(self, x):
         p, s = self.p, {}
         s["x"] = x
@@ -68,23 +64,17 @@ class Blocks:
         s["topk"], s["gates"] = self.route(s["y2"], p["Wr2"])
         ix = s["index"] = moe.sort_index(s["topk"], self.E, self.align)
         s["X"] = moe.sort_rows(s["y2"], ix)
-        s["Z"], s["Y"] = torch.zeros((len(s["X"]), self.F), dtype=self.dtype, device="cuda"), torch.zeros_like(s["X"])
-        for e, rows in self.segments(ix):
-            s["Z"][rows] = s["X"][rows] @ p["A"][e]
-            s["Y"][rows] = s["Z"][rows].relu().square() @ p["B"][e]
+        s["Z"] = moe.grouped_matmul(s["X"], p["A"], ix)
+        s["R"] = s["Z"].relu().square()
+        s["Y"] = moe.grouped_matmul(s["R"], p["B"], ix)
         return moe.unsort_rows(s["Y"], ix, s["gates"], s["h2"]), s
 
     def backward(self, dout, s):
         p, ix = self.p, s["index"]
-        d = {n: torch.zeros_like(p[n]) for n in ("A", "B")}
+        d = {}
         dY, dg = moe.unsort_rows_backward(dout, s["Y"], ix, s["gates"])
-        dX = torch.zeros_like(s["X"])
-        for e, rows in self.segments(ix):
-            r = s["Z"][rows].relu()
-            d["B"][e] = r.square().T @ dY[rows]
-            dz = 2 * r * (dY[rows] @ p["B"][e].T)
-            d["A"][e] = s["X"][rows].T @ dz
-            dX[rows] = dz @ p["A"][e].T
+        dR, d["B"] = moe.grouped_matmul_backward(dY, s["R"], p["B"], ix)
+        dX, d["A"] = moe.grouped_matmul_backward(2 * s["Z"].relu() * dR, s["X"], p["A"], ix)
         # the router's share: sigmoid scores over their sum
         chosen = s["topk"].long()
         score = torch.sigmoid((s["y2"].float() @ p["Wr2"]).gather(1, chosen))
@@ -113,9 +103,19 @@ class Blocks:
         topk, gates = self.route(n["y"], self.p["Wr2"])
         ix = moe.sort_index(topk, self.E)
         X = moe.sort_rows(n["y"], ix)
-        Y = torch.stack([(X[r] @ self.p["A"][e]).relu().square() @ self.p["B"][e]
-                         for r, e in enumerate(sorted(topk.flatten().tolist()))])
+        Y = moe.grouped_matmul(moe.grouped_matmul(X, self.p["A"], ix).relu().square(), self.p["B"], ix)
         return moe.unsort_rows(Y, ix, gates, n["h"]), n["codes"], n["scales"]
+
+    def decode_8bit(self, x):
+        """The same tokens through experts whose weights are kept as E4M3 codes."""
+        if not hasattr(self, "codes"):
+            self.codes = {n: moe.quantize_tiles(self.p[n]) for n in ("A", "B")}
+        n = moe.add_rms_norm(x, self.p["n2"], torch.zeros_like(x))
+        topk, gates = self.route(n["y"], self.p["Wr2"])
+        ix = moe.sort_index(topk, self.E)
+        X = moe.quantize_rows(moe.sort_rows(n["y"], ix), ix)
+        R = moe.quantize_rows(moe.fp8_matmul(*X, *self.codes["A"], ix).relu().square(), ix)
+        return moe.unsort_rows(moe.fp8_matmul(*R, *self.codes["B"], ix), ix, gates, n["h"])
 
 
 def main():
@@ -131,6 +131,8 @@ def main():
         print(f"step {i}: loss {loss.item():.4f}, gradient norm {norm.item():.4f}")
     y, codes, scales = m.decode(x[:1])
     print(f"decoded one token: |y| {y.float().norm().item():.3f}, {codes.numel()} codes, {scales.numel()} scale bytes")
+    y8 = m.decode_8bit(x[:1])
+    print(f"with 8-bit experts: |y| {y8.float().norm().item():.3f}")
 
 
 if __name__ == "__main__":
