@@ -5,14 +5,16 @@
 //   rows            Y[r][n] = sum_k X[r][k] W[e(r)][k][n]
 //   weight gradient D[e][m][n] = sum over the expert's rows r of A[r][m] B[r][n]
 //
-// A block of 256 threads owns a TM x TN tile of outputs, a thread (TM/16) x (TN/16) of
-// them as pairs of columns (fma.rn.f32x2; scalar FMAs 128 us where pairs take 105). Chunks of 16 along the contraction come through a
-// ring of three stages of shared memory by cp.async, four bytes at a time, so that any strides
-// and widths take this path and operands are transposed on the way; with the loads through
-// registers and one chunk ahead, a chunk cost a round trip to L2 (2042 rows of 1024 x 640
-// 120 us). Each output is one thread's sum in ascending order. Blocks are persistent and
-// read the segments on the device. Tiles of 128 x 128 need half of the reads of shared
-// memory, tiles of 64 x 64 are taken while the larger ones do not fill the SMs.
+// A block of 256 threads owns a tile of TT x TT outputs (16 x 64 for few rows), a thread
+// (TT/16)^2 of them. Chunks of
+// 32 along the contraction come through a ring of stages of shared memory by cp.async,
+// each operand as it lies in memory: in 16-byte pieces where its rows are aligned (four-byte
+// ones, transposed on the way, took 107 us for 2042 rows of 1024 x 640), else value by value.
+// A thread reads four values along the contraction (or four neighbours at each of four
+// steps) at a time; the layout in shared memory keeps both ways free of bank conflicts. Each
+// output is one thread's sum in ascending order. Blocks are persistent and read the segments
+// on the device. Tiles of 128 need half of the reads of shared memory; tiles of 64 are taken
+// while the larger ones are fewer than four for each SM.
 #include "grouped.cuh"
 #include "epilogue.cuh"
 
@@ -21,183 +23,196 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, BK = 16, kStages = 3;
+constexpr int kThreads = 256, BK = 32;
+// Stages of the ring: with few rows the time is the loads' (one row of 8192 x 8192 197 us with three).
+template <int TM> constexpr int kStages = TM == 16 ? 8 : 3;
 
-__device__ __forceinline__ uint64_t dup2(float a)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(a));
-    return r;
-}
-__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b)
-{
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-
-// A stage of one operand: TT values by 16 along the contraction.
-template <int TT> using Stage = float[BK][TT + 4];
-
-// What a thread copies of each chunk of one operand: value (i, k) stands at i ld + k (K_FIRST)
-// or k ld + i; a thread's values of a chunk have one i and k in steps, or the other way round.
+// One operand of a tile: TT values of i by the contraction, value (i, k) at p + i ld + k
+// (K_FIRST) or p + k ld + i; n_i of the i exist. In shared memory a chunk lies the same way, in
+// rows of BK + 4 or TT + 4.
 template <int TT, bool K_FIRST>
-struct Loader {
-    static constexpr int COUNT = TT * BK / kThreads;
-    static constexpr int STEP = K_FIRST ? kThreads / BK : kThreads / TT;    // of i, or of k
-    const float *p, *first;             // the next chunk's; a value that exists
-    long long step, chunk;
-    int i, k, n_i;
-    __device__ __forceinline__ Loader(const float* base, long long ld, int n_i_) : first(base), n_i(n_i_)
+struct Operand {
+    static constexpr int ROWS = K_FIRST ? TT : BK, ROW = K_FIRST ? BK : TT, LD = ROW + 4;
+    static constexpr int STAGE = ROWS * LD;    // values
+    static constexpr int PER = TT / 16;        // of a thread
+    const float* p;
+    long long ld;
+    int n_i;
+    bool vec;                                  // rows in 16-byte pieces
+
+    // Copies the chunk from k0 on, of which `left` along the contraction exist; the rest is zeros.
+    __device__ __forceinline__ void copy(float* s, int k0, int left) const
     {
-        i = K_FIRST ? threadIdx.x / BK : threadIdx.x % TT;
-        k = K_FIRST ? threadIdx.x % BK : threadIdx.x / TT;
-        p = base + (K_FIRST ? i * ld + k : k * ld + i);
-        step = STEP * ld;
-        chunk = K_FIRST ? (long long)BK : BK * ld;
-    }
-    // the next chunk, of which n_k values along the contraction exist; the others are zeros
-    __device__ __forceinline__ void copy(Stage<TT>& s, int n_k)
-    {
-        uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&s[k][i]));
-        const float* src = p;
+        const float* src = p + (K_FIRST ? (long long)k0 : k0 * ld);
+        const int n_rows = K_FIRST ? n_i : left, n_row = K_FIRST ? left : n_i;
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(s));
+        if (vec) {
 #pragma unroll
-        for (int j = 0; j < COUNT; ++j) {
-            const bool have = K_FIRST ? k < n_k && i + j * STEP < n_i : k + j * STEP < n_k && i < n_i;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(have ? src : first), "r"(have ? 4 : 0) : "memory");
-            src += step;
-            dst += (K_FIRST ? STEP : STEP * (TT + 4)) * 4;
+            for (int j = 0; j < (ROWS * ROW / 4 + kThreads - 1) / kThreads; ++j) {
+                const int c = threadIdx.x + j * kThreads, r = c / (ROW / 4), x = c % (ROW / 4) * 4;
+                if (ROWS * ROW / 4 < kThreads && r >= ROWS) break;
+                const int n = r < n_rows ? min(max(n_row - x, 0), 4) : 0;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (r * LD + x) * 4),
+                             "l"(n > 0 ? src + r * ld + x : p), "r"(4 * n) : "memory");
+            }
+        } else {
+#pragma unroll 4
+            for (int j = 0; j < ROWS * ROW / kThreads; ++j) {
+                const int c = threadIdx.x + j * kThreads, r = c / ROW, x = c % ROW;
+                const bool have = r < n_rows && x < n_row;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + (r * LD + x) * 4),
+                             "l"(have ? src + r * ld + x : p), "r"(have ? 4 : 0) : "memory");
+            }
         }
-        p += chunk;
+    }
+    // The i of a thread's j-th value: neighbours where they are read together, else sixteen apart.
+    static __device__ __forceinline__ int index(int t, int j)
+    {
+        return K_FIRST ? t + 16 * j : (j / 4) * (TT / 2) + t * 4 + j % 4;
+    }
+    // v[j][q]: the thread's j-th value at step k + q
+    __device__ __forceinline__ void read(const float* s, int t, int k, float (&v)[PER][4]) const
+    {
+        if constexpr (K_FIRST) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const float4 f = *reinterpret_cast<const float4*>(s + index(t, j) * LD + k);
+                v[j][0] = f.x; v[j][1] = f.y; v[j][2] = f.z; v[j][3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int h = 0; h < PER / 4; ++h) {
+                    const float4 f = *reinterpret_cast<const float4*>(s + (k + q) * LD + index(t, 4 * h));
+                    v[4 * h][q] = f.x; v[4 * h + 1][q] = f.y; v[4 * h + 2][q] = f.z; v[4 * h + 3][q] = f.w;
+                }
+        }
     }
 };
 
-// acc = A B over n_k > 0 values: A is n_m values of i by k at a, B n_n at b likewise.
-template <int TM, int TN, bool A_K, bool B_K>
-__device__ __forceinline__ void tile_product(const float* a, long long lda, int n_m, const float* b, long long ldb, int n_n,
-                                             int n_k, Stage<TM>* As, Stage<TN>* Bs, uint64_t (&acc)[TM / 16][TN / 32])
+template <typename OA, typename OB>
+constexpr int stage_values() { return OA::STAGE + OB::STAGE; }
+
+// acc = A B over n_k > 0 values.
+template <int S, typename OA, typename OB>
+__device__ __forceinline__ void tile_product(const OA& a, const OB& b, int n_k, float* smem, float (&acc)[OA::PER][OB::PER])
 {
-    constexpr int MT = TM / 16, NT = TN / 16;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    Loader<TM, A_K> la(a, lda, n_m);
-    Loader<TN, B_K> lb(b, ldb, n_n);
-    auto load = [&](int st, int left) {
-        if (left > 0) {
-            la.copy(As[st], left);
-            lb.copy(Bs[st], left);
+    auto load = [&](int st, int k0) {
+        if (k0 < n_k) {
+            a.copy(smem + st * stage_values<OA, OB>(), k0, n_k - k0);
+            b.copy(smem + st * stage_values<OA, OB>() + OA::STAGE, k0, n_k - k0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) load(i, n_k - i * BK);
+    for (int i = 0; i < S - 1; ++i) load(i, i * BK);
     int st = 0;
     for (int k0 = 0; k0 < n_k; k0 += BK) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
         __syncthreads();                       // this chunk is there, and the stage before it is read
-        load(st == 0 ? kStages - 1 : st - 1, n_k - k0 - (kStages - 1) * BK);
+        load(st == 0 ? S - 1 : st - 1, k0 + (S - 1) * BK);
+        const float* sa = smem + st * stage_values<OA, OB>();
+        const float* sb = sa + OA::STAGE;
 #pragma unroll
-        for (int kk = 0; kk < BK; ++kk) {
-            float av[MT];
-            uint64_t bv[NT / 2];
-            // rows ty*4.. and, in the larger tile, TM/2 + ty*4..; columns likewise: four
-            // consecutive values per read, the lanes side by side in the banks
+        for (int k = 0; k < BK; k += 4) {
+            float av[OA::PER][4], bv[OB::PER][4];
+            a.read(sa, ty, k, av);
+            b.read(sb, tx, k, bv);
 #pragma unroll
-            for (int h = 0; h < MT / 4; ++h) {
-                const float4 q = *reinterpret_cast<const float4*>(&As[st][kk][h * (TM / 2) + ty * 4]);
-                av[4 * h] = q.x; av[4 * h + 1] = q.y; av[4 * h + 2] = q.z; av[4 * h + 3] = q.w;
-            }
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int h = 0; h < NT / 4; ++h) {
-                const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&Bs[st][kk][h * (TN / 2) + tx * 4]);
-                bv[2 * h] = q.x; bv[2 * h + 1] = q.y;
-            }
+                for (int i = 0; i < OA::PER; ++i)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const uint64_t d = dup2(av[i]);
-#pragma unroll
-                for (int j = 0; j < NT / 2; ++j) fma2(acc[i][j], d, bv[j]);
-            }
+                    for (int j = 0; j < OB::PER; ++j) acc[i][j] = fmaf(av[i][q], bv[j][q], acc[i][j]);
         }
-        st = st + 1 == kStages ? 0 : st + 1;
+        st = st + 1 == S ? 0 : st + 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 }
 
-template <int TM, int TN>
+template <typename OA, typename OB>
 __device__ __forceinline__ void store_tile(float* out, long long ld, int n_m, int n_valid, int n_n,
-                                           const uint64_t (&acc)[TM / 16][TN / 32])
+                                           const float (&acc)[OA::PER][OB::PER])
 {
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
-    for (int i = 0; i < TM / 16; ++i) {
-        const int m = (i / 4) * (TM / 2) + ty * 4 + i % 4;
+    for (int i = 0; i < OA::PER; ++i) {
+        const int m = OA::index(ty, i);
         if (m >= n_m) continue;
 #pragma unroll
-        for (int j = 0; j < TN / 32; ++j) {
-            const int n = (j / 2) * (TN / 2) + tx * 4 + 2 * (j % 2);
-            float lo, hi;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(acc[i][j]));
-            if (n < n_n) out[m * ld + n] = m < n_valid ? lo : 0.f;
-            if (n + 1 < n_n) out[m * ld + n + 1] = m < n_valid ? hi : 0.f;
+        for (int j = 0; j < OB::PER; ++j) {
+            const int n = OB::index(tx, j);
+            if (n < n_n) out[m * ld + n] = m < n_valid ? acc[i][j] : 0.f;
         }
     }
 }
 
-template <int TM, int TN>
-constexpr int kStageBytes = kStages * BK * (TM + TN + 8) * 4;
-
-template <int TM, int TN, bool W_NK>
-__global__ void __launch_bounds__(kThreads, TM == 128 ? 2 : 3)
-grouped_rows_kernel(const GroupedRows p)
+// Whether matrices at p with these strides in values have rows on 16-byte boundaries.
+bool vectors(const void* p, long long ld, long long stride)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
-    Stage<TM>* As = reinterpret_cast<Stage<TM>*>(smem);
-    Stage<TN>* Bs = reinterpret_cast<Stage<TN>*>(smem + kStages * sizeof(Stage<TM>));
-    SegmentTable& table = *reinterpret_cast<SegmentTable*>(smem + kStageBytes<TM, TN>);
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 4 == 0 && stride % 4 == 0;
+}
+
+struct Vec { bool a, b; };
+
+template <int TM, int TT, bool W_NK>
+__global__ void __launch_bounds__(kThreads, TT == 128 ? 1 : 2)
+grouped_rows_kernel(const GroupedRows p, const Vec vec)
+{
+    using OA = Operand<TM, true>;
+    using OB = Operand<TT, W_NK>;
+    extern __shared__ __align__(16) float smem[];
+    SegmentTable& table = *reinterpret_cast<SegmentTable*>(smem + kStages<TM> * stage_values<OA, OB>());
     read_segments<TM>(p.g, &table);
     const int* pre = table.pre;
-    const int num_n = (p.N + TN - 1) / TN;
+    const int num_n = (p.N + TT - 1) / TT;
     const long long total = (long long)pre[p.g.E] * num_n;
     for (long long w = blockIdx.x; w < total; w += gridDim.x) {
-        const int q = (int)(w / num_n), n0 = (int)(w % num_n) * TN;
+        const int q = (int)(w / num_n), n0 = (int)(w % num_n) * TT;
         const int e = segment_at(pre, p.g.E, q);
         const Segment s = table.at(e);
         const int at = (q - pre[e]) * TM, row = s.begin + at, valid = s.valid - at;
-        uint64_t acc[TM / 16][TN / 32] = {};
+        float acc[OA::PER][OB::PER] = {};
         if (valid > 0) {
-            const float* x = static_cast<const float*>(p.X) + (long long)row * p.ldx;
-            const float* wt = static_cast<const float*>(p.W) + e * p.sw + (W_NK ? (long long)n0 * p.ldw : (long long)n0);
-            tile_product<TM, TN, true, W_NK>(x, p.ldx, valid, wt, p.ldw, p.N - n0, p.K, As, Bs, acc);
+            const OA a{static_cast<const float*>(p.X) + (long long)row * p.ldx, p.ldx, valid, vec.a};
+            const OB b{static_cast<const float*>(p.W) + e * p.sw + (W_NK ? (long long)n0 * p.ldw : (long long)n0), p.ldw,
+                       p.N - n0, vec.b};
+            tile_product<kStages<TM>>(a, b, p.K, smem, acc);
         }
-        store_tile<TM, TN>(static_cast<float*>(p.Y) + (long long)row * p.ldy + n0, p.ldy, s.end - row, valid, p.N - n0, acc);
+        store_tile<OA, OB>(static_cast<float*>(p.Y) + (long long)row * p.ldy + n0, p.ldy, min(s.end - row, TM), valid,
+                           p.N - n0, acc);
     }
 }
 
-template <int TM, int TN>
-__global__ void __launch_bounds__(kThreads, TM == 128 ? 2 : 3)
-grouped_wgrad_kernel(const GroupedWgrad p)
+template <int TT>
+__global__ void __launch_bounds__(kThreads, TT == 128 ? 1 : 2)
+grouped_wgrad_kernel(const GroupedWgrad p, const Vec vec)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
-    Stage<TM>* As = reinterpret_cast<Stage<TM>*>(smem);
-    Stage<TN>* Bs = reinterpret_cast<Stage<TN>*>(smem + kStages * sizeof(Stage<TM>));
-    const int num_m = (p.M + TM - 1) / TM, num_n = (p.N + TN - 1) / TN;
+    using O = Operand<TT, false>;
+    extern __shared__ __align__(16) float smem[];
+    const int num_m = (p.M + TT - 1) / TT, num_n = (p.N + TT - 1) / TT;
     const long long per = (long long)num_m * num_n, total = per * p.g.E;
     for (long long w = blockIdx.x; w < total; w += gridDim.x) {
-        const int e = (int)(w / per), r = (int)(w % per), m0 = r / num_n * TM, n0 = r % num_n * TN;
+        const int e = (int)(w / per), r = (int)(w % per), m0 = r / num_n * TT, n0 = r % num_n * TT;
         const Segment s = segment_of(p.g, e);
-        uint64_t acc[TM / 16][TN / 32] = {};
-        if (s.valid > 0)
-            tile_product<TM, TN, false, false>(static_cast<const float*>(p.A) + (long long)s.begin * p.lda + m0, p.lda,
-                                               p.M - m0, static_cast<const float*>(p.B) + (long long)s.begin * p.ldb + n0,
-                                               p.ldb, p.N - n0, s.valid, As, Bs, acc);
-        store_tile<TM, TN>(static_cast<float*>(p.D) + e * p.sd + (long long)m0 * p.ldd + n0, p.ldd, p.M - m0, p.M - m0,
-                           p.N - n0, acc);
+        float acc[O::PER][O::PER] = {};
+        if (s.valid > 0) {
+            const O a{static_cast<const float*>(p.A) + (long long)s.begin * p.lda + m0, p.lda, p.M - m0, vec.a};
+            const O b{static_cast<const float*>(p.B) + (long long)s.begin * p.ldb + n0, p.ldb, p.N - n0, vec.b};
+            tile_product<kStages<TT>>(a, b, s.valid, smem, acc);
+        }
+        store_tile<O, O>(static_cast<float*>(p.D) + e * p.sd + (long long)m0 * p.ldd + n0, p.ldd, p.M - m0, p.M - m0,
+                             p.N - n0, acc);
     }
 }
 
 // A persistent launch; the kernel's shared memory is set up on the first call of a device.
 template <typename P>
-cudaError_t launch(void (*k)(const P), const P& p, int smem, std::atomic<bool> (&ready)[64], long long tiles, int most,
-                   cudaStream_t s)
+cudaError_t launch(void (*k)(const P, const Vec), const P& p, const Vec& vec, int smem, std::atomic<bool> (&ready)[64],
+                   long long tiles, int most, cudaStream_t s)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -207,25 +222,31 @@ cudaError_t launch(void (*k)(const P), const P& p, int smem, std::atomic<bool> (
         if (e != cudaSuccess) return e;
         if (dev < 64) ready[dev].store(true, std::memory_order_release);
     }
-    k<<<(unsigned)(tiles < most ? (tiles > 0 ? tiles : 1) : most), kThreads, smem, s>>>(p);
+    k<<<(unsigned)(tiles < most ? (tiles > 0 ? tiles : 1) : most), kThreads, smem, s>>>(p, vec);
     return cudaGetLastError();
 }
 
-template <int TT, bool W_NK>
+template <int TM, int TT, bool W_NK>
 cudaError_t rows_simt(const GroupedRows& p, int num_sms, cudaStream_t s)
 {
     static std::atomic<bool> ready[64];
-    const long long tiles = row_tiles_bound(p.g.rows, p.g.E, TT) * ((p.N + TT - 1) / TT);
-    return launch(grouped_rows_kernel<TT, TT, W_NK>, p, kStageBytes<TT, TT> + (int)sizeof(SegmentTable), ready, tiles,
-                  num_sms * (TT == 128 ? 2 : 3), s);
+    constexpr int smem = kStages<TM> * stage_values<Operand<TM, true>, Operand<TT, W_NK>>() * 4 + (int)sizeof(SegmentTable);
+    const long long tiles = row_tiles_bound(p.g.rows, p.g.E, TM) * ((p.N + TT - 1) / TT);
+    return launch(grouped_rows_kernel<TM, TT, W_NK>, p, Vec{vectors(p.X, p.ldx, 0), vectors(p.W, p.ldw, p.sw)}, smem, ready,
+                  tiles, num_sms * (TT == 128 ? 1 : 2), s);
 }
 template <int TT>
 cudaError_t wgrad_simt(const GroupedWgrad& p, int num_sms, cudaStream_t s)
 {
     static std::atomic<bool> ready[64];
+    constexpr int smem = kStages<TT> * stage_values<Operand<TT, false>, Operand<TT, false>>() * 4;
     const long long tiles = (long long)p.g.E * ((p.M + TT - 1) / TT) * ((p.N + TT - 1) / TT);
-    return launch(grouped_wgrad_kernel<TT, TT>, p, kStageBytes<TT, TT>, ready, tiles, num_sms * (TT == 128 ? 2 : 3), s);
+    return launch(grouped_wgrad_kernel<TT>, p, Vec{vectors(p.A, p.lda, 0), vectors(p.B, p.ldb, 0)}, smem, ready, tiles,
+                  num_sms * (TT == 128 ? 1 : 2), s);
 }
+// Rows an expert has on average below which a tile has 16 of them (one row of 8192 x 8192:
+// 289 us with 64).
+constexpr long long kFewRows = 32;
 // Whether tiles of 128 x 128 are at least four for each SM.
 bool large_tiles(long long by_m, int n, int num_sms) { return by_m * ((n + 127) / 128) >= 4ll * num_sms; }
 
@@ -233,9 +254,11 @@ bool large_tiles(long long by_m, int n, int num_sms) { return by_m * ((n + 127) 
 
 cudaError_t launch_grouped_rows_simt(const GroupedRows& p, int num_sms, cudaStream_t s)
 {
+    if (p.g.rows / p.g.E < kFewRows)
+        return p.w_nk ? rows_simt<16, 64, true>(p, num_sms, s) : rows_simt<16, 64, false>(p, num_sms, s);
     if (large_tiles(p.g.rows / 128, p.N, num_sms))
-        return p.w_nk ? rows_simt<128, true>(p, num_sms, s) : rows_simt<128, false>(p, num_sms, s);
-    return p.w_nk ? rows_simt<64, true>(p, num_sms, s) : rows_simt<64, false>(p, num_sms, s);
+        return p.w_nk ? rows_simt<128, 128, true>(p, num_sms, s) : rows_simt<128, 128, false>(p, num_sms, s);
+    return p.w_nk ? rows_simt<64, 64, true>(p, num_sms, s) : rows_simt<64, 64, false>(p, num_sms, s);
 }
 cudaError_t launch_grouped_wgrad_simt(const GroupedWgrad& p, int num_sms, cudaStream_t s)
 {
