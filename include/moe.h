@@ -582,6 +582,8 @@ moe_status_t moe_clip_grad_norm(int count, const moe_grad_t* list, float max_nor
  *     as zeros; rows past the last segment are neither read nor written;
  *   - each value depends on its own row (or expert) alone: infinities and NaN
  *     elsewhere do not reach it;
+ *   - an output overlaps no input and no other output (the same pointer is
+ *     INVALID_ARG);
  *   - row strides (ld*) count elements and are at least a row's values, in any
  *     alignment for moe_grouped_*: operands whose pointer and strides are
  *     multiples of 16 bytes are read by TMA, others by loads that cost more.
@@ -653,7 +655,8 @@ moe_status_t moe_quantize_rows(long long rows, int K, int dtype, const void* x, 
 
 /* Synchronise `stream`, then say whether a device-side wait of the products above ran
  * out on the current device since the last such call (MOE_ERR_DEVICE_TIMEOUT: their
- * outputs since then cannot be used), as moe_read_status does for the layer. */
+ * outputs since then cannot be used), as moe_read_status does for the layer. Not for
+ * streams under capture. */
 moe_status_t moe_products_status(moe_stream_t stream);
 
 /* MOE_ABI_VERSION of the loaded library. */

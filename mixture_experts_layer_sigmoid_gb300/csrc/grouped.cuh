@@ -65,8 +65,10 @@ __device__ __forceinline__ void read_segments(const Groups& g, SegmentTable* tab
                 const int u = __shfl_up_sync(0xffffffffu, v, off);
                 if ((int)threadIdx.x >= off) v += u;
             }
-            if (e < g.E) pre[e + 1] = carry + v;
-            carry += __shfl_sync(0xffffffffu, v, 31);
+            // (segments of a valid index are no more tiles than an int counts; others may overlap)
+            const int most = 0x7fffffff - carry;
+            if (e < g.E) pre[e + 1] = carry + min(v, most);
+            carry += min(__shfl_sync(0xffffffffu, v, 31), most);
         }
     }
     __syncthreads();

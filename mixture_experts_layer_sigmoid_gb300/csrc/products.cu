@@ -4,7 +4,8 @@
 // Row codes: a thread holds sixteen consecutive values (32 or 64 bytes in, 16 out), eight
 // neighbours share a block of 128 and its largest magnitude. Bound by HBM, with the
 // instructions close behind: with eight values a thread, the block's division and shuffles
-// came twice as often (139264 rows of 4096 bf16 349 us).
+// came twice as often (139264 rows of 4096 bf16 349 us; 278 now). More pieces of a thread in
+// flight cost blocks of an SM: two 311 us, four 475; 8 waves of blocks instead of 16 315.
 #include "grouped_tc.cuh"
 #include "mx.cuh"
 #include "rowvec.cuh"
@@ -12,7 +13,7 @@
 namespace moe {
 namespace {
 
-constexpr int kQThreads = 256, kPieces = 2, kPer = 16;
+constexpr int kQThreads = 256, kPer = 16;
 // Scales from which the corrected product's codes are those of a division (norm.cu has
 // the reason, and the test that walks the pairs).
 constexpr float kRowQuotientMin = 0x1p-92f;
@@ -53,42 +54,32 @@ quantize_rows_kernel(const T* __restrict__ x, long long ldx, uint8_t* codes, lon
         rows = n < 0 ? 0u : (unsigned)(n < (long long)rows ? n : (long long)rows);
     }
     const unsigned total = rows * per_row.d;               // below 2^31: the host cuts the rows
-    for (unsigned base = blockIdx.x * (kQThreads * kPieces) + threadIdx.x; base - threadIdx.x < total;
-         base += gridDim.x * (kQThreads * kPieces)) {
-        float v[kPieces][kPer];
-        unsigned r[kPieces], c[kPieces];
+    for (unsigned at = blockIdx.x * kQThreads + threadIdx.x; at - threadIdx.x < total; at += gridDim.x * kQThreads) {
+        const unsigned r = per_row(at), c = (at - r * per_row.d) * kPer;
+        float v[kPer];
+        if (at < total) {
+            load16(x + (long long)r * ldx + c, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const unsigned at = base + i * kQThreads;
-            r[i] = per_row(at);
-            c[i] = (at - r[i] * per_row.d) * kPer;
-            if (at < total) {
-                load16(x + (long long)r[i] * ldx + c[i], v[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) v[i][j] = 0.f;
-            }
+            for (int j = 0; j < kPer; ++j) v[j] = 0.f;
         }
+        float a = max_abs(v);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            float a = max_abs(v[i]);
+        for (int off = 4; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        if (at >= total) continue;                         // the eight lanes of a block alike
+        const float t = __fdiv_rn(a, 448.f);
+        const float s = t == 0.f ? 1.f : t;
+        if (s >= kRowQuotientMin && s < 0x1p100f) {
+            divide_vec(v, s, __frcp_rn(s));
+        } else {                                           // the remainder could underflow
 #pragma unroll
-            for (int off = 4; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-            if (base + i * kQThreads >= total) continue;   // the eight lanes of a block alike
-            const float t = __fdiv_rn(a, 448.f);
-            const float s = t == 0.f ? 1.f : t;
-            if (s >= kRowQuotientMin && s < 0x1p100f) {
-                divide_vec(v[i], s, __frcp_rn(s));
-            } else {                                       // the remainder could underflow
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) v[i][j] = __fdiv_rn(v[i][j], s);
-            }
-            if (c[i] % 128 == 0) scales[(long long)r[i] * lds + c[i] / 128] = s;
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = e4m3x4(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3]);
-            *reinterpret_cast<uint4*>(codes + (long long)r[i] * ldc + c[i]) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < kPer; ++j) v[j] = __fdiv_rn(v[j], s);
         }
+        if (c % 128 == 0) scales[(long long)r * lds + c / 128] = s;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = e4m3x4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        *reinterpret_cast<uint4*>(codes + (long long)r * ldc + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -100,7 +91,7 @@ cudaError_t quantize_rows(long long rows, int K, const void* x, long long ldx, u
     const long long slab = (1ll << 30) / per_row.d;        // rows whose pieces 32 bits count
     for (long long r = 0; r < rows; r += slab) {
         const long long n = rows - r < slab ? rows - r : slab;
-        const long long blocks = (n * per_row.d + kQThreads * kPieces - 1) / (kQThreads * kPieces);
+        const long long blocks = (n * per_row.d + kQThreads - 1) / kQThreads;
         const unsigned grid = (unsigned)(blocks < num_sms * 16ll ? blocks : num_sms * 16ll);
         quantize_rows_kernel<T><<<grid, kQThreads, 0, s>>>(static_cast<const T*>(x) + r * ldx, ldx, codes + r * ldc, ldc,
                                                            scales + r * lds, lds, (unsigned)n, per_row, r, in_use);
@@ -159,6 +150,7 @@ moe_status_t moe_grouped_matmul(const moe_groups_t* groups, int K, int N, const 
         return MOE_ERR_INVALID_ARG;
     if (!is_aligned16(X) || !is_aligned16(W) || !is_aligned16(Y)) return MOE_ERR_MISALIGNED;
     if (groups->rows == 0) return MOE_OK;
+    if (Y == X || Y == W) return MOE_ERR_INVALID_ARG;
     p.K = K; p.N = N;
     p.X = X; p.ldx = ldx;
     p.W = W; p.ldw = ldw; p.sw = groups->E > 1 ? sw : 0; p.w_nk = w_nk;
@@ -180,6 +172,7 @@ moe_status_t moe_grouped_wgrad(const moe_groups_t* groups, int M, int N, const v
         !stride_ok(ldb, N) || !stride_ok(ldd, N) || !block_ok(sd, groups->E, M, ldd, N))
         return MOE_ERR_INVALID_ARG;
     if (!is_aligned16(A) || !is_aligned16(B) || !is_aligned16(D)) return MOE_ERR_MISALIGNED;
+    if (D == A || D == B) return MOE_ERR_INVALID_ARG;
     p.M = M; p.N = N;
     p.A = A; p.lda = lda;
     p.B = B; p.ldb = ldb;
@@ -209,6 +202,7 @@ moe_status_t moe_fp8_matmul(const moe_groups_t* groups, int K, int N, const moe_
         a.lda % 16 || a.ldb % 16 || (groups->E > 1 && a.sb % 16))
         return MOE_ERR_MISALIGNED;
     if (groups->rows == 0) return MOE_OK;
+    if (a.Y == a.A || a.Y == a.SA || a.Y == a.B || a.Y == a.SB) return MOE_ERR_INVALID_ARG;
     p.K = K; p.N = N; p.dtype = groups->dtype;
     p.a = a;
     if (groups->E == 1) p.a.sb = p.a.ssb = 0;
@@ -229,6 +223,7 @@ moe_status_t moe_quantize_rows(long long rows, int K, int dtype, const void* x, 
         (reinterpret_cast<uintptr_t>(in_use) & 3u))
         return MOE_ERR_MISALIGNED;
     if (rows == 0) return MOE_OK;
+    if (codes == x || static_cast<const void*>(scales) == x || reinterpret_cast<uint8_t*>(scales) == codes) return MOE_ERR_INVALID_ARG;
     int sms = 0;
     if (!current_sms(&sms)) return MOE_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

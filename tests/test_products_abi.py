@@ -8,7 +8,8 @@ import torch
 import mixture_experts_layer_sigmoid_gb300 as moe
 from mixture_experts_layer_sigmoid_gb300 import _build, operators
 
-P = 4096          # an aligned address that nothing dereferences
+P = 4096          # aligned addresses that nothing dereferences
+Q, R = 8192, 12288
 ARG, ALIGN = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_MISALIGNED
 BIG = (1 << 20) + 1
 
@@ -29,19 +30,19 @@ BAD_GROUPS = [(dict(E=0), ARG), (dict(E=1025), ARG), (dict(dtype=2), ARG), (dict
 
 
 def rows_call(lib, g=None, **kw):
-    c = dict(K=64, N=32, X=P, ldx=64, W=P, ldw=32, sw=64 * 32, w_nk=0, Y=P, ldy=32)
+    c = dict(K=64, N=32, X=P, ldx=64, W=Q, ldw=32, sw=64 * 32, w_nk=0, Y=R, ldy=32)
     c.update(kw)
     return lib.moe_grouped_matmul(ctypes.byref(g or groups()), *c.values(), None)
 
 
 def wgrad_call(lib, g=None, **kw):
-    c = dict(M=64, N=32, A=P, lda=64, B=P, ldb=32, D=P, ldd=32, sd=64 * 32)
+    c = dict(M=64, N=32, A=P, lda=64, B=Q, ldb=32, D=R, ldd=32, sd=64 * 32)
     c.update(kw)
     return lib.moe_grouped_wgrad(ctypes.byref(g or groups()), *c.values(), None)
 
 
 def fp8_call(lib, g=None, K=256, N=64, **kw):
-    a = moe.moe_fp8_matmul_args_t(**{**dict(A=P, lda=256, SA=P, ldsa=2, B=P, ldb=64, sb=256 * 64, SB=P, ldsb=1, ssb=2, b_nk=0, Y=P,
+    a = moe.moe_fp8_matmul_args_t(**{**dict(A=P, lda=256, SA=Q, ldsa=2, B=P, ldb=64, sb=256 * 64, SB=Q, ldsb=1, ssb=2, b_nk=0, Y=R,
                                             ldy=64), **kw})
     return lib.moe_fp8_matmul(ctypes.byref(g or groups()), K, N, ctypes.byref(a), None)
 
@@ -63,7 +64,8 @@ def test_null_arguments(lib):
     (dict(K=0), ARG), (dict(N=0), ARG), (dict(K=BIG, ldx=BIG), ARG), (dict(N=BIG, ldw=BIG, ldy=BIG), ARG), (dict(X=None), ARG),
     (dict(W=None), ARG), (dict(Y=None), ARG), (dict(ldx=63), ARG), (dict(ldy=31), ARG), (dict(ldw=31), ARG), (dict(ldx=-64), ARG),
     (dict(w_nk=1), ARG), (dict(w_nk=2), ARG), (dict(w_nk=-1), ARG), (dict(sw=64 * 32 - 1), ARG), (dict(sw=0), ARG),
-    (dict(ldx=1 << 50), ARG), (dict(sw=1 << 50), ARG), (dict(X=P + 2), ALIGN), (dict(W=P + 8), ALIGN), (dict(Y=P + 4), ALIGN)])
+    (dict(ldx=1 << 50), ARG), (dict(sw=1 << 50), ARG), (dict(X=P + 2), ALIGN), (dict(W=P + 8), ALIGN), (dict(Y=P + 4), ALIGN), (dict(Y=P), ARG),
+    (dict(Y=Q), ARG)])
 def test_grouped_matmul_refuses(lib, change, want):
     assert rows_call(lib, **change) == want
 
@@ -71,7 +73,7 @@ def test_grouped_matmul_refuses(lib, change, want):
 @pytest.mark.parametrize("change,want", [
     (dict(M=0), ARG), (dict(N=-1), ARG), (dict(M=BIG, lda=BIG), ARG), (dict(A=None), ARG), (dict(B=None), ARG), (dict(D=None), ARG),
     (dict(lda=63), ARG), (dict(ldb=31), ARG), (dict(ldd=31), ARG), (dict(sd=64 * 32 - 1), ARG), (dict(A=P + 2), ALIGN),
-    (dict(B=P + 2), ALIGN), (dict(D=P + 2), ALIGN)])
+    (dict(B=P + 2), ALIGN), (dict(D=P + 2), ALIGN), (dict(D=P), ARG), (dict(D=Q), ARG)])
 def test_grouped_wgrad_refuses(lib, change, want):
     assert wgrad_call(lib, **change) == want
 
@@ -81,7 +83,7 @@ def test_grouped_wgrad_refuses(lib, change, want):
     (dict(SB=None), ARG), (dict(Y=None), ARG), (dict(lda=240), ARG), (dict(ldsa=1), ARG), (dict(ldb=48), ARG), (dict(ldsb=0), ARG),
     (dict(ldy=63), ARG), (dict(sb=16), ARG), (dict(ssb=1), ARG), (dict(b_nk=1), ARG), (dict(b_nk=3), ARG), (dict(A=P + 8), ALIGN),
     (dict(SA=P + 4), ALIGN), (dict(B=P + 1), ALIGN), (dict(SB=P + 4), ALIGN), (dict(Y=P + 2), ALIGN), (dict(lda=257), ALIGN),
-    (dict(ldb=72, sb=256 * 72), ALIGN), (dict(sb=256 * 64 + 8), ALIGN)])
+    (dict(ldb=72, sb=256 * 72), ALIGN), (dict(sb=256 * 64 + 8), ALIGN), (dict(Y=P), ARG), (dict(Y=Q), ARG)])
 def test_fp8_matmul_refuses(lib, change, want):
     assert fp8_call(lib, **change) == want
 
@@ -90,9 +92,9 @@ def test_fp8_matmul_refuses(lib, change, want):
     (dict(rows=-1), ARG), (dict(rows=2 ** 31 - 1), ARG), (dict(K=0), ARG), (dict(K=100), ARG), (dict(dtype=2), ARG), (dict(x=None), ARG),
     (dict(codes=None), ARG), (dict(scales=None), ARG), (dict(ldx=255), ARG), (dict(ldc=128), ARG), (dict(lds=1), ARG),
     (dict(x=P + 2), ALIGN), (dict(codes=P + 8), ALIGN), (dict(scales=P + 4), ALIGN), (dict(ldx=257), ALIGN), (dict(ldc=264), ALIGN),
-    (dict(in_use=P + 2), ALIGN)])
+    (dict(in_use=P + 2), ALIGN), (dict(codes=P), ARG), (dict(scales=P), ARG), (dict(scales=Q), ARG)])
 def test_quantize_rows_refuses(lib, change, want):
-    c = dict(rows=4, K=256, dtype=1, x=P, ldx=256, codes=P, ldc=256, scales=P, lds=2, in_use=None)
+    c = dict(rows=4, K=256, dtype=1, x=P, ldx=256, codes=Q, ldc=256, scales=R, lds=2, in_use=None)
     c.update(change)
     assert lib.moe_quantize_rows(*c.values(), None) == want
 

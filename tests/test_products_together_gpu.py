@@ -209,3 +209,29 @@ def test_many_tokens_decoded_one_by_one_match_the_batch():
         one = moe.sort_index(topk[t:t + 1].clone(), m.E)
         y = moe.unsort_rows(moe.grouped_matmul(moe.sort_rows(n[t:t + 1], one), m.p["A"], one), one, gates[t:t + 1].clone())
         assert torch.equal(y[0], whole[t])               # a row's sum does not depend on its neighbours
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+def test_gradients_without_rows(dtype, layout):
+    """An empty batch: zero weight gradients, and nothing else to write."""
+    w = torch.randn((3, 64, 40) if layout == "kn" else (3, 40, 64), device="cuda").to(dtype)
+    w = w if layout == "kn" else w.transpose(1, 2)
+    ix = dict(offsets=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    x, dy = torch.empty((0, 64), dtype=dtype, device="cuda"), torch.empty((0, 40), dtype=dtype, device="cuda")
+    dx, dw = moe.grouped_matmul_backward(dy, x, w, ix, dw=torch.full_like(w, float("nan")))
+    assert dx.shape == (0, 64) and bool((dw == 0).all())
+
+
+def test_one_expert_needs_no_index():
+    x, w = torch.randn((77, 136), device="cuda").to(BF), torch.randn((1, 136, 200), device="cuda").to(BF)
+    ix = dict(offsets=torch.tensor([0, 77], dtype=torch.int32, device="cuda"))
+    assert torch.equal(moe.grouped_matmul(x, w, None), moe.grouped_matmul(x, w, ix))
+
+
+def test_outputs_and_inputs_at_one_address_are_refused():
+    x, w = torch.randn((8, 64), device="cuda"), torch.randn((1, 64, 64), device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.grouped_matmul(x, w, None, out=x)
+    with pytest.raises(moe.MoEError):
+        moe.grouped_matmul(x, w, None, out=w[0][:8])
