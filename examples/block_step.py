@@ -106,16 +106,18 @@ class Blocks:
         Y = moe.grouped_matmul(moe.grouped_matmul(X, self.p["A"], ix).relu().square(), self.p["B"], ix)
         return moe.unsort_rows(Y, ix, gates, n["h"]), n["codes"], n["scales"]
 
-    def decode_8bit(self, x):
-        """The same tokens through experts whose weights are kept as E4M3 codes."""
-        if not hasattr(self, "codes"):
-            self.codes = {n: moe.quantize_tiles(self.p[n]) for n in ("A", "B")}
+    def codes(self):
+        """Block 2's weights as they are now, as E4M3 codes and scales of 128 x 128 tiles."""
+        return {n: moe.quantize_tiles(self.p[n]) for n in ("A", "B")}
+
+    def decode_8bit(self, x, codes):
+        """Tokens through block 2 with the experts' weights in these codes."""
         n = moe.add_rms_norm(x, self.p["n2"], torch.zeros_like(x))
         topk, gates = self.route(n["y"], self.p["Wr2"])
         ix = moe.sort_index(topk, self.E)
         X = moe.quantize_rows(moe.sort_rows(n["y"], ix), ix)
-        R = moe.quantize_rows(moe.fp8_matmul(*X, *self.codes["A"], ix).relu().square(), ix)
-        return moe.unsort_rows(moe.fp8_matmul(*R, *self.codes["B"], ix), ix, gates, n["h"])
+        R = moe.quantize_rows(moe.fp8_matmul(*X, *codes["A"], ix).relu().square(), ix)
+        return moe.unsort_rows(moe.fp8_matmul(*R, *codes["B"], ix), ix, gates, n["h"])
 
 
 def main():
@@ -131,7 +133,7 @@ def main():
         print(f"step {i}: loss {loss.item():.4f}, gradient norm {norm.item():.4f}")
     y, codes, scales = m.decode(x[:1])
     print(f"decoded one token: |y| {y.float().norm().item():.3f}, {codes.numel()} codes, {scales.numel()} scale bytes")
-    y8 = m.decode_8bit(x[:1])
+    y8 = m.decode_8bit(x[:1], m.codes())
     print(f"with 8-bit experts: |y| {y8.float().norm().item():.3f}")
 
 

@@ -1,5 +1,5 @@
 // grouped.cuh -- segments of rows sorted by expert, as the products over them see
-// them (grouped_simt.cu, grouped_tc.cu, matmul_fp8.cu): the rows of each expert and
+// them (grouped_simt.cu, grouped_tc.cuh, matmul_fp8.cu): the rows of each expert and
 // the list of row tiles, read on the device, so that no call waits for the routing.
 #pragma once
 #include "internal.h"

@@ -16,7 +16,6 @@
 // on the device. Tiles of 128 need half of the reads of shared memory; tiles of 64 are taken
 // while the larger ones are fewer than four for each SM.
 #include "grouped.cuh"
-#include "epilogue.cuh"
 
 #include <atomic>
 

@@ -16,7 +16,6 @@
 //     in flight); loop bounds and addresses of the fold are made uniform by a shuffle, and its
 //     waits are bare (spin): each kept the compiler from copying sums in the loop.
 #include "grouped_tc.cuh"
-#include "epilogue.cuh"
 
 namespace moe {
 namespace {
@@ -25,6 +24,7 @@ using namespace gtc;
 
 constexpr int QK = 128;                        // depth of a block, and of a scale
 constexpr int kThreads8 = 384;
+constexpr int kRegs = (128 * 88 + 256 * 208) / kThreads8;   // a thread's at the launch
 constexpr int kFirst = 4;                      // first folding warp
 constexpr int kGroup = 4;                      // blocks whose scales are copied together
 constexpr int kSlots = 6;                      // groups of them in shared memory
@@ -132,7 +132,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
         return ptx::wait_bounded(bar, parity, &abort_flag, status, where);
     };
 
-    // 384 threads x 168 registers at the launch = 128 x 88 + 256 x 208
+    // 384 threads x 168 registers at the launch (the host looks) = 128 x 88 + 256 x 208
     if (warp < kFirst) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
@@ -365,6 +365,13 @@ cudaError_t fp8_rows(const Fp8Rows& in, int num_sms, cudaStream_t s)
     auto k = fp8_kernel<T, B_MN>;
     static std::atomic<int> slots[64];
     int n = 0;
+    // a build with fewer registers would leave setmaxnreg waiting
+    static const cudaError_t registers = [k] {
+        cudaFuncAttributes at{};
+        const cudaError_t e = cudaFuncGetAttributes(&at, k);
+        return e != cudaSuccess || at.numRegs >= kRegs ? e : cudaErrorInvalidKernelImage;
+    }();
+    if (registers != cudaSuccess) return registers;
     const cudaError_t e = units_at_once(reinterpret_cast<const void*>(k), kThreads8, SMEM8, false, num_sms, slots, &n);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)(units < n ? units : n), kThreads8, SMEM8, s>>>(mA, mB, p);

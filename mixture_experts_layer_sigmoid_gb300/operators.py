@@ -3,8 +3,9 @@
 Torch allocates outputs and scratch and supplies the current stream of the
 tensors' device; every value is computed by the kernels behind include/moe.h
 (``moe_add_rms_norm``, ``moe_sort_*``, ``moe_unsort_*``, ``moe_clip_grad_norm``,
-``moe_grouped_*``, ``moe_fp8_matmul``, ``moe_quantize_rows``), whose entries describe the mathematics, the limits and the errors. Activations
-are fp32 or bf16 matrices whose last dimension is contiguous (any row stride).
+``moe_grouped_*``, ``moe_fp8_matmul``, ``moe_quantize_rows``), whose entries
+describe the mathematics, the limits and the errors. Activations are fp32 or bf16
+matrices whose last dimension is contiguous (any row stride).
 Wrong devices, types and shapes raise ValueError here; what the library
 refuses raises MoEError.
 """
@@ -388,7 +389,8 @@ def grouped_matmul_backward(dY, rows, w, index, *, want_drows: bool = True, want
     """Gradients of grouped_matmul (moe_grouped_matmul, moe_grouped_wgrad):
     ``(drows, dw)``, ``drows[r] = dY[r] @ w[e].T`` with rows outside the segments
     as there, and ``dw[e]`` the sum of its rows' ``rows[r].T @ dY[r]``, zeros for
-    an expert without rows, laid out as ``w``. ``drows`` and ``dw`` may be given.
+    an expert without rows, laid out as ``w``. ``drows`` and ``dw`` may be given
+    (apart from each other and from what the call reads).
     ``rows`` is only read for dw, ``w`` only for drows (then its shape and strides
     still say dw's)."""
     lib = _load()
@@ -402,6 +404,10 @@ def grouped_matmul_backward(dY, rows, w, index, *, want_drows: bool = True, want
         raise ValueError(f"w: {K} x {Nw} for gradients of {N}")
     ldx = _act(rows, "rows", (R, K), dY)
     g = _groups(index, R, E, dY.dtype, dev)
+    if want_drows and want_dw:           # drows is written first; the library sees one product at a time
+        for out, name, others in ((drows, "drows", (rows, dw)), (dw, "dw", (w, drows))):
+            if out is not None and R > 0 and any(o is not None and o.data_ptr() == out.data_ptr() for o in others):
+                raise ValueError(f"{name}: at the address of another tensor of the call")
     if want_drows:
         drows, ldd = _rows_out(drows, "drows", R, K, dY, dY.dtype)
         _call("moe_grouped_matmul", dev, lib.moe_grouped_matmul, ctypes.byref(g), N, K, dY.data_ptr(), lddy, w.data_ptr(),

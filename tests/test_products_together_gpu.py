@@ -178,10 +178,11 @@ def test_two_graphs_replayed_in_turns():
 def test_8bit_experts_decode_what_their_codes_say():
     m = Blocks(T=64, H=256, E=8, F=128, k=2)
     x = torch.randn((5, 256), device="cuda").to(m.dtype)
-    y = m.decode_8bit(x)
+    codes = m.codes()
+    y = m.decode_8bit(x, codes)
     n = moe.add_rms_norm(x, m.p["n2"], torch.zeros_like(x))
     topk, gates = m.route(n["y"], m.p["Wr2"])
-    A, B = (tile_values8(*m.codes[c]) for c in "AB")
+    A, B = (tile_values8(*codes[c]) for c in "AB")
     xv = values8(*moe.quantize_rows(n["y"]))
     for t in range(5):
         out = n["h"][t].double()
@@ -235,3 +236,29 @@ def test_outputs_and_inputs_at_one_address_are_refused():
         moe.grouped_matmul(x, w, None, out=x)
     with pytest.raises(moe.MoEError):
         moe.grouped_matmul(x, w, None, out=w[0][:8])
+
+
+def test_gradients_written_over_their_inputs_are_refused():
+    """drows is written before dw reads the rows, and dw may not be the weights."""
+    x, dy, w = (torch.randn(s, device="cuda") for s in ((8, 64), (8, 64), (1, 64, 64)))
+    for kw in (dict(drows=x), dict(drows=dy), dict(dw=w)):
+        with pytest.raises((moe.MoEError, ValueError)):
+            moe.grouped_matmul_backward(dy, x, w, None, **kw)
+    both = torch.empty((64, 64), device="cuda")
+    with pytest.raises(ValueError):
+        moe.grouped_matmul_backward(dy, x, w, None, drows=both[:8], dw=both[None])
+    dx, _ = moe.grouped_matmul_backward(dy, x, w, None, want_dw=False, drows=x)   # nothing reads the rows
+    assert dx is x
+
+
+def test_eight_bit_decoding_follows_the_weights():
+    m = Blocks(T=64, H=256, E=8, F=128, k=2)
+    x = torch.randn((3, 256), device="cuda").to(m.dtype)
+    before = m.decode_8bit(x, m.codes())
+    m.p["B"].mul_(-1)
+    h = moe.add_rms_norm(x, m.p["n2"], torch.zeros_like(x))["h"].float()
+    after = m.decode_8bit(x, m.codes())
+    # the experts' part changes its sign; each output is rounded once
+    slack = 2.0 ** -8 * (before.float().abs() + after.float().abs()) + 1e-6
+    assert bool((((before.float() - h) + (after.float() - h)).abs() <= slack).all())
+    assert not torch.equal(before, after)
