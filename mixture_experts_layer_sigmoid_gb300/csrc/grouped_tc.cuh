@@ -27,7 +27,9 @@
 //     to read: 16 stages of 8 KB of them in flight, and enough tiles for every SM. (The MMAs
 //     still take 128 rows, 250 cycles a block, less than HBM takes to bring it.)
 //   - GUARD: operands that TMA cannot take (strides off the 16-byte boundaries) are loaded by
-//     ten warps, as pairs of aligned 16-byte windows that are shifted, into the same layout.
+//     sixteen warps, as pairs of aligned 16-byte windows that are shifted, into the same layout
+//     (1777 x 3 rows of 1001 x 771 74 us; ten warps that worked out each address took 113, the
+//     second window as the neighbour's by a shuffle 78).
 #pragma once
 #include "grouped.cuh"
 #include "ptx.cuh"
@@ -80,7 +82,7 @@ struct Cfg {
 // Set by a wait that ran out (one word per translation unit and device).
 static __device__ DeviceStatus wait_status;
 
-constexpr int kLoaders = 320;                  // GUARD: loading threads
+constexpr int kLoaders = 512;                  // GUARD: loading threads, eight to a row of 64
 
 template <bool WGRAD, bool GUARD>
 constexpr int threads() { return GUARD ? 192 + kLoaders : (WGRAD ? 224 : 192); }
@@ -197,21 +199,19 @@ struct Work {
     }
 };
 
-// Eight bf16 values from any 2-byte aligned address, of which `n` exist, in two steps: the
-// aligned 16-byte windows that hold them, and the shift.
+// Eight bf16 values from an address `off` bytes behind a 16-byte boundary, of which `n` exist,
+// in two steps: the aligned 16-byte windows that hold them, and the shift.
 struct Windows { uint4 a, b; };
-__device__ __forceinline__ Windows load_windows(const __nv_bfloat16* p, int n)
+__device__ __forceinline__ Windows load_windows(const __nv_bfloat16* p, unsigned off, int n)
 {
     Windows w{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
     const uint4* base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
     if (n > 0) w.a = base[0];                           // holds the first value
     if (n > 0 && off + 2 * min(n, 8) > 16) w.b = base[1];   // holds the last one
     return w;
 }
-__device__ __forceinline__ uint4 shift_windows(const Windows& q, const __nv_bfloat16* p, int n)
+__device__ __forceinline__ uint4 shift_windows(const Windows& q, unsigned off, int n)
 {
-    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(p) & 15u);
     uint32_t w[8] = {q.a.x, q.a.y, q.a.z, q.a.w, q.b.x, q.b.y, q.b.z, q.b.w};
     if (off & 8u) {
 #pragma unroll
@@ -224,9 +224,11 @@ __device__ __forceinline__ uint4 shift_windows(const Windows& q, const __nv_bflo
     const unsigned sh = (off & 2u) * 8;
     uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r[i] = __funnelshift_r(w[i], w[i + 1], sh);
-        if (2 * i + 2 > n) r[i] = 2 * i + 1 > n ? 0u : r[i] & 0xFFFFu;
+    for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(w[i], w[i + 1], sh);
+    if (n > 0 && n < 8) {                               // (with none the windows are zeros)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * i + 2 > n) r[i] = 2 * i + 1 > n ? 0u : r[i] & 0xFFFFu;
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
@@ -503,64 +505,48 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         __syncwarp();
     } else if (GUARD && warp >= 6) {
         // ------------------------------------------- loads off the boundaries
-        const int tid = (int)threadIdx.x - 192, ch = tid & 7;
+        // The stage as rows of 128 bytes, A's (rows, or two stripes of 64) and then B's (columns,
+        // or stripes of 64), eight threads to a row. A thread's rows are 64 apart, in memory 64
+        // rows or 64 values: a multiple of 16 bytes, as is the way to the next block, so that the
+        // shift is the tile's. All six loads are under way before the stage is free.
+        const int tid = (int)threadIdx.x - 192, ch = tid & 7, r = tid >> 3;
+        const uint32_t place = (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
+        const long long ja = WGRAD ? 64 : 64 * a.lda, jb = B_MN ? 64 : 64 * a.ldb;
+        const long long ka = WGRAD ? 64 * a.lda : 64, kb_ = B_MN ? 64 * a.ldb : 64;
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
         for (long long w = unit0; ok && w < work.total; w += nunits) {
             const Tile t = work.at(a, table, w, rank);
-            const int n_cols = a.N - t.n0;
-            for (int kb = 0; kb < t.kblocks; ++kb) {
+            const int n_cols = a.N - t.n0, stripes = (t.nt + 63) / 64;
+            const __nv_bfloat16* pa = a.A + (long long)(t.row + r) * a.lda + t.m0 + ch * 8;
+            const __nv_bfloat16* pb = WGRAD ? a.B + (long long)(t.row + r) * a.ldb + t.n0 + ch * 8
+                                            : a.B + t.e * a.sb + (B_MN ? r * a.ldb + t.n0 : (long long)(t.n0 + r) * a.ldb) + ch * 8;
+            const unsigned offa = (unsigned)(reinterpret_cast<uintptr_t>(pa) & 15u);
+            const unsigned offb = (unsigned)(reinterpret_cast<uintptr_t>(pb) & 15u);
+            for (int kb = 0; kb < t.kblocks; ++kb, pa += ka, pb += kb_) {
+                const int left = WGRAD ? (kb == t.kblocks - 1 ? t.tail : BK) : a.K - kb * BK;
+                Windows q[6];
+                int n[6];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    n[j] = WGRAD ? (r < left ? a.M - t.m0 - 64 * j - ch * 8 : 0) : (r + 64 * j < t.valid ? left - ch * 8 : 0);
+                    q[j] = load_windows(pa + j * ja, offa, n[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int m = B_MN ? (r < left ? n_cols - 64 * j - ch * 8 : 0) : (r + 64 * j < n_cols ? left - ch * 8 : 0);
+                    n[2 + j] = j < stripes ? m : 0;
+                    q[2 + j] = load_windows(pb + j * jb, offb, n[2 + j]);
+                }
                 if (!__all_sync(0xffffffffu, wait(empty_bar(s), ph ^ 1u, 6))) { ok = false; break; }
-                const uint32_t dst = ring + s * C::STAGE;
-                // The stage as rows of 128 bytes: 128 of A (rows, or two stripes of 64), then B's
-                // (columns, or stripes of 64); eight threads to a row, five rows of a thread in
-                // flight.
-                const int k = kb * BK, total = BM + (B_MN ? (t.nt + 63) / 64 * 64 : t.nt);
-                const int n_k = WGRAD ? (kb == t.kblocks - 1 ? t.tail : BK) : a.K - k;
-                auto source = [&](int v, int& n) -> const __nv_bfloat16* {
-                    const bool is_a = v < BM;
-                    const int i = is_a ? v : v - BM;
-                    if constexpr (WGRAD) {
-                        const int col = (i & ~63) + ch * 8, r = i & 63;
-                        n = r < n_k ? (is_a ? a.M - t.m0 : n_cols) - col : 0;
-                        return is_a ? a.A + (long long)(t.row + k + r) * a.lda + t.m0 + col
-                                    : a.B + (long long)(t.row + k + r) * a.ldb + t.n0 + col;
-                    } else {
-                        const __nv_bfloat16* w = a.B + t.e * a.sb;
-                        if (is_a) {
-                            n = i < t.valid ? n_k - ch * 8 : 0;
-                            return a.A + (long long)(t.row + i) * a.lda + k + ch * 8;
-                        }
-                        if constexpr (B_MN) {
-                            const int col = (i & ~63) + ch * 8, r = i & 63;
-                            n = r < n_k ? n_cols - col : 0;
-                            return w + (long long)(k + r) * a.ldb + t.n0 + col;
-                        } else {
-                            n = i < n_cols ? n_k - ch * 8 : 0;
-                            return w + (long long)(t.n0 + i) * a.ldb + k + ch * 8;
-                        }
-                    }
-                };
-                for (int v0 = tid >> 3; v0 < total; v0 += 5 * (kLoaders / 8)) {
-                    Windows q[5];
+                const uint32_t dst = ring + s * C::STAGE + place;
 #pragma unroll
-                    for (int j = 0; j < 5; ++j) {
-                        const int v = v0 + j * (kLoaders / 8);
-                        int n = 0;
-                        const __nv_bfloat16* p = source(v, n);
-                        q[j] = load_windows(p, v < total ? n : 0);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 5; ++j) {
-                        const int v = v0 + j * (kLoaders / 8);
-                        int n = 0;
-                        const __nv_bfloat16* p = source(v, n);
-                        const uint4 x = shift_windows(q[j], p, n);
-                        if (v < total)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + v * 128 + ((ch ^ (v & 7)) << 4)),
-                                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
-                    }
+                for (int j = 0; j < 6; ++j) {
+                    if (j - 2 >= stripes) break;
+                    const uint4 x = shift_windows(q[j], j < 2 ? offa : offb, n[j]);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + j * STRIPE), "r"(x.x), "r"(x.y),
+                                 "r"(x.z), "r"(x.w) : "memory");
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::mbar_arrive(full_bar(s));
