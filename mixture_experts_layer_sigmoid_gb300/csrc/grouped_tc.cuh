@@ -400,9 +400,8 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             }
         }
         __syncwarp();
-        // every MMA has completed before tensor memory is freed (the odd CTA's is written
-        // by its peer's MMAs)
-        if (lane == 0) {
+        // every MMA has completed before tensor memory is freed
+        if (rank == 0 && lane == 0) {
             volatile int never = 0;
             ptx::wait_bounded(final_bar, 0, &never, status, 4);
         }
@@ -585,6 +584,13 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
     if (PAIR) ptx::cluster_sync();             // both CTAs are done with tensor memory and signals
     else __syncthreads();
     if (warp == 1) {
+        // the odd CTA's tensor memory is written by its peer's MMAs, whose last signal is on its way
+        // here too (only now: a wait from the start on would have the whole kernel's time for a limit)
+        if (PAIR && rank == 1 && lane == 0) {
+            volatile int never = 0;
+            ptx::wait_bounded(final_bar, 0, &never, status, 8);
+        }
+        __syncwarp();
         ptx::tc_fence_after();
         if (PAIR) ptx::tmem_dealloc_pair(tmem, 2 * BN);
         else ptx::tmem_dealloc(tmem, 2 * BN);
