@@ -127,6 +127,10 @@ __device__ __forceinline__ void store_3d(const CUtensorMap* m, uint32_t src, int
                      reinterpret_cast<uint64_t>(m)), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
+// The limit of a wait for tiles of this many blocks in all, each up to some twenty times as long as
+// the slowest one takes (0.9 us): a weight gradient's only tile may hold 2^31 rows.
+__device__ __forceinline__ uint64_t limit_of(long long blocks) { return kWaitLimitNs + (uint64_t)blocks * 20000u; }
+
 // A tile of outputs, as every role of a block sees it.
 struct Tile {
     int e;
@@ -304,8 +308,8 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
     Work<WGRAD, MODE> work;
     work.init(a, table.pre);
     work.total = __shfl_sync(0xffffffffu, work.total, 0);
-    auto wait = [&](uint32_t bar, uint32_t parity, int where) {
-        return ptx::wait_bounded(bar, parity, &abort_flag, status, where);
+    auto wait = [&](uint32_t bar, uint32_t parity, int where, uint64_t limit = kWaitLimitNs) {
+        return ptx::wait_bounded(bar, parity, &abort_flag, status, where, limit);
     };
 
     if (warp == 0 && !GUARD) {
@@ -415,7 +419,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         for (long long w = unit0; w < work.total; w += nunits) {
             Tile t = work.at(a, table, w, rank);
             t.kblocks = __shfl_sync(0xffffffffu, t.kblocks, 0);
-            if (!__all_sync(0xffffffffu, wait(accf_bar(acc), aph, 5))) break;
+            if (!__all_sync(0xffffffffu, wait(accf_bar(acc), aph, 5, limit_of(t.kblocks)))) break;
             ptx::tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
             // this warp's rows and columns of the tile: with M = 256 (or 128 in one CTA) a lane is a
@@ -556,14 +560,17 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         // ------------------------------- the contraction's last, partial block
         int s0 = 0;
         uint32_t phases = 0;
+        long long blocks = 0;                  // since the last such block, outputs (64 a tile) among them
         for (long long w = unit0; w < work.total; w += nunits) {
             const Tile t = work.at(a, table, w, rank);
+            blocks += t.kblocks + 64;
             if (t.kblocks == 0) continue;
             const int s = (s0 + t.kblocks - 1) % S;
             s0 = (s0 + t.kblocks) % S;
             if (t.tail == BK) continue;
-            if (!__all_sync(0xffffffffu, wait(land_bar(s), (phases >> s) & 1u, 7))) break;
+            if (!__all_sync(0xffffffffu, wait(land_bar(s), (phases >> s) & 1u, 7, limit_of(blocks)))) break;
             phases ^= 1u << s;
+            blocks = 0;
             // the rows up to the next multiple of 16, in A's two stripes and in B's
             const int n = ((t.tail + 15) / 16 * 16 - t.tail) * 8;
             const int bcols = PAIR ? t.nt / 2 : t.nt, stripes = BM / 64 + (bcols + 63) / 64;

@@ -60,10 +60,11 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
 }
 
 // Wait until the phase with parity `parity` of `bar` has completed. Gives up
-// when another role of the CTA has aborted, or after kWaitLimitNs; on a
+// when another role of the CTA has aborted, or after limit_ns; on a
 // timeout it records MOE_ERR_DEVICE_TIMEOUT and raises the CTA's abort flag.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
-                                             volatile int* abort_flag, DeviceStatus* st, int where)
+                                             volatile int* abort_flag, DeviceStatus* st, int where,
+                                             uint64_t limit_ns = kWaitLimitNs)
 {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
@@ -71,7 +72,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 63u) == 0) {
             if (*abort_flag) return false;
-            if (globaltimer() - t0 > kWaitLimitNs) {
+            if (globaltimer() - t0 > limit_ns) {
                 *abort_flag = 1;
                 if (atomicCAS(&st->code, 0, (int)MOE_ERR_DEVICE_TIMEOUT) == 0) st->where = where;
                 return false;
