@@ -591,7 +591,7 @@ moe_status_t moe_clip_grad_norm(int count, const moe_grad_t* list, float max_nor
 typedef struct {
     int E;                   /* experts, 1..1024                               */
     int dtype;               /* MOE_FP32 or MOE_BF16                           */
-    long long rows;          /* rows of the row buffers, 0..2^31 - 2           */
+    long long rows;          /* rows of the row buffers, 0..2^31 - 1024        */
     const int32_t* offsets;  /* E + 1; NULL with E = 1: one segment, all rows  */
     const int32_t* counts;   /* E, or NULL                                     */
 } moe_groups_t;

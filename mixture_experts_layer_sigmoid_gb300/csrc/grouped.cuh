@@ -7,6 +7,9 @@
 namespace moe {
 
 constexpr int kMaxGroups = 1024;       // experts, as the sort's index has them
+// Rows: any of them plus a unit of tiles (256 rows and a quarter's 96 more) or a ring of blocks of
+// the contraction (8 x 32) is a row number in 32 bits, here and in a TMA coordinate.
+constexpr long long kMaxRows = (1ll << 31) - 1024;
 
 // The segments of one call. offsets null: one segment of all rows.
 struct Groups {

@@ -116,7 +116,7 @@ bool block_ok(long long stride, int E, int n_out, long long ld, int n_in)
 moe_status_t check_groups(const moe_groups_t* in, Groups* g)
 {
     if (!in || in->E < 1 || in->E > kMaxGroups || (in->dtype != MOE_FP32 && in->dtype != MOE_BF16) || in->rows < 0 ||
-        in->rows >= (1ll << 31) - 1 || (!in->offsets && (in->E != 1 || in->counts)))
+        in->rows > kMaxRows || (!in->offsets && (in->E != 1 || in->counts)))
         return MOE_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(in->offsets) | reinterpret_cast<uintptr_t>(in->counts)) & 3u)
         return MOE_ERR_MISALIGNED;
