@@ -385,7 +385,7 @@ moe_status_t moe_mx_quantize(int rows, int cols, const void* in, uint8_t* codes,
 moe_status_t moe_nv_quantize(int rows, int cols, const void* in, float* amax, uint8_t* codes, uint8_t* scales,
                              uint8_t* codes_t, uint8_t* scales_t, moe_stream_t stream);
 
-/* Failure-detection check. Every pipelined kernel of the library waits on
+/* Failure-detection check. Every pipelined kernel of the layer waits on
  * its shared-memory mbarriers with a bounded wait (2 s); when a wait runs out
  * the kernel records MOE_ERR_DEVICE_TIMEOUT in the status word and returns,
  * so a stalled pipeline ends with an error instead of hanging the GPU. This
@@ -658,6 +658,13 @@ moe_status_t moe_quantize_rows(long long rows, int K, int dtype, const void* x, 
  * outputs since then cannot be used), as moe_read_status does for the layer. Not for
  * streams under capture. */
 moe_status_t moe_products_status(moe_stream_t stream);
+
+/* Failure-detection check of the products, as moe_diag_wait_timeout is the layer's: runs the
+ * waits of their kernels on an mbarrier that is never signalled: one with a limit of 10 ms, one
+ * with the usual limit that the first one's abort flag ends, and one of 4000 tries. which: the row products' status word
+ * (0), the weight gradients' (1) or the 8-bit products' (2). moe_products_status then returns
+ * MOE_ERR_DEVICE_TIMEOUT once, and the device stays usable. Errors: INVALID_ARG, CUDA. */
+moe_status_t moe_diag_products_wait(int which, moe_stream_t stream);
 
 /* MOE_ABI_VERSION of the loaded library. */
 int moe_abi_version(void);

@@ -40,7 +40,7 @@ EXPORTS = ("moe_plan_create", "moe_plan_destroy", "moe_workspace_size", "moe_for
            "moe_sort_rows_cap", "moe_sort_index", "moe_sort_rows", "moe_unsort_rows",
            "moe_unsort_rows_backward", "moe_clip_workspace_size", "moe_clip_grad_norm",
            "moe_grouped_matmul", "moe_grouped_wgrad", "moe_fp8_matmul", "moe_quantize_rows",
-           "moe_products_status", "moe_abi_version")
+           "moe_products_status", "moe_diag_products_wait", "moe_abi_version")
 MOE_Q_ROWS, MOE_Q_TILES, MOE_Q_COLS_T, MOE_Q_TILES_T = 0, 1, 2, 3
 
 
@@ -154,6 +154,7 @@ def load_library() -> ctypes.CDLL:
         lib.moe_fp8_matmul.argtypes = [P(moe_groups_t), i, i, P(moe_fp8_matmul_args_t), _vp]
         lib.moe_quantize_rows.argtypes = [ll, i, i, _vp, ll, _vp, ll, _vp, ll, _vp, _vp]
         lib.moe_products_status.argtypes = [_vp]
+        lib.moe_diag_products_wait.argtypes = [i, _vp]
         lib.moe_abi_version.argtypes = []
         for n in EXPORTS:
             if n not in ("moe_status_string", "moe_abi_version"):

@@ -5,7 +5,7 @@
 // b_e += rate * sign(mean load - load of e), compared exactly in integers.
 //
 // moe_diag_wait_timeout: exercises the device-side bounded wait
-// (ptx::wait_bounded) that every pipelined kernel of the library uses, on an
+// (ptx::wait_bounded) that every pipelined kernel of the layer uses, on an
 // mbarrier that nothing ever signals. The wait gives up after its limit and
 // records MOE_ERR_DEVICE_TIMEOUT in the status word, so a test can check
 // that a stalled pipeline ends with an error instead of hanging the GPU.

@@ -93,13 +93,33 @@ __device__ __forceinline__ bool elect_one()
     asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
     return p != 0;
 }
-// Waits for the phase with this parity, up to a number of tries, each of which the hardware
-// lets sleep a while (all of them are more than a tenth of a second). Nothing else stands in
-// the loop: with a look at the abort flag or the clock in it, the compiler's code around the
-// waits of matmul_fp8.cu's fold took 961 cycles a block instead of 711.
-__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity)
+// Waits for the phase with this parity as ptx::wait_bounded does, for the threads that issue MMAs:
+// gives up when another role of the block has raised the abort flag (at this address), or LIMIT_NS
+// after its first look at the clock; the caller raises the flag and records it. The looks come
+// between rounds of tries, and their outcome is voted on: a branch on it that the compiler cannot
+// prove uniform would take the MMAs behind it off the uniform datapath (four decoded tokens 97
+// instead of 62 us).
+template <uint64_t LIMIT_NS = kWaitLimitNs>
+__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, uint32_t abort_flag)
 {
-    for (int i = 0; i < (1 << 22); ++i)
+    uint64_t t0 = 0;
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+        uint32_t raised;
+        asm volatile("ld.volatile.shared::cta.u32 %0, [%1];" : "=r"(raised) : "r"(abort_flag) : "memory");
+        const uint64_t t = ptx::globaltimer();
+        if (t0 == 0) t0 = t;
+        if (__any_sync(__activemask(), raised != 0 || t - t0 > LIMIT_NS)) return false;
+    }
+}
+// The same with nothing but tries, for matmul_fp8.cu's fold: one on a barrier that nothing signals
+// takes 2.8 us here, all of them 3 s. With a look at the flag or the clock between them the
+// compiler copied the fold's sums (8192 x 7168 x 4096 codes 216 to 221 us instead of 195).
+template <int TRIES = 1 << 20>
+__device__ __forceinline__ bool spin_tries(uint32_t bar, uint32_t parity)
+{
+    for (int i = 0; i < TRIES; ++i)
         if (ptx::mbar_try_wait(bar, parity)) return true;
     return false;
 }
@@ -263,6 +283,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
     const uint32_t final_bar = bar0 + 8u * (3 * S + 4);
     uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem + C::SMEM - 1024 - 16);
     volatile int& abort_flag = *reinterpret_cast<volatile int*>(smem + C::SMEM - 1024 - 8);
+    const uint32_t flag = ring + C::SMEM - 1024 - 8;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)ptx::cluster_ctarank() : 0;
@@ -365,13 +386,13 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
             bool ok = true;
             for (long long w = unit0; ok && w < work.total; w += nunits) {
                 const Tile t = work.at(a, table, w, rank);
-                if (!spin(acce_bar(acc), aph ^ 1u)) { ok = false; break; }
+                if (!spin(acce_bar(acc), aph ^ 1u, flag)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * BN);
                 // (256 rows less 128 in the M / 16 field)
                 const uint32_t id = (IDESC | ((uint32_t)(t.nt >> 3) << 17)) - (t.half ? 8u << 24 : 0u);
                 for (int kb = 0; kb < t.kblocks; ++kb) {
-                    if (!spin(full_bar(s), ph)) { ok = false; break; }
+                    if (!spin(full_bar(s), ph, flag)) { ok = false; break; }
                     ptx::tc_fence_after();
                     const uint32_t pa = ring + s * C::STAGE, pb = pa + C::A_BYTES;
                     const int steps = WGRAD && kb == t.kblocks - 1 ? (t.tail + 15) / 16 : BK / 16;
@@ -645,8 +666,8 @@ inline cudaError_t units_at_once(const void* k, int threads, int smem, bool pair
     *out = n;
     return cudaSuccess;
 }
-// Waits for the stream and takes the word.
-inline cudaError_t take_status(int* code, cudaStream_t s)
+// Waits for the stream and takes this translation unit's word.
+static inline cudaError_t take_status(int* code, cudaStream_t s)
 {
     DeviceStatus h{};
     cudaError_t e = cudaMemcpyFromSymbolAsync(&h, wait_status, sizeof(h), 0, cudaMemcpyDeviceToHost, s);
@@ -658,6 +679,37 @@ inline cudaError_t take_status(int* code, cudaStream_t s)
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     }
     return e;
+}
+
+// A stalled pipeline in small, on a barrier that nothing signals: one thread's wait runs out after
+// 10 ms, raises the flag and records it in this translation unit's word; another's, of 2 s, ends
+// with the flag; a third's after 4000 tries.
+static __global__ void stalled_kernel()
+{
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int abort_flag;
+    const uint32_t b = ptx::smem_u32(&bar), flag = ptx::smem_u32(&abort_flag);
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(b, 1);
+        abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (!spin<10000000>(b, 0, flag)) {
+            *static_cast<volatile int*>(&abort_flag) = 1;
+            report_timeout(&wait_status, 98);
+        }
+    } else if (threadIdx.x == 32) {
+        spin(b, 0, flag);
+    } else if (threadIdx.x == 64) {
+        spin_tries<4000>(b, 0);
+    }
+}
+static inline cudaError_t launch_stalled(cudaStream_t s)
+{
+    stalled_kernel<<<1, 96, 0, s>>>();
+    return cudaGetLastError();
 }
 
 template <bool WGRAD, bool B_MN, Mode MODE, bool GUARD>
@@ -693,5 +745,9 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
 cudaError_t take_rows_status(int* code, cudaStream_t s);
 cudaError_t take_wgrad_status(int* code, cudaStream_t s);
 cudaError_t take_fp8_status(int* code, cudaStream_t s);
+// Makes one run out (moe_diag_products_wait).
+cudaError_t stall_rows(cudaStream_t s);
+cudaError_t stall_wgrad(cudaStream_t s);
+cudaError_t stall_fp8(cudaStream_t s);
 
 }  // namespace moe

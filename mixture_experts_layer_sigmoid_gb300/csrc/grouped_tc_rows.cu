@@ -84,5 +84,6 @@ cudaError_t launch_grouped_rows_tc(const GroupedRows& p, int num_sms, cudaStream
     return p.w_nk ? rows_tc<false>(p, num_sms, s) : rows_tc<true>(p, num_sms, s);
 }
 cudaError_t take_rows_status(int* code, cudaStream_t s) { return take_status(code, s); }
+cudaError_t stall_rows(cudaStream_t s) { return launch_stalled(s); }
 
 }  // namespace moe

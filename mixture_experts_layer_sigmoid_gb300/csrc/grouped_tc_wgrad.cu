@@ -27,5 +27,6 @@ cudaError_t launch_grouped_wgrad_tc(const GroupedWgrad& p, int num_sms, cudaStre
     return launch<true, true, SINGLE, true>(CUtensorMap{}, CUtensorMap{}, CUtensorMap{}, mO, a, units(BM), num_sms, s);
 }
 cudaError_t take_wgrad_status(int* code, cudaStream_t s) { return take_status(code, s); }
+cudaError_t stall_wgrad(cudaStream_t s) { return launch_stalled(s); }
 
 }  // namespace moe

@@ -14,7 +14,7 @@
 //     cycles a block).
 //   - setmaxnreg moves the loading warps' registers to the folding ones (128 sums, 64 columns
 //     in flight); loop bounds and addresses of the fold are made uniform by a shuffle, and its
-//     waits are bare (spin): each kept the compiler from copying sums in the loop.
+//     waits are bare (spin_tries): each kept the compiler from copying sums in the loop.
 #include "grouped_tc.cuh"
 
 namespace moe {
@@ -95,6 +95,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
     const uint32_t final_bar = bar0 + 8u * (2 * S + 4);
     uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem + SMEM8 - 1024 - 16);
     volatile int& abort_flag = *reinterpret_cast<volatile int*>(smem + SMEM8 - 1024 - 8);
+    const uint32_t flag = ring + SMEM8 - 1024 - 8;
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -172,7 +173,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
                     const uint32_t id = IDESC | ((uint32_t)(t.nt >> 3) << 17);
                     for (int kb = 0; kb < t.kblocks; ++kb, ++used) {
                         const int b = (int)(used & 1u);
-                        if (!spin(full_bar(s), ph) || !spin(pempty_bar(b), ((used >> 1) & 1u) ^ 1u)) { ok = false; break; }
+                        if (!spin(full_bar(s), ph, flag) || !spin(pempty_bar(b), ((used >> 1) & 1u) ^ 1u, flag)) { ok = false; break; }
                         ptx::tc_fence_after();
                         const uint32_t d = tmem + (uint32_t)(b * 256);
                         const uint32_t pa = ring + s * STAGE8, pb = pa + A8;
@@ -263,13 +264,13 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
 #pragma unroll 1
             for (int kb = 0; kb < t.kblocks; ++kb, ++it) {
                 const uint32_t off = (kb & 3) * 4;
-                if (off == 0) ok = ok && spin(scale_bar(slot), sph);
+                if (off == 0) ok = ok && spin_tries(scale_bar(slot), sph);
                 float sa, sb;
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sa) : "r"(slots + slot * kSlot + off + 16 * (q * 32 + lane)));
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sb) : "r"(slots + slot * kSlot + off + 2048 + 16 * h));
                 sa *= sb;
                 const uint32_t b = it & 1u;
-                ok = ok && spin(pfull_bar(b), (it >> 1) & 1u);
+                ok = ok && spin_tries(pfull_bar(b), (it >> 1) & 1u);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + b * 256 + h * 128;
@@ -386,5 +387,6 @@ cudaError_t launch_fp8_rows(const Fp8Rows& p, int num_sms, cudaStream_t s)
     return p.a.b_nk ? fp8_rows<__nv_bfloat16, false>(p, num_sms, s) : fp8_rows<__nv_bfloat16, true>(p, num_sms, s);
 }
 cudaError_t take_fp8_status(int* code, cudaStream_t s) { return take_status(code, s); }
+cudaError_t stall_fp8(cudaStream_t s) { return launch_stalled(s); }
 
 }  // namespace moe

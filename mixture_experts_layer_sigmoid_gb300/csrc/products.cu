@@ -239,3 +239,11 @@ moe_status_t moe_products_status(moe_stream_t stream)
         if (take(&code, s) != cudaSuccess) return MOE_ERR_CUDA;
     return code ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
+
+moe_status_t moe_diag_products_wait(int which, moe_stream_t stream)
+{
+    if (which < 0 || which > 2) return MOE_ERR_INVALID_ARG;
+    cudaError_t (*const stall[])(cudaStream_t) = {stall_rows, stall_wgrad, stall_fp8};
+    count_launches();
+    return done(stall[which](reinterpret_cast<cudaStream_t>(stream)));
+}
