@@ -79,6 +79,9 @@ struct Cfg {
     static_assert(BM * BK * 2 - STAGE <= kStaging, "inside the block's shared memory");
 };
 
+// Limit of the wait for a stage's loads once a pipeline has given up.
+constexpr uint64_t kDrainNs = 10000000;
+
 // Set by a wait that ran out (one word per translation unit and device).
 static __device__ DeviceStatus wait_status;
 
@@ -337,7 +340,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
         // ------------------------------------------------------- TMA loads
         if (elect_one()) {
             int s = 0;
-            uint32_t ph = 0;
+            uint32_t ph = 0, loaded = 0, fixed = 0, lands = 0;   // bits of stages
             bool ok = true;
             for (long long w = unit0; ok && w < work.total; w += nunits) {
                 const Tile t = work.at(a, table, w, rank);
@@ -349,10 +352,14 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                     const uint32_t dst_a = ring + s * C::STAGE, dst_b = dst_a + C::A_BYTES;
                     const bool fix = WGRAD && kb == t.kblocks - 1 && t.tail < BK;
                     uint32_t bar;
+                    loaded |= 1u << s;
                     if (fix) {
                         bar = land_bar(s);
                         ptx::mbar_arrive_expect_tx(bar, bytes);
+                        fixed |= 1u << s;
+                        lands ^= 1u << s;
                     } else {
+                        if (WGRAD) fixed &= ~(1u << s);
                         bar = PAIR ? ptx::mapa_shared(full_bar(s), 0) : full_bar(s);
                         if (rank == 0) {
                             ptx::mbar_arrive_expect_tx(full_bar(s), (PAIR ? 2 : 1) * bytes);
@@ -376,6 +383,20 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
+            // what is on its way into the ring lands before the block ends, with a limit of its own once
+            // the pipeline has given up. (The even CTA waits for both; loads of the odd one that it never
+            // counted get a millisecond.)
+            volatile int never = 0;
+            auto land = [&](uint32_t bar, uint32_t parity) {
+                ok = ok && wait(bar, parity, 9);
+                if (!ok) ptx::wait_bounded(bar, parity, &never, status, 9, kDrainNs);
+            };
+            for (int i = 0; i < S; ++i) {
+                if (!(loaded >> i & 1u)) continue;
+                if (fixed >> i & 1u) land(land_bar(i), (lands >> i & 1u) ^ 1u);
+                else if (rank == 0) land(full_bar(i), i < s ? ph : ph ^ 1u);
+            }
+            if (PAIR && !ok && rank != 0) ptx::wait_bounded(full_bar(0), 0, &never, status, 9, kDrainNs / 10);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -140,7 +140,7 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
             // --------------------------------------------------- TMA loads
             if (elect_one()) {
                 int s = 0;
-                uint32_t ph = 0;
+                uint32_t ph = 0, loaded = 0;           // bits of stages
                 bool ok = true;
                 for (long long w = blockIdx.x; ok && w < work.total; w += gridDim.x) {
                     const Tile t = work.at(a, table, w, 0);
@@ -157,8 +157,18 @@ fp8_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUten
                         } else {
                             load_3d<false>(dst_b, &mB, bar, kb * QK, t.n0, t.e);
                         }
+                        loaded |= 1u << s;
                         if (++s == S) { s = 0; ph ^= 1u; }
                     }
+                }
+                // what is on its way into the ring lands before the block ends, with a limit of its own
+                // once the pipeline has given up
+                volatile int never = 0;
+                for (int i = 0; i < S; ++i) {
+                    if (!(loaded >> i & 1u)) continue;
+                    const uint32_t parity = i < s ? ph : ph ^ 1u;
+                    ok = ok && wait(full_bar(i), parity, 27);
+                    if (!ok) ptx::wait_bounded(full_bar(i), parity, &never, status, 27, kDrainNs);
                 }
             }
             __syncwarp();
