@@ -16,8 +16,7 @@
 // on the device. Tiles of 128 need half of the reads of shared memory; tiles of 64 are taken
 // while the larger ones are fewer than four for each SM.
 #include "grouped.cuh"
-
-#include <atomic>
+#include "per_device.h"
 
 namespace moe {
 namespace {
@@ -210,17 +209,17 @@ grouped_wgrad_kernel(const GroupedWgrad p, const Vec vec)
 
 // A persistent launch; the kernel's shared memory is set up on the first call of a device.
 template <typename P>
-cudaError_t launch(void (*k)(const P, const Vec), const P& p, const Vec& vec, int smem, std::atomic<bool> (&ready)[64],
+cudaError_t launch(void (*k)(const P, const Vec), const P& p, const Vec& vec, int smem, std::atomic<int> (&ready)[kMaxDevices],
                    long long tiles, int most, cudaStream_t s)
 {
-    int dev = 0;
+    int dev = 0, set = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) ready[dev].store(true, std::memory_order_release);
-    }
+    e = per_device<cudaError_t>(ready, dev, [&](int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    }, &set);
+    if (e != cudaSuccess) return e;
     k<<<(unsigned)(tiles < most ? (tiles > 0 ? tiles : 1) : most), kThreads, smem, s>>>(p, vec);
     return cudaGetLastError();
 }
@@ -228,7 +227,7 @@ cudaError_t launch(void (*k)(const P, const Vec), const P& p, const Vec& vec, in
 template <int TM, int TT, bool W_NK>
 cudaError_t rows_simt(const GroupedRows& p, int num_sms, cudaStream_t s)
 {
-    static std::atomic<bool> ready[64];
+    static std::atomic<int> ready[kMaxDevices];
     constexpr int smem = kStages<TM> * stage_values<Operand<TM, true>, Operand<TT, W_NK>>() * 4 + (int)sizeof(SegmentTable);
     const long long tiles = row_tiles_bound(p.g.rows, p.g.E, TM) * ((p.N + TT - 1) / TT);
     return launch(grouped_rows_kernel<TM, TT, W_NK>, p, Vec{vectors(p.X, p.ldx, 0), vectors(p.W, p.ldw, p.sw)}, smem, ready,
@@ -237,7 +236,7 @@ cudaError_t rows_simt(const GroupedRows& p, int num_sms, cudaStream_t s)
 template <int TT>
 cudaError_t wgrad_simt(const GroupedWgrad& p, int num_sms, cudaStream_t s)
 {
-    static std::atomic<bool> ready[64];
+    static std::atomic<int> ready[kMaxDevices];
     constexpr int smem = kStages<TT> * stage_values<Operand<TT, false>, Operand<TT, false>>() * 4;
     const long long tiles = (long long)p.g.E * ((p.M + TT - 1) / TT) * ((p.N + TT - 1) / TT);
     return launch(grouped_wgrad_kernel<TT>, p, Vec{vectors(p.A, p.lda, 0), vectors(p.B, p.ldb, 0)}, smem, ready, tiles,

@@ -32,11 +32,11 @@
 //     second window as the neighbour's by a shuffle 78).
 #pragma once
 #include "grouped.cuh"
+#include "per_device.h"
 #include "ptx.cuh"
 
 #include <atomic>
 #include <cudaTypedefs.h>
-#include <mutex>
 
 namespace moe {
 namespace gtc {
@@ -654,38 +654,38 @@ bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, lo
               long long stride, int box_rows, int bytes = 2, int width = 128);
 
 // The units that run at once of a kernel with this much shared memory, set up on the first
-// call of each device (slots: one per kernel, zeros).
-inline cudaError_t units_at_once(const void* k, int threads, int smem, bool pair, int num_sms, std::atomic<int> (&slots)[64],
-                                 int* out)
+// call of each device (slots: one per kernel, zeros). `regs`: the least registers a thread that the
+// kernel may have been built with.
+inline cudaError_t units_at_once(const void* k, int threads, int smem, bool pair, int num_sms, std::atomic<int> (&slots)[kMaxDevices],
+                                 int* out, int regs = 0)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int n = dev < 64 ? slots[dev].load(std::memory_order_acquire) : 0;
-    if (n == 0) {
+    return per_device<cudaError_t>(slots, dev, [&](int* n) {
+        cudaFuncAttributes built{};
+        cudaError_t e = regs ? cudaFuncGetAttributes(&built, k) : cudaSuccess;
+        if (e != cudaSuccess) return e;
+        if (built.numRegs < regs) return cudaErrorInvalidKernelImage;
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        n = num_sms;
-        if (pair) {
-            cudaLaunchConfig_t cfg{};
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = 2;
-            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-            cfg.gridDim = dim3(2);
-            cfg.blockDim = dim3((unsigned)threads);
-            cfg.dynamicSmemBytes = (size_t)smem;
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            int most = 0;
-            e = cudaOccupancyMaxActiveClusters(&most, k, &cfg);
-            if (e != cudaSuccess) return e;
-            n = most > 0 ? most : 1;
-        }
-        if (dev < 64) slots[dev].store(n, std::memory_order_release);
-    }
-    *out = n;
-    return cudaSuccess;
+        *n = num_sms;
+        if (!pair) return cudaSuccess;
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int most = 0;
+        e = cudaOccupancyMaxActiveClusters(&most, k, &cfg);
+        *n = most > 0 ? most : 1;
+        return e;
+    }, out);
 }
 // Waits for the stream and takes this translation unit's word.
 static inline cudaError_t take_status(int* code, cudaStream_t s)
@@ -751,7 +751,7 @@ cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorM
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
-    static std::atomic<int> slots[64];
+    static std::atomic<int> slots[kMaxDevices];
     int n = 0;
     const cudaError_t e = units_at_once(reinterpret_cast<const void*>(k), threads<WGRAD, GUARD>(), C::SMEM, PAIR, num_sms, slots, &n);
     if (e != cudaSuccess) return e;

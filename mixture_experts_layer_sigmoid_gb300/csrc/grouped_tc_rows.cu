@@ -8,15 +8,15 @@ namespace gtc {
 bool make_map(CUtensorMap* m, const void* p, long long inner, long long rows, long long mats, long long ld,
               long long stride, int box_rows, int bytes, int width)
 {
-    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 encode = found.load(std::memory_order_acquire);
+    if (!encode) {                                     // (not found is asked again)
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    });
+            found.store(encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn), std::memory_order_release);
+    }
     if (!encode || (reinterpret_cast<uintptr_t>(p) & 15u) || ld * bytes % 16 || (mats > 1 && stride * bytes % 16)) return false;
     if (mats == 1) stride = ld * rows;
     if (stride * bytes >= (1ll << 40) || ld * bytes >= (1ll << 40)) return false;

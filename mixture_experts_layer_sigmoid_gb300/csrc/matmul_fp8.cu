@@ -374,16 +374,10 @@ cudaError_t fp8_rows(const Fp8Rows& in, int num_sms, cudaStream_t s)
                : make_map(&mB, f.B, in.K, in.N, in.g.E, f.ldb, f.sb, BN, 1)))
         return cudaErrorInvalidValue;
     auto k = fp8_kernel<T, B_MN>;
-    static std::atomic<int> slots[64];
+    static std::atomic<int> slots[kMaxDevices];
     int n = 0;
-    // a build with fewer registers would leave setmaxnreg waiting
-    static const cudaError_t registers = [k] {
-        cudaFuncAttributes at{};
-        const cudaError_t e = cudaFuncGetAttributes(&at, k);
-        return e != cudaSuccess || at.numRegs >= kRegs ? e : cudaErrorInvalidKernelImage;
-    }();
-    if (registers != cudaSuccess) return registers;
-    const cudaError_t e = units_at_once(reinterpret_cast<const void*>(k), kThreads8, SMEM8, false, num_sms, slots, &n);
+    // (a build with fewer registers would leave setmaxnreg waiting)
+    const cudaError_t e = units_at_once(reinterpret_cast<const void*>(k), kThreads8, SMEM8, false, num_sms, slots, &n, kRegs);
     if (e != cudaSuccess) return e;
     k<<<(unsigned)(units < n ? units : n), kThreads8, SMEM8, s>>>(mA, mB, p);
     return cudaGetLastError();
