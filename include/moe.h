@@ -598,7 +598,8 @@ typedef struct {
 
 /* Y[r] = X[r] W_e for the rows r of each segment e; X rows x K, Y rows x N, of
  * type groups->dtype (products of bf16 values are exact and summed in fp32 on
- * the tensor cores; fp32 values use fp32 FMAs), rounded once.
+ * the tensor cores; fp32 values use fp32 FMAs, in pieces of 256 terms that are
+ * added up), rounded once.
  * W_e[k][n] stands at W + e sw + k ldw + n, or with w_nk at W + e sw + n ldw + k
  * (weights stored out x in). The gradient of X is the same call on dY with the
  * other w_nk and K and N exchanged.
