@@ -101,14 +101,14 @@ __device__ __forceinline__ bool elect_one()
 // after its first look at the clock; the caller raises the flag and records it. The looks come
 // between rounds of tries, and their outcome is voted on: a branch on it that the compiler cannot
 // prove uniform would take the MMAs behind it off the uniform datapath (four decoded tokens 97
-// instead of 62 us).
-template <uint64_t LIMIT_NS = kWaitLimitNs>
+// instead of 62 us). CLUSTER: the peer's fixing warp may be the last to arrive.
+template <uint64_t LIMIT_NS = kWaitLimitNs, bool CLUSTER = false>
 __device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, uint32_t abort_flag)
 {
     uint64_t t0 = 0;
     for (;;) {
         for (int i = 0; i < 64; ++i)
-            if (ptx::mbar_try_wait(bar, parity)) return true;
+            if (CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
         uint32_t raised;
         asm volatile("ld.volatile.shared::cta.u32 %0, [%1];" : "=r"(raised) : "r"(abort_flag) : "memory");
         const uint64_t t = ptx::globaltimer();
@@ -413,7 +413,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                 // (256 rows less 128 in the M / 16 field)
                 const uint32_t id = (IDESC | ((uint32_t)(t.nt >> 3) << 17)) - (t.half ? 8u << 24 : 0u);
                 for (int kb = 0; kb < t.kblocks; ++kb) {
-                    if (!spin(full_bar(s), ph, flag)) { ok = false; break; }
+                    if (!spin<kWaitLimitNs, WGRAD && PAIR>(full_bar(s), ph, flag)) { ok = false; break; }
                     ptx::tc_fence_after();
                     const uint32_t pa = ring + s * C::STAGE, pb = pa + C::A_BYTES;
                     const int steps = WGRAD && kb == t.kblocks - 1 ? (t.tail + 15) / 16 : BK / 16;

@@ -59,6 +59,23 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// The same where the phase may end with an arrival from the other CTA of a pair whose writes (to its
+// own shared memory) the caller's next step reads.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Wait until the phase with parity `parity` of `bar` has completed. Gives up
 // when another role of the CTA has aborted, or after limit_ns; on a
 // timeout it records MOE_ERR_DEVICE_TIMEOUT and raises the CTA's abort flag.
