@@ -474,7 +474,7 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                                (WGRAD ? t.e * a.so + (long long)(t.m0 + r0) * a.ldo
                                       : (long long)(t.row + r0) * a.ldo);
             const int cols = __shfl_sync(0xffffffffu, min(a.N - t.n0 - c0, t.half ? t.nt / 2 : t.nt), 0);
-            const bool whole = a.vec && (WGRAD || rows >= 32), last = t.n0 + c0 + cols == a.N;
+            const bool whole = a.vec && (WGRAD || rows >= 32), last = t.n0 + c0 + cols == a.N && a.N % 8 == 0;
 #pragma unroll 1
             for (int u = 0; u * 32 < cols && rows > 0; ++u) {
                 uint32_t v[32];
@@ -487,7 +487,8 @@ kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorM
                     for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
                 // 32 rows of 64 bytes, swizzled over them, in turns with the other half's store; TMA
-                // leaves out what lies past the tensor (not past this warp's columns)
+                // leaves out what lies past the tensor (not past this warp's columns), in columns by
+                // whole 16 bytes: a row that ends inside them would have zeros behind it
                 const int left = cols - u * 32;
                 const bool by_tma = __shfl_sync(0xffffffffu, (int)(whole && (left >= 32 || last)), 0) != 0;
                 const uint32_t buf = stg + (uint32_t)(stores & 1) * 2048u;
