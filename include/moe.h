@@ -625,10 +625,13 @@ moe_status_t moe_grouped_wgrad(const moe_groups_t* groups, int M, int N, const v
  * with MOE_Q_TILES over the E K x N weights), K a multiple of 128, N any:
  *   Y[r][n] = sum_kb SA[r][kb] SB_e[kb][n/128] sum_{k in block kb} A[r][k] B_e[k][n],
  * code products and their sums of 128 in fp32 on the tensor cores, the scaled sums in
- * fp32 FMAs in ascending kb, rounded once to groups->dtype.
+ * fp32 FMAs in ascending kb, rounded once to groups->dtype. SA SB is formed first, in fp32:
+ * it is infinite above 2^128 and loses bits below 2^-126, whatever the sum beside it is.
  * B_e[k][n] at B + e sb + k ldb + n with SB_e[kb][nb] at SB + e ssb + kb ldsb + nb, or
  * with b_nk B + e sb + n ldb + k and SB + e ssb + nb ldsb + kb (the transpose's view of
- * the same codes: the gradient of A's rows takes the codes of dY and this view).
+ * the same codes: the gradient of A's rows takes the codes of dY and this view). A dense
+ * weight gradient over a multiple of 128 tokens is A = X's codes along the tokens
+ * (MOE_Q_COLS_T) times B = dY's tile codes.
  * Errors: as moe_grouped_matmul, and INVALID_ARG for K not a multiple of 128,
  * MISALIGNED for lda, ldb or sb not multiples of 16. */
 typedef struct {

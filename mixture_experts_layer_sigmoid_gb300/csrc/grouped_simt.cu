@@ -266,8 +266,8 @@ cudaError_t wgrad_simt(const GroupedWgrad& p, int num_sms, cudaStream_t s)
     return launch(grouped_wgrad_kernel<TT>, p, Vec{vectors(p.A, p.lda, 0), vectors(p.B, p.ldb, 0)}, smem, ready, tiles,
                   num_sms * (TT == 128 ? 1 : 2), s);
 }
-// Rows an expert has on average below which a tile has 16 of them (one row of 8192 x 8192:
-// 289 us with 64).
+// Rows of the buffers (padding included) for each expert below which a tile has 16 of them (one
+// row of 8192 x 8192: 289 us with 64).
 constexpr long long kFewRows = 32;
 // Whether tiles of 128 x 128 are at least four for each SM.
 bool large_tiles(long long by_m, int n, int num_sms) { return by_m * ((n + 127) / 128) >= 4ll * num_sms; }

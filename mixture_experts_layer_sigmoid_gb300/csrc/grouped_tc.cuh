@@ -23,7 +23,7 @@
 //     others (perhaps NaN). That block's loads complete on a barrier of their own; a fixing
 //     warp zeroes the rows up to the next multiple of 16 in both operands and then signals
 //     the block; the MMAs stop at that multiple.
-//   - FEW: tiles of 32 rows by 64 columns for experts of few rows, whose weights are all there is
+//   - FEW: tiles of 32 rows by 64 columns for buffers of few rows an expert, whose weights are all there is
 //     to read: 16 stages of 8 KB of them in flight, and enough tiles for every SM. (The MMAs
 //     still take 128 rows, 250 cycles a block, less than HBM takes to bring it.)
 //   - GUARD: operands that TMA cannot take (strides off the 16-byte boundaries) are loaded by

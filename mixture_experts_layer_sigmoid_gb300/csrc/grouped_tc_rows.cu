@@ -34,8 +34,10 @@ using namespace gtc;
 
 namespace {
 
-// Rows an expert has on average from which tiles go to CTA pairs (64 experts of 256 rows,
-// 7168 x 2048, the gradient of the rows: 451 us as single CTAs, 414 as pairs).
+// Rows of the buffers for each expert from which tiles go to CTA pairs (64 experts of 256 rows,
+// 7168 x 2048, the gradient of the rows: 451 us as single CTAs, 414 as pairs). The host knows the
+// buffers' rows, padding and room included, and not the routing: a batch of few rows in segments
+// padded to 128 of them counts as one of 128-row experts.
 constexpr long long kPairRows = 128;
 
 // ... and below which they are tiles of few rows.
