@@ -665,9 +665,10 @@ moe_status_t moe_products_status(moe_stream_t stream);
 
 /* Failure-detection check of the products, as moe_diag_wait_timeout is the layer's: runs the
  * waits of their kernels on an mbarrier that is never signalled: one with a limit of 10 ms, one
- * with the usual limit that the first one's abort flag ends, and one of 4000 tries. which: the row products' status word
- * (0), the weight gradients' (1) or the 8-bit products' (2). moe_products_status then returns
- * MOE_ERR_DEVICE_TIMEOUT once, and the device stays usable. Errors: INVALID_ARG, CUDA. */
+ * with the usual limit that the first one's abort flag ends, and one of 4000 tries. which: the
+ * row products' status word (0), the weight gradients' (1) or the 8-bit products' (2).
+ * moe_products_status then returns MOE_ERR_DEVICE_TIMEOUT once, and the device stays usable.
+ * Errors: INVALID_ARG, CUDA. */
 moe_status_t moe_diag_products_wait(int which, moe_stream_t stream);
 
 /* MOE_ABI_VERSION of the loaded library. */

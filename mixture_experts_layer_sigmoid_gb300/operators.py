@@ -369,7 +369,9 @@ def grouped_matmul(rows, w, index, out=None):
     x N) contiguous in either of its last two dimensions (weights stored out x
     in are passed as their transposed view), ``index`` the sort's or a layer's
     ``offsets`` and, where there is padding, ``counts``. Padding rows come out as
-    zeros; rows behind the last segment are neither read nor written."""
+    zeros; rows behind the last segment are neither read nor written. Each tensor
+    starts on a 16-byte boundary (a slice that does not is refused); its strides
+    are free."""
     lib = _load()
     ldx = _act(rows, "rows")
     R, K = rows.shape
@@ -444,7 +446,8 @@ def fp8_matmul(codes, scales, w_codes, w_scales, index=None, *, dtype=None, out=
     the contiguous one, the same in both tensors: the transposed views of codes
     and scales give the product with the transposed weights. ``dtype`` (default
     bf16) or ``out`` says fp32 or bf16; padding rows and rows behind the last
-    segment as in grouped_matmul."""
+    segment as in grouped_matmul. Each tensor starts on a 16-byte boundary, and so
+    does every row of codes (in either tensor)."""
     lib = _load()
     t = _torch
     if codes.dim() != 2 or codes.dtype != t.uint8 or not codes.is_cuda:
